@@ -42,6 +42,12 @@ _SIGS = {
     "tq_gemv_f32_scratch": ([_i32, _p, _i64, _i64, _p, _p, _p], _i32),
     "tq_gemm": ([_i32, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p], _i32),
     "tq_group_dots": ([_i32, _p, _i64, _i64, _i64, _p, _p, _p, _p], _i32),
+    # the argument structs of these are passed as packed bytes (seq.py)
+    "tq_rope_append": ([ctypes.c_char_p, _p], _i32),
+    "tq_paged_attn_workspace_bytes": ([_i64, _i64, _i32, _i32, _i32], _i64),
+    "tq_paged_attn": ([ctypes.c_char_p, _p], _i32),
+    "tq_gdn_workspace_bytes": ([_i64, _i64, _i64, _i32, _i32, _i32], _i64),
+    "tq_gdn": ([ctypes.c_char_p, _p], _i32),
     "tq_status_str": ([_i32], ctypes.c_char_p),
     "tq_last_hip_error": ([], _i32),
     "tq_version": ([], _i32),
@@ -340,3 +346,7 @@ class TernaryMatrix:
         """fp32 activations [tokens, cols] -> fp32 [tokens, rows] (quantize, then product)."""
         q, d, bs = quantize_q8k(x)
         return self.matmul(q, d, bs)
+
+
+from .seq import (attn_workspace, attn_workspace_bytes, gdn, gdn_workspace, gdn_workspace_bytes, kv_cache,  # noqa: E402
+                  paged_attn, rope_append, rope_frequencies)

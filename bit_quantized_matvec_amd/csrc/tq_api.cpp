@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/tq.h"
+#include "api_status.h"
 #include "kernels.h"
 
 namespace {
@@ -29,12 +30,6 @@ int shape_status(int f, int64_t rows, int64_t cols, int64_t tokens) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return TQ_OK;
-  g_last_hip_error = (int)e;
-  return TQ_ERR_HIP;
-}
-
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // Shared checks of the product entry points.
@@ -50,6 +45,14 @@ int product_args(int fmt, const void* w, int64_t rows, int64_t cols, int64_t tok
 }
 
 }  // namespace
+
+int tq::hip_status(hipError_t e) {
+  if (e == hipSuccess) return TQ_OK;
+  g_last_hip_error = (int)e;
+  return TQ_ERR_HIP;
+}
+
+using tq::hip_status;
 
 extern "C" {
 
@@ -218,9 +221,9 @@ const char* tq_status_str(int status) {
   switch (status) {
     case TQ_OK: return "ok";
     case TQ_ERR_NULL: return "a required pointer is NULL";
-    case TQ_ERR_SHAPE: return "unsupported shape (rows >= 1, cols a multiple of 256, tokens >= 1, size limits)";
-    case TQ_ERR_ALIGN: return "misaligned pointer (weights and q: 16 bytes; x, d, y, idots: 4; bsums: 2)";
-    case TQ_ERR_FORMAT: return "unknown weight format";
+    case TQ_ERR_SHAPE: return "unsupported shape (products: rows >= 1, cols a multiple of 256, tokens >= 1; the entry point's limits in tq.h)";
+    case TQ_ERR_ALIGN: return "misaligned pointer or stride (products: weights and q 16 bytes; x, d, y, idots 4; bsums 2; strided inputs: 16)";
+    case TQ_ERR_FORMAT: return "unknown weight format, or element type or layout that the operation does not take";
     case TQ_ERR_UNSUPPORTED: return "operation not provided for this format";
     case TQ_ERR_HIP: return "HIP runtime error (see tq_last_hip_error)";
     default: return "unknown status";

@@ -226,6 +226,138 @@ int tq_gemm(int fmt, const void *w, int64_t rows, int64_t cols, int64_t tokens, 
 int tq_group_dots(int fmt, const void *w, int64_t rows, int64_t cols, int64_t tokens, const int8_t *q,
                   const int16_t *bsums, int32_t *idots, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The operators between a block's projections: rotary append, paged attention,
+ * gated delta rule.  Conventions as above, and:
+ *
+ *   - Index tensors are device memory, so their values cannot be checked on
+ *     the host: the kernels check every page, slot and offset before they use
+ *     it, skip what is out of range and, if `bad_flag` (nullable, device
+ *     int32) is given, store 1 into it (the caller clears it beforehand).
+ *   - Strides are in elements; the last dimension is contiguous.  Tensors read
+ *     with strides need 16-byte aligned pointers and strides that are a
+ *     multiple of 16 bytes.
+ *   - tokens and seqs may be zero: nothing is launched then (tq_gdn with
+ *     seqs > 0 and no tokens copies the states).
+ *   - A field that a struct documents as nullable may be NULL, others not.
+ *
+ * Sequences: `seqs` sequences share the token axis.  Sequence b has the tokens
+ * cu[b] .. cu[b + 1] - 1 (int32 [seqs + 1], cu[0] = 0, cu[seqs] = tokens, not
+ * decreasing; a sequence may be empty).  cu = NULL means one token each
+ * (tokens == seqs).  `max_len` is the longest sequence's token count if the
+ * caller knows it, 0 if not: it chooses between kernels and limits nothing.
+ *
+ * Paged cache: K [pages][kv_heads][page][dim], V [pages][kv_heads][dim][page]
+ * (transposed inside a page, so that the product with the probabilities reads
+ * consecutive keys of one column as it lies), bf16 or fp16; page = tokens of a
+ * page, a power of two from 16 to 256.  Token slot s is place s % page of page
+ * s / page.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_type;
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_layout;
+
+/* Per-head RMS norm of q and k, rotary positions, and the append of k and v to
+ * the paged cache, in one launch.  For each token t and head:
+ *   n = x * (mean(x^2) + eps)^-1/2 * w     (q_norm / k_norm given, else n = x)
+ *   a_i = positions[t] * inv_freq[i], c_i = rope_scale cos a_i, s_i likewise
+ *   half:         y_i  = n_i c_i - n_{i+rot/2} s_i,  y_{i+rot/2} = n_{i+rot/2} c_i + n_i s_i
+ *   interleaved:  y_2i = n_2i c_i - n_{2i+1} s_i,    y_{2i+1}    = n_{2i+1} c_i + n_2i s_i
+ * for i < rot/2; values from rot on are n unchanged.  The angle is formed and
+ * reduced in fp64, the rest is fp32, rounded once to the cache's type.
+ * slots[t] < 0: a padding token, its q_out is written and nothing is stored.
+ * slots[t] >= pages * page: not stored, bad_flag.  Two tokens with one slot
+ * race.  dim 64, 128 or 256; rot 0 (no rotation, inv_freq and positions may be
+ * NULL) or a multiple of 16 up to dim. */
+typedef struct {
+    const void *q, *k, *v; /* [tokens][heads | kv_heads][dim], in_type */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+    const int32_t *positions; /* [tokens] */
+    const int64_t *slots;     /* [tokens] */
+    const double *inv_freq;   /* [rot / 2] */
+    const float *q_norm, *k_norm; /* [dim], nullable */
+    void *q_out;              /* [tokens][heads][dim] contiguous, cache_type */
+    void *k_cache, *v_cache;
+    int32_t *bad_flag;
+    int64_t tokens, pages;
+    int32_t heads, kv_heads, dim, rot, page, in_type, cache_type, layout;
+    float eps, rope_scale;
+} tq_rope_append_args;
+
+int tq_rope_append(const tq_rope_append_args *args, void *stream);
+
+/* Attention of new tokens over a paged cache that already holds their keys and
+ * values.  Sequence b has kv_len[b] keys; token i of its n new ones sits at
+ * position p = kv_len[b] - n + i and sees keys j <= p, and j > p - window if
+ * window > 0:
+ *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j).
+ * A token that sees no key (p < 0) gives out = 0 and lse = -inf.  What lies in
+ * the cache at keys that no token of the sequence sees is not used, whatever
+ * it holds, and table entries of pages that no token sees are not read.
+ * block_table[b][j / page] is the page of key j.  A page outside [0, pages)
+ * counts as keys that nobody sees, with bad_flag; so does kv_len[b] beyond
+ * the table.  Query head h reads key head h / (heads / kv_heads).
+ * Products are exact, sums and statistics fp32.  out in the cache's type: the
+ * probabilities are rounded to that type before the product with V, which is
+ * what the output's own rounding amounts to; out fp32: they are split into
+ * two (fp16) or three (bf16) terms that hold 22 or 24 bits.
+ * workspace (nullable): tq_paged_attn_workspace_bytes, zeroed before its first
+ * use and left with its counters at zero by every call; without it no
+ * sequence's keys are split over workgroups. */
+typedef struct {
+    const void *q; /* [tokens][heads][dim], cache_type */
+    int64_t q_token, q_head;
+    const void *k_cache, *v_cache;
+    const int32_t *block_table; /* [seqs][table_width], rows table_stride apart */
+    const int32_t *kv_len;      /* [seqs] */
+    const int32_t *cu;          /* [seqs + 1], nullable */
+    void *out;                  /* [tokens][heads][dim] contiguous, out_type */
+    float *lse;                 /* [tokens][heads], nullable */
+    void *workspace;
+    int32_t *bad_flag;
+    int64_t table_width, table_stride, tokens, seqs, pages, max_len, workspace_bytes;
+    int32_t heads, kv_heads, dim, page, cache_type, out_type, window;
+    float scale;
+} tq_paged_attn_args;
+
+/* Bytes for any window, table and lengths of this many tokens and sequences;
+ * 0 for sizes that tq_paged_attn refuses. */
+int64_t tq_paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim);
+int tq_paged_attn(const tq_paged_attn_args *args, void *stream);
+
+/* The gated delta rule.  Per value head (key head = value head / (v_heads /
+ * k_heads)) with state S [dk][dv], for each token of a sequence in order:
+ *   S <- exp(g) S;   S <- S + k (x) beta (v - S^T k);   out = scale S^T q.
+ * l2norm != 0: q and k are first divided by sqrt(sum(x^2) + eps).  g <= 0
+ * (-inf clears the state).  Sequence b starts from state[slots[b]] and leaves
+ * its last state in state_out[slots[b]] (slots NULL: b).  slots[b] < 0 starts
+ * from zeros and stores nothing; slots[b] >= states does that too, with
+ * bad_flag.  Two sequences with one slot race.  state_out may be state.  An
+ * empty sequence copies its state.  All arithmetic and the states are fp32,
+ * running sums of g fp64.  dk 64 or 128, dv a multiple of 32 up to 256.
+ * workspace: nullable; with tq_gdn_workspace_bytes of scratch (needs no
+ * clearing), long sequences are computed in chunks on the matrix units. */
+typedef struct {
+    const void *q, *k, *v; /* [tokens][k_heads | k_heads | v_heads][dk | dk | dv], in_type */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+    const float *g, *beta;  /* [tokens][v_heads] contiguous */
+    const float *state;     /* [states][v_heads][dk][dv] contiguous */
+    float *state_out;
+    const int32_t *slots;   /* [seqs], nullable */
+    const int32_t *cu;      /* [seqs + 1], nullable */
+    void *out;              /* [tokens][v_heads][dv] contiguous, out_type */
+    void *workspace;
+    int32_t *bad_flag;
+    int64_t tokens, seqs, states, max_len, workspace_bytes;
+    int32_t k_heads, v_heads, dk, dv, in_type, out_type, l2norm;
+    float scale, eps;
+} tq_gdn_args;
+
+/* Bytes for these sizes (0 if no call with them uses a workspace, or for sizes
+ * that tq_gdn refuses). */
+int64_t tq_gdn_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int32_t v_heads, int32_t dk, int32_t dv);
+int tq_gdn(const tq_gdn_args *args, void *stream);
+
 /* Static description of a status code. */
 const char *tq_status_str(int status);
 
