@@ -1,72 +1,569 @@
-// k_paged_attn.hip -- attention of new tokens over a paged cache: one wave per
-// (token, query head), a key at a time with a running maximum and sum.
+// k_paged_attn.hip -- attention of new tokens over a paged cache.
+//
+// Mathematics.  For one key head the query rows are (token, head of the group)
+// pairs; their scores S = scale Q K^T and outputs O = softmax(S) V are taken in
+// one pass over the keys with a running maximum m and sum l per row (base 2:
+// p = 2^(s - m), s scaled by scale log2 e), so S never leaves registers.
+//
+// Operands.  Both products are computed transposed, S^T = K Q^T and
+// O^T = V^T P^T: a column of a matrix-instruction tile is a query row, so a
+// row's m, l and rescaling belong to a lane.  The key a lane finds in its
+// S^T registers depends on which K row was fed as which A row, and that
+// is free to choose: rows are fed in the order that leaves lane group g with
+// the consecutive keys 8g .. 8g + 7, which is the layout the B operand of the
+// second product wants.  So P goes from the first product to the second
+// without a lane exchange, and V^T (stored transposed) is read 16 bytes = 8
+// consecutive keys at a time.
+//
+// Rounding.  Q, K, V enter as they are; products are exact and summed in
+// fp32.  P enters the second product in the cache's type when the output has
+// that type, and as 2 (fp16) or 3 (bf16) terms whose sum holds 22 or 24 bits
+// when the output is fp32.  fp16 P is scaled by 2^15 (removed by the division
+// by l, which carries it too), so that small probabilities stay normal.
+//
+// Unseen keys.  Their scores become -inf; their V values are made zero where
+// no row of the workgroup sees them, as 0 * NaN would spoil a sum.  A value
+// that is not finite and that some rows see spoils the others too, and an
+// infinity times a term of P that is zero or negative becomes NaN: a result
+// with a NaN is therefore computed a second time with pv_each(), which takes
+// finite values as before and counts infinities and NaN per (row, column) with
+// the 0/1 visibility in the place of P.  Finite caches never come there.
+//
+// Two kernels:
+//
+//   attn_rows    16 query rows per workgroup, 4 waves that each take every
+//                fourth block of 32 keys straight from memory to registers; no
+//                LDS before the waves are joined.  For few rows (single
+//                tokens): bound by the cache's bytes.
+//   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles
+//                staged in LDS, double-buffered, shared by the 4 waves.  Bound
+//                by the matrix units and the exponentials beside them.
+//
+// Few workgroups: the keys of a tile are split over several, whose partial
+// (m, l, O) go to the workspace.  The last to arrive of each 16 joins them, the
+// last of those joins the joined ones (a tree of two levels, up to 256 parts).
+#include <algorithm>
+
+#include "kernels.h"
 #include "seq.h"
 
 namespace tq {
 namespace {
 
-template <typename C, typename O, int D>
-__global__ __launch_bounds__(64) void attn_simple_kernel(tq_paged_attn_args a, int page_shift) {
-  constexpr int E = D / 64;
-  const int64_t row = blockIdx.x;
-  const int64_t t = row / a.heads;
-  const int h = (int)(row % a.heads), kvh = h / (a.heads / a.kv_heads), lane = threadIdx.x;
-  int64_t b = 0;
-  SeqRange r{0, 0};
-  for (; b < a.seqs; ++b) {
-    r = seq_range(a.cu, b, a.tokens, a.bad_flag);
-    if (t >= r.t0 && t < r.t0 + r.n) break;
-  }
-  if (b == a.seqs) return;
-  const int64_t len = min((int64_t)max(a.kv_len[b], 0), a.table_width << page_shift);
-  if (len != a.kv_len[b]) raise_flag(a.bad_flag);
-  const int64_t pos = len - r.n + (t - r.t0);
-  const C* q = static_cast<const C*>(a.q) + t * a.q_token + h * a.q_head + lane * E;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kRowsTile = 16;    // query rows of an attn_rows workgroup
+constexpr int kChunkTile = 128;  // query rows of an attn_chunk workgroup
+constexpr int kBlock = 32;       // keys per step of an attn_rows wave
+constexpr int kFan = 16;         // parts joined at once
+constexpr int kMaxSplits = kFan * kFan;
+constexpr int kMaxParts = 512;   // parts of all tiles together
+constexpr int kCounters = kFan + 1;
+constexpr int64_t kHeader = (int64_t)kMaxParts * kCounters * 4;  // the counters, before the parts
+static_assert(kHeader % 256 == 0, "");
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct AttnParams {
+  tq_paged_attn_args a;
+  float scale2;  // scale * log2 e
+  int group, page_shift, splits, slots;
+};
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename C>
+struct Half;
+template <>
+struct Half<bf16> {
+  typedef bf16 frag __attribute__((ext_vector_type(8)));
+  static constexpr unsigned kExp = 0x7F807F80u;  // exponent bits of both halves of a dword
+  static constexpr unsigned short kOne = 0x3F80;
+  static constexpr float kShift = 0.f;
+  static constexpr int kTerms = 3;
+  static __device__ f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+  static __device__ f32x16 mma(frag a, frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+};
+template <>
+struct Half<f16> {
+  typedef f16 frag __attribute__((ext_vector_type(8)));
+  static constexpr unsigned kExp = 0x7C007C00u;
+  static constexpr unsigned short kOne = 0x3C00;
+  static constexpr float kShift = 15.f;
+  static constexpr int kTerms = 2;
+  static __device__ f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+  static __device__ f32x16 mma(frag a, frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+};
+template <typename C>
+using Frag = typename Half<C>::frag;
+
+// Zeroes the keys of an 8-key chunk (first key k) outside [begin, end).
+__device__ inline u32x4 keep_keys(u32x4 x, int k, int begin, int end) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = (float)q[e], o[e] = 0.f;
-  for (int64_t j = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0; j <= pos; ++j) {
-    const int64_t page = a.block_table[b * a.table_stride + (j >> page_shift)];
-    if (page < 0 || page >= a.pages) {
-      raise_flag(a.bad_flag);
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = k + 2 * i >= begin && k + 2 * i < end, hi = k + 2 * i + 1 >= begin && k + 2 * i + 1 < end;
+    x[i] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+  }
+  return x;
+}
+
+// The largest b with slot0(b) <= slot, slot0(b) = cu[b] * group / rows + b: sequence b's tiles of `rows` query rows are
+// slots slot0(b) and on.  64 candidates at a time.
+__device__ inline int find_seq(const int32_t* cu, int64_t seqs, int group, int rows, int64_t slot, int lane) {
+  int64_t lo = 0, n = seqs;
+  while (n > 1) {
+    const int64_t step = (n + 63) / 64, i = lo + lane * step;
+    const bool ok = lane * step < n && (int64_t)cu[i] * group / rows + i <= slot;
+    const int64_t last = max(1, __popcll(__ballot(ok))) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return __builtin_amdgcn_readfirstlane((int)lo);
+}
+
+// What a workgroup computes: query rows row0 .. of sequence b for one key head, and which keys any of them sees.
+struct Tile {
+  int64_t t0;       // first token of the sequence
+  int64_t b;
+  int row0, rows;   // first row and count in this tile (rows <= 0: none)
+  int kvh;
+  int first_pos;    // position of the sequence's first new token (may be negative)
+  int begin, end;   // keys seen by some row: [begin, end)
+};
+
+template <int ROWS>
+__device__ inline Tile find_tile(const AttnParams& p, int64_t tile, int lane) {
+  const auto& a = p.a;
+  Tile r;
+  r.kvh = (int)(tile % a.kv_heads);
+  const int64_t slot = tile / a.kv_heads;
+  if (a.cu) {
+    r.b = find_seq(a.cu, a.seqs, p.group, ROWS, slot, lane);
+  } else {
+    r.b = slot / ((p.group + ROWS - 1) / ROWS);
+  }
+  const SeqRange s = seq_range(a.cu, r.b, a.tokens, a.bad_flag);
+  const int64_t slot0 = a.cu ? (int64_t)a.cu[r.b] * p.group / ROWS + r.b : r.b * ((p.group + ROWS - 1) / ROWS);
+  const int64_t row0 = (slot - slot0) * ROWS, all = (int64_t)s.n * p.group;
+  r.t0 = s.t0;
+  r.row0 = (int)row0;
+  r.rows = row0 < 0 || row0 >= all ? 0 : (int)min((int64_t)ROWS, all - row0);
+  const int64_t want = a.kv_len[r.b], len = min(max(want, (int64_t)0), a.table_width << p.page_shift);
+  if (want != len) raise_flag(a.bad_flag);
+  r.first_pos = (int)(len - s.n);
+  const int lo = r.first_pos + r.row0 / p.group, hi = r.first_pos + (r.row0 + r.rows - 1) / p.group;
+  r.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
+  r.end = r.rows > 0 ? hi + 1 : 0;
+  return r;
+}
+
+// The page of the 16 keys from k on; -1 if nobody sees its page or the table's entry is no page.
+__device__ inline int page_of(const AttnParams& p, const Tile& t, int k) {
+  if (k >= t.end || (k >> p.page_shift) < (t.begin >> p.page_shift)) return -1;
+  const int pg = p.a.block_table[t.b * p.a.table_stride + (k >> p.page_shift)];
+  if (pg < 0 || pg >= p.a.pages) {
+    raise_flag(p.a.bad_flag);
+    return -1;
+  }
+  return pg;
+}
+
+// One 8-value slice of P as the terms that the second product takes.
+template <typename C, int TERMS>
+__device__ inline void terms_of(const float* p, Frag<C>* out) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float r = p[j];
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      out[t][j] = (C)r;
+      if (t + 1 < TERMS) r -= (float)out[t][j];
+    }
+  }
+}
+
+// acc += V P, where V values that are not finite reach the rows that see their keys and no other.
+template <typename C, int TERMS, typename ACC>
+__device__ __forceinline__ ACC pv_each(u32x4 v, const Frag<C>* p, Frag<C> seen, ACC acc) {
+  typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+  constexpr unsigned short e = Half<C>::kExp & 0xFFFF;
+  const u16x8 x = __builtin_bit_cast(u16x8, v);
+  u16x8 kind[4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool inf = (x[j] & 0x7FFF) == e, odd = (x[j] & e) == e;
+    kind[0][j] = odd ? 0 : x[j];
+    kind[1][j] = inf && !(x[j] & 0x8000) ? Half<C>::kOne : 0;
+    kind[2][j] = inf && (x[j] & 0x8000) ? Half<C>::kOne : 0;
+    kind[3][j] = odd && !inf ? Half<C>::kOne : 0;
+  }
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) acc = Half<C>::mma(__builtin_bit_cast(Frag<C>, kind[0]), p[t], acc);
+  const float what[3] = {INFINITY, -INFINITY, NAN};
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    ACC n;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(ACC) / 4); ++i) n[i] = 0.f;
+    n = Half<C>::mma(__builtin_bit_cast(Frag<C>, kind[c + 1]), seen, n);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(ACC) / 4); ++i)
+      if (n[i] > 0.f) acc[i] += what[c];
+  }
+  return acc;
+}
+
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- joining parts -------------------------------------------------------------------------------------------------
+
+// A part: m [ROWS], l [ROWS], O [ROWS][D].  Stores and loads go through to the level that all XCDs share.
+template <int ROWS, int D>
+constexpr int64_t part_floats() {
+  return (int64_t)ROWS * (D + 2);
+}
+__device__ inline void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ inline float get(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ inline void put4(float* p, const float* v) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t w = (uint64_t)__float_as_uint(v[2 * i]) | (uint64_t)__float_as_uint(v[2 * i + 1]) << 32;
+    __hip_atomic_store(q + i, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+__device__ inline float4 get4(const float* p) {
+  const uint64_t* q = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t x = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t y = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return {__uint_as_float((unsigned)x), __uint_as_float((unsigned)(x >> 32)), __uint_as_float((unsigned)y), __uint_as_float((unsigned)(y >> 32))};
+}
+
+// Called by the whole workgroup after its stores to the workspace: whether it is the last of `count` to arrive.  The
+// counter goes back to zero.
+__device__ inline bool last_of(unsigned* counter, int count, int* shared) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // this wave's stores are done
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *shared = n == (unsigned)(count - 1);
+    if (*shared) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool last = *shared;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  return last;
+}
+
+template <typename O>
+__device__ inline void store4(O* dst, const float* v) {
+  struct alignas(4 * sizeof(O)) V4 {
+    O v[4];
+  } o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o.v[j] = (O)v[j];
+  *reinterpret_cast<V4*>(dst) = o;
+}
+
+// Final values of 4 columns of a row.
+template <typename C, typename O, int D>
+__device__ inline void finish(const AttnParams& p, const Tile& t, int row, int col, float m, float l, const float* o) {
+  const int r = t.row0 + row, i = r / p.group, h = t.kvh * p.group + r % p.group;
+  const int64_t at = (t.t0 + i) * p.a.heads + h;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+  store4(static_cast<O*>(p.a.out) + at * D + col, v);
+  if (p.a.lse && col == 0) p.a.lse[at] = l == 0.f ? -INFINITY : (m - Half<C>::kShift + log2f(l)) * kLn2;
+}
+
+// Joins `count` parts from `src` on, into `dst` or, if that is NULL, into the output.
+template <typename C, typename O, int ROWS, int D>
+__device__ void join(const AttnParams& p, const Tile& t, const float* src, int count, float* dst) {
+  constexpr int64_t step = part_floats<ROWS, D>();
+  for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
+    const int row = i / (D / 4), col = i % (D / 4) * 4;
+    float ms[kFan], ls[kFan];
+    float4 os[kFan];
+#pragma unroll
+    for (int e = 0; e < kFan; ++e) {  // everything is asked for before the first use; past the last part it repeats the last
+      const float* q = src + min(e, count - 1) * step;
+      ms[e] = get(q + row);
+      ls[e] = get(q + ROWS + row);
+      os[e] = get4(q + 2 * ROWS + row * D + col);
+    }
+    float m = -INFINITY, l = 0.f, o[4] = {};
+#pragma unroll
+    for (int e = 0; e < kFan; ++e) m = fmaxf(m, ms[e]);
+#pragma unroll
+    for (int e = 0; e < kFan; ++e) {
+      const float w = e >= count || ms[e] == -INFINITY ? 0.f : exp2_(ms[e] - m);
+      if (e >= count || (w == 0.f && ls[e] == 0.f)) continue;  // (an infinite or NaN part keeps its say)
+      l = fmaf(w, ls[e], l);
+      o[0] = fmaf(w, os[e].x, o[0]), o[1] = fmaf(w, os[e].y, o[1]), o[2] = fmaf(w, os[e].z, o[2]), o[3] = fmaf(w, os[e].w, o[3]);
+    }
+    if (!dst) {
+      finish<C, O, D>(p, t, row, col, m, l, o);
       continue;
     }
-    const int at = (int)(j & (a.page - 1));
-    const C* k = static_cast<const C*>(a.k_cache) + ((page * a.kv_heads + kvh) * a.page + at) * D + lane * E;
-    const C* v = static_cast<const C*>(a.v_cache) + ((page * a.kv_heads + kvh) * D + lane * E) * a.page + at;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], (float)k[e], s);
-    s = wave_sum(s) * a.scale;
-    const float mn = fmaxf(m, s), keep = m == -INFINITY ? 0.f : __expf(m - mn), p = __expf(s - mn);
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(p, (float)v[e * a.page], o[e] * keep);
-    m = mn;
+    put4(dst + 2 * ROWS + row * D + col, o);
+    if (col == 0) put(dst + row, m), put(dst + ROWS + row, l);
   }
-  O* out = static_cast<O*>(a.out) + row * D + lane * E;
+}
+
+// Two-level join over the `active` parts of a tile; called by every one of them after it has stored its part.
+template <typename C, typename O, int ROWS, int D>
+__device__ void join_tree(const AttnParams& p, const Tile& t, int64_t tile, int part, int active, int* shared) {
+  uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
+  unsigned* counters = reinterpret_cast<unsigned*>(ws) + tile * kCounters;
+  float* parts = reinterpret_cast<float*>(ws + kHeader);
+  const int64_t step = part_floats<ROWS, D>();
+  float* mine = parts + tile * p.splits * step;
+  float* joined = parts + ((int64_t)p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
+  const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
+  if (!last_of(counters + set, in_set, shared)) return;
+  join<C, O, ROWS, D>(p, t, mine + set * kFan * step, in_set, sets == 1 ? nullptr : joined + set * step);
+  if (sets == 1) return;
+  if (!last_of(counters + kFan, sets, shared)) return;
+  join<C, O, ROWS, D>(p, t, joined, sets, nullptr);
+}
+
+// ---- few rows ------------------------------------------------------------------------------------------------------
+
+template <typename C, typename O, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p) {
+  constexpr int KK = D / 32, DT = D / 16;
+  constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
+  typedef Half<C> H;
+  __shared__ __attribute__((aligned(16))) float stage[kWaves][kRowsTile][D + 4];
+  __shared__ float stat[kWaves][2][kRowsTile];
+  __shared__ int shared;
+  const auto& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = blockIdx.x % p.splits;
+  const int64_t tile = blockIdx.x / p.splits;
+  const Tile t = find_tile<kRowsTile>(p, tile, lane);
+  if (t.rows <= 0) return;
+  // blocks of 32 keys; every wave of a part has at least one
+  const int first = t.begin / kBlock, blocks = t.end > 0 ? (t.end + kBlock - 1) / kBlock - first : 0;
+  const int active = max(1, min(p.splits, (blocks + kWaves - 1) / kWaves));
+  if (part >= active) return;
+  const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
+
+  const int r = lane & 15, g = lane >> 4;
+  const bool row_ok = r < t.rows;
+  const int row = t.row0 + (row_ok ? r : 0);
+  const int pos = t.first_pos + row / p.group;
+  const int least = a.window > 0 ? pos - a.window + 1 : 0;  // first key that this row sees
+  const int pos_lo = t.first_pos + t.row0 / p.group, pos_hi = t.end - 1;
+
+  Frag<C> q[KK];
+  {
+    const C* src = static_cast<const C*>(a.q) + (t.t0 + row / p.group) * a.q_token + (int64_t)(t.kvh * p.group + row % p.group) * a.q_head + 8 * g;
+    const Frag<C> zero = {};
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = (O)(l > 0.f ? o[e] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    for (int kk = 0; kk < KK; ++kk) q[kk] = row_ok ? *reinterpret_cast<const Frag<C>*>(src + 32 * kk) : zero;
+  }
+
+  const C* kc = static_cast<const C*>(a.k_cache);
+  const C* vc = static_cast<const C*>(a.v_cache);
+  u32x4 k[2][KK], v[DT];
+  int pages[2];
+  auto look = [&](int block) {
+    pages[0] = page_of(p, t, block * kBlock);
+    pages[1] = page_of(p, t, block * kBlock + 16);
+  };
+  auto load_k = [&](int block) {  // A row r of tile c is key 8 (r / 4) + 4 c + r % 4
+    const int pg = max(r < 8 ? pages[0] : pages[1], 0);
+    const int at = (block * kBlock + 8 * (r >> 2) + (r & 3)) & (a.page - 1);
+    const C* src = kc + ((int64_t)(pg * (int64_t)a.kv_heads + t.kvh) * a.page + at) * D + 8 * g;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) k[c][kk] = *reinterpret_cast<const u32x4*>(src + 4 * c * D + 32 * kk);
+  };
+  auto load_v = [&](int block) {
+    const int pg = max(g < 2 ? pages[0] : pages[1], 0);
+    const int at = (block * kBlock + 8 * g) & (a.page - 1);
+    const C* src = vc + ((int64_t)(pg * (int64_t)a.kv_heads + t.kvh) * D + r) * a.page + at;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) v[d] = *reinterpret_cast<const u32x4*>(src + (int64_t)d * 16 * a.page);
+  };
+
+  f32x4 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  int block = lo + wave;
+  auto begin = [&]() {
+    if (block < hi) {
+      look(block);
+      load_k(block);
+      load_v(block);
+    }
+  };
+  bool careful = false;
+  begin();
+  while (block < hi) {
+    const int k0 = block * kBlock, ok0 = pages[0], ok1 = pages[1], next = block + kWaves;
+    f32x4 s[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      s[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) s[c] = H::mma(__builtin_bit_cast(Frag<C>, k[c][kk]), q[kk], s[c]);
+    }
+    if (next < hi) {
+      look(next);
+      load_k(next);
+    }
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][j & 3] * p.scale2;
+    const bool whole = ok0 >= 0 && ok1 >= 0 && k0 + kBlock - 1 <= pos_lo && (a.window <= 0 || k0 > pos_hi - a.window);
+    const bool ok = (g < 2 ? ok0 : ok1) >= 0;
+    auto seen = [&](int j) {
+      const int key = k0 + 8 * g + j;
+      return ok && key <= pos && key >= least;
+    };
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!seen(j)) x[j] = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) v[d] = ok ? keep_keys(v[d], k0 + 8 * g, t.begin, t.end) : u32x4{0u, 0u, 0u, 0u};
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) mx = fmaxf(mx, x[j]);
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : exp2_(m - mn);
+      m = mn;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= keep;
+    }
+    const float base = (m == -INFINITY ? 0.f : m) - H::kShift;
+    float pr[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      pr[j] = exp2_(x[j] - base);
+      l += pr[j];
+    }
+    Frag<C> pt[TERMS];
+    terms_of<C, TERMS>(pr, pt);
+    if (careful) {
+      Frag<C> sf;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sf[j] = seen(j) ? (C)1.f : (C)0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = pv_each<C, TERMS>(v[d], pt, sf, o[d]);
+    } else {
+#pragma unroll
+      for (int tm = 0; tm < TERMS; ++tm)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = H::mma(__builtin_bit_cast(Frag<C>, v[d]), pt[tm], o[d]);
+    }
+    if (next < hi) load_v(next);
+    block = next;
+    if (block >= hi && !careful) {  // a NaN: once more, with care
+      bool odd = false;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd = odd || o[d][j] != o[d][j];
+      if (__any(odd)) {
+        careful = true;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        m = -INFINITY, l = 0.f, block = lo + wave;
+        begin();
+      }
+    }
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+
+  // the waves' results through LDS: O^T registers hold columns 16 d + 4 g .. + 3 of row r
+#pragma unroll
+  for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(&stage[wave][r][16 * d + 4 * g]) = o[d];
+  if (g == 0) stat[wave][0][r] = m, stat[wave][1][r] = l;
+  __syncthreads();
+  float* dst = nullptr;
+  if (active > 1)
+    dst = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kHeader) + (tile * p.splits + part) * part_floats<kRowsTile, D>();
+  for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
+    const int rr = i / (D / 4), col = i % (D / 4) * 4;
+    float M = -INFINITY, L = 0.f, out[4] = {};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, stat[w][0][rr]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = stat[w][0][rr], lw = stat[w][1][rr], f = mw == -INFINITY ? 0.f : exp2_(mw - M);
+      if (f == 0.f && lw == 0.f) continue;
+      const f32x4 x = *reinterpret_cast<const f32x4*>(&stage[w][rr][col]);
+      L = fmaf(f, lw, L);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[j] = fmaf(f, x[j], out[j]);
+    }
+    if (!dst) {
+      finish<C, O, D>(p, t, rr, col, M, L, out);
+    } else {
+      put4(dst + 2 * kRowsTile + rr * D + col, out);
+      if (col == 0) put(dst + rr, M), put(dst + kRowsTile + rr, L);
+    }
+  }
+  if (dst) join_tree<C, O, kRowsTile, D>(p, t, tile, part, active, &shared);
+}
+
+// ---- host ----------------------------------------------------------------------------------------------------------
+
+// Tiles of `rows` query rows over all sequences (an upper bound; what is left over finds no rows) and key heads.
+int64_t slots_of(int64_t tokens, int64_t seqs, int group, int rows, bool offsets) {
+  return offsets ? tokens * group / rows + seqs : seqs * ((group + rows - 1) / rows);
+}
+
+// Parts per tile: enough workgroups to fill the card, none for tiles that fill it alone.
+int splits_of(int64_t tiles, int64_t units, int64_t target) {
+  if (tiles * 2 > target) return 1;
+  const int64_t s = std::min<int64_t>(target / tiles, units);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits));
+}
+
+template <typename C, typename O, int D>
+hipError_t launch_rows(AttnParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((attn_rows_kernel<C, O, D>), dim3((unsigned)((int64_t)p.slots * p.a.kv_heads * p.splits)), dim3(kThreads), 0, s, p);
+  return hipGetLastError();
 }
 
 template <typename C, typename O>
-hipError_t launch(const tq_paged_attn_args& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tokens * a.heads));
-  const int sh = __builtin_ctz(a.page);
-  if (a.dim == 64) hipLaunchKernelGGL((attn_simple_kernel<C, O, 64>), grid, dim3(64), 0, s, a, sh);
-  if (a.dim == 128) hipLaunchKernelGGL((attn_simple_kernel<C, O, 128>), grid, dim3(64), 0, s, a, sh);
-  if (a.dim == 256) hipLaunchKernelGGL((attn_simple_kernel<C, O, 256>), grid, dim3(64), 0, s, a, sh);
-  return hipGetLastError();
+hipError_t launch_type(AttnParams& p, hipStream_t s) {
+  return p.a.dim == 64 ? launch_rows<C, O, 64>(p, s) : p.a.dim == 128 ? launch_rows<C, O, 128>(p, s) : launch_rows<C, O, 256>(p, s);
 }
 
 }  // namespace
 
-int64_t paged_attn_workspace_bytes(int64_t, int64_t, int, int, int) { return 0; }
+int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int kv_heads, int dim) {
+  if (tokens == 0) return 0;
+  (void)heads, (void)kv_heads, (void)seqs;
+  return kHeader + (int64_t)(kMaxParts + kMaxParts / kFan + kMaxParts) * kRowsTile * (dim + 2) * 4;
+}
 
 hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
-  if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch<bf16, float>(a, s) : launch<bf16, bf16>(a, s);
-  return a.out_type == TQ_F32 ? launch<f16, float>(a, s) : launch<f16, f16>(a, s);
+  AttnParams p{a};
+  p.scale2 = a.scale * kLog2e;
+  p.group = a.heads / a.kv_heads;
+  p.page_shift = __builtin_ctz(a.page);
+  const int64_t keys = a.table_width * a.page;
+  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, kRowsTile, a.cu != nullptr);
+  const int64_t tiles = (int64_t)p.slots * a.kv_heads;
+  p.splits = a.workspace ? splits_of(tiles, (keys + kWaves * kBlock - 1) / (kWaves * kBlock), kMaxParts) : 1;
+  if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch_type<bf16, float>(p, s) : launch_type<bf16, bf16>(p, s);
+  return a.out_type == TQ_F32 ? launch_type<f16, float>(p, s) : launch_type<f16, f16>(p, s);
 }
 
 }  // namespace tq
