@@ -23,7 +23,7 @@ PROBE_SOURCES = ["hbm_probe.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["tq_api.cpp", "k_workspace.hip", "scratch.hip", "k_quant.hip", "k_repack.hip", "k_gemv_pq2.hip", "k_gemm_pq2.hip", "k_gemv_ptq1.hip", "k_gemm_ptq1.hip",
-           "seq_api.cpp", "k_rope_append.hip", "k_paged_attn.hip", "k_gdn.hip"]
+           "seq_api.cpp", "k_rope_append.hip", "k_paged_attn.hip", "k_gdn.hip", "k_gdn_chunk.hip"]
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -22,11 +22,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 32;
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
-  T v[N];
-};
-
 template <typename IN, typename O, int DK>
 __global__ __launch_bounds__(kThreads) void gdn_step_kernel(tq_gdn_args a) {
   constexpr int R = DK / 32;  // rows per thread
@@ -122,9 +117,12 @@ hipError_t launch_step(const tq_gdn_args& a, hipStream_t s) {
 
 }  // namespace
 
-int64_t gdn_workspace_bytes(int64_t, int64_t, int64_t, int, int, int) { return 0; }
+int64_t gdn_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int v_heads, int dk, int dv) {
+  return gdn_chunked(tokens, seqs, max_len) ? gdn_chunk_workspace_bytes(tokens, seqs, max_len, v_heads, dk, dv) : 0;
+}
 
 hipError_t launch_gdn(const tq_gdn_args& a, hipStream_t s) {
+  if (a.workspace && a.cu && gdn_chunked(a.tokens, a.seqs, a.max_len)) return launch_gdn_chunk(a, s);
   switch (a.in_type) {
     case TQ_F32: return launch_step<float, float>(a, s);
     case TQ_BF16: return a.out_type == TQ_F32 ? launch_step<bf16, float>(a, s) : launch_step<bf16, bf16>(a, s);

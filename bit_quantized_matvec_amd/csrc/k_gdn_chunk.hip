@@ -1,0 +1,638 @@
+// k_gdn_chunk.hip -- the gated delta rule over chunks of 64 tokens.
+//
+// Mathematics.  Within a chunk let G_i be the running sum of g, k_i and q_i the
+// (normalised) rows, S the state before it.  Unrolling the recurrence, the
+// values x_i = d_i that token i writes solve the unit triangular system
+//   x_i + sum_{j<i} A_ij x_j = r_i,   A_ij = beta_i e^(G_i - G_j) k_i.k_j,
+//   r_i = beta_i v_i - beta_i e^(G_i) S^T k_i,
+// and with T = (I + A)^-1, P_ij = scale e^(G_i - G_j) q_i.k_j (j <= i):
+//   X = T R,   out_i = scale e^(G_i) S^T q_i + sum_j P_ij x_j,
+//   S <- e^(G_63) S + sum_j k_j (x) e^(G_63 - G_j) x_j.
+// Every exponent is at most 0.  T and P do not depend on S: a first kernel
+// computes them for all chunks at once; a second one walks the chunks of each
+// sequence, one wave per 16 columns of a head's state (columns do not meet).
+//
+// Precision.  All products run on the bf16 matrix instructions with fp32 sums;
+// operands are split into bf16 terms whose sum holds them: fp32 values as 3
+// terms (24 bits, bf16's range is fp32's), fp16 as 2, bf16 as 1, and products
+// of terms below 2^-24 of the whole are left out.  Q and K enter as given;
+// norms and decays multiply rows of results.  Where out has 16 bits, what goes
+// only into it (S in S^T q, P, X in P X) takes 2 terms: 2^-17 of the values'
+// size beside the 2^-9 or 2^-12 of the output's own rounding.
+// T is built in fp32 on the fp32 matrix instructions.  Every entry that the
+// block recursion forms is one of T's own, and those are bounded by the
+// recurrence's transitions, so nothing grows on the way.
+//
+// Layout.  A matrix-instruction result leaves lane (n, g) with rows 4g .. 4g+3
+// of column n, and an operand wants 8g .. 8g+7 of the summed index.  Rows of
+// the left operands are therefore fed in the order row r of tile (s, c) =
+// 32s + 8(r/4) + 4c + r%4, which leaves lane group g with 32s + 8g + 4c + i:
+// two tiles make one operand, and the state, R and X go from product to product
+// in the registers that they are in.  The first kernel writes K, Q, K^T, T and
+// P as operands: 1 KB per fragment, 16 consecutive bytes per lane, zeros past
+// the sequence's end.  K^T is K times the identity, whose result is K
+// transposed in just that order.
+//
+// Values that are not finite reach only later tokens of the recurrence, but
+// every row of a matrix product.  A chunk with any in q, k, v, beta or with
+// g > 0 is walked token after token instead (as are sequences of less than
+// kStepLen tokens).
+#include <algorithm>
+
+#include "seq.h"
+
+namespace tq {
+namespace {
+
+constexpr int kChunk = 64;
+constexpr int kStepLen = 24;
+constexpr int kPrepThreads = 256;
+constexpr int64_t kBudget = int64_t(256) << 20;  // workspace: what the last-level cache holds
+constexpr int kFragBytes = 1024;
+constexpr int kScalarBytes = 2048;
+constexpr float kLeastG = -1024.f;  // e^g is 0 in fp32 far above
+
+typedef bf16 frag __attribute__((ext_vector_type(8)));
+
+// Per chunk and value head.
+struct Scalars {
+  float beta[kChunk], far_k[kChunk], far_q[kChunk], last_k[kChunk];
+  float decay;
+  int odd;
+};
+static_assert(sizeof(Scalars) <= kScalarBytes, "");
+
+template <typename IN>
+constexpr int terms_in() {
+  return sizeof(IN) == 4 ? 3 : __is_same(IN, bf16) ? 1 : 2;
+}
+constexpr int key_frags(int dk, int tk) { return 12 * (dk / 32) * tk; }  // K, Q, K^T of a chunk and key head
+constexpr int tri_frags(int terms) { return 6 * terms; }                 // lower triangle in tiles of 16 x 32
+
+struct ChunkParams {
+  tq_gdn_args a;
+  uint8_t* units;
+  float* carry;  // states between launches, [nseq][v_heads][dk][dv]
+  int64_t unit_bytes, seq0, slots;
+  int nseq, chunk0, chunks;  // this launch: chunks [chunk0, chunk0 + chunks) of sequences [seq0, seq0 + nseq)
+  int whole;                 // one launch for everything: chunks laid out by cu
+  int last;
+};
+
+__device__ inline f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ inline f32x4 mma4(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// c += a b over the terms' products above 2^-24 of the whole
+template <int TA, int TB>
+__device__ inline f32x4 mma_terms(const frag* a, const frag* b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < TA; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      if (i + j < 3) c = mma(a[i], b[j], c);
+  return c;
+}
+
+// place of row r of 16-row tile t in the chunk (or the head's rows)
+__device__ inline int place(int t, int r) { return 32 * (t >> 1) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3); }
+__device__ inline int tri_at(int tile, int s) { return tile < 2 ? tile : 2 * tile - 2 + s; }
+
+template <typename IN>
+__device__ inline void load8(const IN* p, float* x) {
+  const Vec<IN, 8> v = *reinterpret_cast<const Vec<IN, 8>*>(p);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = (float)v.v[j];
+}
+
+// ---- T, P and the operands of every chunk --------------------------------------------------------------------------
+
+template <typename IN, int DK, int OT>
+__global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p) {
+  constexpr int KS = DK / 32, TK = terms_in<IN>(), W = kChunk + 4;
+  __shared__ __attribute__((aligned(16))) float A[kChunk][W], T[kChunk][W];
+  __shared__ double sums[kChunk];
+  __shared__ float norms[kChunk];
+  const auto& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
+  const int h = blockIdx.x % a.v_heads, group = a.v_heads / a.k_heads, kh = h / group;
+  const int64_t slot = blockIdx.x / a.v_heads;
+  const int64_t b = p.whole ? find_seq(a.cu, a.seqs, 1, kChunk, slot, lane) : p.seq0 + slot / p.chunks;
+  const SeqRange r = seq_range(a.cu, b, a.tokens, nullptr);
+  const int64_t c = p.whole ? slot - (r.t0 / kChunk + b) : p.chunk0 + slot % p.chunks;
+  if (r.n < kStepLen || c < 0 || c * kChunk >= r.n) return;
+  const int64_t t0 = r.t0 + c * kChunk;
+  const int len = min(kChunk, r.n - (int)c * kChunk);
+
+  uint8_t* unit = p.units + slot * p.unit_bytes;
+  uint8_t* keys = unit + (int64_t)kh * (key_frags(DK, TK) * kFragBytes);
+  uint8_t* tri = unit + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
+  Scalars* sc = reinterpret_cast<Scalars*>(tri + tri_frags(3 + OT) * kFragBytes);
+  auto put = [&](uint8_t* at, int index, frag f) { *reinterpret_cast<frag*>(at + index * kFragBytes + lane * 16) = f; };
+  const bool writes_keys = h % group == 0;
+
+  // this wave's 16 tokens, as right operands; column n is token i
+  const int i = place(wave, n);
+  const IN* kp = static_cast<const IN*>(a.k) + t0 * a.k_token + kh * a.k_head + 8 * g;
+  const IN* qp = static_cast<const IN*>(a.q) + t0 * a.q_token + kh * a.q_head + 8 * g;
+  frag qf[KS][TK], kf[KS][TK];
+  float qq = 0.f, kk = 0.f;
+  {
+    const int at = min(i, len - 1);
+    const float live = i < len ? 1.f : 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8], y[8];
+      load8(qp + at * a.q_token + 32 * s, x);
+      load8(kp + at * a.k_token + 32 * s, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        qq = fmaf(x[j], x[j], qq), kk = fmaf(y[j], y[j], kk);
+        if (live == 0.f) x[j] = y[j] = 0.f;
+      }
+      split_terms<TK>(x, qf[s]);
+      split_terms<TK>(y, kf[s]);
+    }
+  }
+  qq += __shfl_xor(qq, 16, 64), kk += __shfl_xor(kk, 16, 64);
+  qq += __shfl_xor(qq, 32, 64), kk += __shfl_xor(kk, 32, 64);
+  float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f, beta = 0.f;
+  bool odd = false;
+  if (i < len) {
+    beta = a.beta[(t0 + i) * a.v_heads + h];
+    odd = !(qq < INFINITY) || !(kk < INFINITY) || !(fabsf(nq) < INFINITY) || !(nk < INFINITY) || !(fabsf(beta) < INFINITY);
+  } else {
+    nq = nk = 0.f;
+  }
+  if (g == 0) norms[i] = nk;
+  {
+    const float x = lane < len ? a.g[(t0 + lane) * a.v_heads + h] : 0.f;
+    odd = odd || !(x <= 0.f);
+    if (wave == 0) {
+      double sum = fmaxf(x, kLeastG);
+#pragma unroll
+      for (int o = 1; o < kChunk; o <<= 1) {
+        const double y = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += y;
+      }
+      sums[lane] = sum;
+    }
+  }
+  odd = __syncthreads_or(odd);
+  if (odd) {  // the walk will not look at anything else
+    if (tid == 0) sc->odd = 1;
+    // the other heads' chunks may still want K, Q and K^T: a chunk that is odd by its beta or g alone
+  }
+  const double mine = sums[i];
+#pragma unroll 1
+  for (int s2 = 0; s2 <= wave >> 1; ++s2) {
+    frag kt[2][KS][TK];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int row = place(2 * s2 + t, n), at = min(row, len - 1);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float y[8];
+        load8(kp + at * a.k_token + 32 * s, y);
+        if (row >= len)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = 0.f;
+        split_terms<TK>(y, kt[t][s]);
+      }
+    }
+    f32x4 akk[2] = {}, aqk[2] = {};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) akk[t] = mma_terms<TK, TK>(kt[t][s], kf[s], akk[t]), aqk[t] = mma_terms<TK, TK>(kt[t][s], qf[s], aqk[t]);
+    float ra[8], rp[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = 32 * s2 + 8 * g + j;
+      const float e = row <= i ? expf((float)(mine - sums[row])) * norms[row] : 0.f;
+      rp[j] = row <= i ? nq * e * aqk[j >> 2][j & 3] : 0.f;
+      ra[j] = row < i ? beta * nk * e * akk[j >> 2][j & 3] : 0.f;
+    }
+    *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g]) = float4{ra[0], ra[1], ra[2], ra[3]};
+    *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g + 4]) = float4{ra[4], ra[5], ra[6], ra[7]};
+    frag pf[OT];
+    split_terms<OT>(rp, pf);
+#pragma unroll
+    for (int t = 0; t < OT; ++t) put(tri + tri_frags(3) * kFragBytes, tri_at(wave, s2) * OT + t, pf[t]);
+    if (writes_keys && s2 == wave >> 1) {
+      const int c2 = wave & 1;  // this wave transposes every second tile of the head's rows
+      frag one;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) one[j] = (bf16)(8 * g + j == place(c2, n) ? 1.f : 0.f);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int t = 0; t < TK; ++t) {
+          const f32x4 lo = mma(kt[0][s][t], one, f32x4{}), hi = mma(kt[1][s][t], one, f32x4{});
+          frag f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = (bf16)lo[j], f[4 + j] = (bf16)hi[j];
+          put(keys + 8 * KS * TK * kFragBytes, ((2 * s + c2) * 2 + s2) * TK + t, f);
+        }
+    }
+  }
+  if (writes_keys)
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int t = 0; t < TK; ++t) {
+        put(keys, (wave * KS + s) * TK + t, kf[s][t]);
+        put(keys + 4 * KS * TK * kFragBytes, (wave * KS + s) * TK + t, qf[s][t]);
+      }
+  if (odd) return;
+  const double all = sums[kChunk - 1];
+  if (g == 0) {
+    const float far = expf((float)mine);
+    sc->beta[i] = beta;
+    sc->far_k[i] = beta * far * nk;
+    sc->far_q[i] = far * nq;
+    sc->last_k[i] = expf((float)(all - mine)) * nk;
+  }
+  if (tid == 0) sc->decay = expf((float)all), sc->odd = 0;
+
+  // T: the diagonal blocks of 16 by substitution, one column per lane ...
+  for (int k = tid; k < kChunk * W; k += kPrepThreads) (&T[0][0])[k] = 0.f;
+  __syncthreads();
+  if (lane < 16) {
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float v = k == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < k; ++j) v = fmaf(-A[16 * wave + k][16 * wave + j], x[j], v);
+      x[k] = v;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) T[16 * wave + k][16 * wave + lane] = x[k];
+  }
+  __syncthreads();
+  // ... then T21 = -T22 (A21 T11), for blocks of 16 and of 32.  A step's 4 summed indices are 4g + s: what a result holds.
+  auto block = [&](const float(*l)[W], int li, int lj, f32x4 right, f32x4 sum, float sign) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) sum = mma4(sign * l[16 * li + n][16 * lj + 4 * g + s], right[s], sum);
+    return sum;
+  };
+  auto column = [&](int bi, int bj) {
+    f32x4 v;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = T[16 * bi + 4 * g + s][16 * bj + n];
+    return v;
+  };
+  auto store = [&](int bi, int bj, f32x4 v) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) T[16 * bi + 4 * g + s][16 * bj + n] = v[s];
+  };
+  if (wave < 2) {
+    const f32x4 m = block(A, 2 * wave + 1, 2 * wave, column(2 * wave, 2 * wave), f32x4{}, 1.f);
+    store(2 * wave + 1, 2 * wave, block(T, 2 * wave + 1, 2 * wave + 1, m, f32x4{}, -1.f));
+  }
+  __syncthreads();
+  if (wave < 2) {
+    f32x4 m[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f32x4 v = column(k, wave);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) m[t] = block(A, 2 + t, k, v, m[t], 1.f);
+    }
+    store(2, wave, block(T, 2, 2, m[0], f32x4{}, -1.f));
+    store(3, wave, block(T, 3, 3, m[1], block(T, 3, 2, m[0], f32x4{}, -1.f), -1.f));
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int s2 = 0; s2 <= wave >> 1; ++s2) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = T[i][32 * s2 + 8 * g + j];
+    frag f[3];
+    split_terms<3>(x, f);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) put(tri, tri_at(wave, s2) * 3 + t, f[t]);
+  }
+}
+
+// ---- the walk over the chunks --------------------------------------------------------------------------------------
+
+// Tokens [t, end) one after another, on the state that lane (n, g) holds: rows 32s + 8g + j of column n (NT columns 16
+// apart).
+template <typename IN, typename O, int DK, int NT>
+__device__ __forceinline__ void walk(const tq_gdn_args& a, int64_t t, int64_t end, int h, int col, f32x4 (&s)[NT][DK / 16]) {
+  constexpr int KS = DK / 32;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int kh = h / (a.v_heads / a.k_heads);
+#pragma unroll 1
+  for (; t < end; ++t) {
+    const IN* qp = static_cast<const IN*>(a.q) + t * a.q_token + kh * a.q_head + 8 * g;
+    const IN* kp = static_cast<const IN*>(a.k) + t * a.k_token + kh * a.k_head + 8 * g;
+    const IN* vp = static_cast<const IN*>(a.v) + t * a.v_token + h * a.v_head + col + n;
+    float q[KS * 8], k[KS * 8], qq = 0.f, kk = 0.f, kq = 0.f;
+#pragma unroll
+    for (int x = 0; x < KS; ++x) load8(qp + 32 * x, q + 8 * x), load8(kp + 32 * x, k + 8 * x);
+#pragma unroll
+    for (int x = 0; x < KS * 8; ++x) qq = fmaf(q[x], q[x], qq), kk = fmaf(k[x], k[x], kk), kq = fmaf(k[x], q[x], kq);
+    float r1[NT] = {}, r2[NT] = {};
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int x = 0; x < KS * 8; ++x) {
+        const float v = s[m][x >> 2][x & 3];
+        r1[m] = fmaf(v, k[x], r1[m]), r2[m] = fmaf(v, q[x], r2[m]);
+      }
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) {
+      qq += __shfl_xor(qq, o, 64), kk += __shfl_xor(kk, o, 64), kq += __shfl_xor(kq, o, 64);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) r1[m] += __shfl_xor(r1[m], o, 64), r2[m] += __shfl_xor(r2[m], o, 64);
+    }
+    const float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f;
+    const float decay = expf(a.g[t * a.v_heads + h]), beta = a.beta[t * a.v_heads + h];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const float d = beta * ((float)vp[16 * m] - decay * (r1[m] * nk));
+      const float o = fmaf(kq * nq * nk, d, decay * (r2[m] * nq));
+#pragma unroll
+      for (int x = 0; x < KS * 8; ++x) s[m][x >> 2][x & 3] = fmaf(k[x] * nk, d, decay * s[m][x >> 2][x & 3]);
+      if (g == 0) static_cast<O*>(a.out)[(t * a.v_heads + h) * a.dv + col + 16 * m + n] = (O)o;
+    }
+  }
+}
+
+template <typename IN, typename O, int DK, int NT>
+__global__ __launch_bounds__(64, 1) void gdn_walk_kernel(ChunkParams p) {
+  constexpr int KS = DK / 32, TK = terms_in<IN>(), OT = sizeof(O) == 4 ? 3 : 2;
+  const auto& a = p.a;
+  const int lane = threadIdx.x, n = lane & 15, g = lane >> 4;
+  const int slices = a.dv / (16 * NT);
+  // Slices of a head read the same operands, heads of a group the same K and Q: they share an XCD (workgroups go round the
+  // 8 of them), unless that left XCDs without work.
+  const int group = a.v_heads / a.k_heads, together = (int64_t)p.nseq * a.k_heads >= 8 ? group : 1;
+  const int64_t x = blockIdx.x / 8 / (slices * together) * 8 + blockIdx.x % 8;
+  const int in = blockIdx.x / 8 % (slices * together);
+  const int64_t head = x * together + in / slices;
+  if (head >= (int64_t)p.nseq * a.v_heads) return;
+  const int col = in % slices * (16 * NT), h = (int)(head % a.v_heads);
+  const int64_t b = p.seq0 + head / a.v_heads;
+  const int kh = h / group;
+
+  const SeqRange r = seq_range(a.cu, b, a.tokens, a.bad_flag);
+  const bool first = p.chunk0 == 0;
+  const int64_t from = (int64_t)p.chunk0 * kChunk;
+  if (!first && from >= r.n) return;
+  const int64_t slot = a.slots ? a.slots[b] : b;
+  const bool kept = slot >= 0 && slot < a.states;
+  if (slot >= a.states) raise_flag(a.bad_flag);
+  const bool ends = p.last || from + (int64_t)p.chunks * kChunk >= r.n;
+
+  f32x4 s[NT][2 * KS];
+  float* carry = p.carry ? p.carry + ((b - p.seq0) * a.v_heads + h) * DK * (int64_t)a.dv : nullptr;
+  const int64_t state_at = ((kept ? slot : 0) * a.v_heads + h) * DK * (int64_t)a.dv;
+  const int cell = 8 * g * a.dv + col + n;
+  {
+    const float* src = first ? a.state + state_at : carry;
+    const bool there = !first || kept;
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[m][t][j] = there ? src[cell + (32 * (t >> 1) + 4 * (t & 1) + j) * a.dv + 16 * m] : 0.f;
+  }
+
+  int64_t done = r.n < kStepLen ? 0 : from;
+  if (r.n >= kStepLen) {
+    const int64_t stop = ends && !p.last ? r.n : min((int64_t)r.n, from + (int64_t)p.chunks * kChunk);
+    for (; done < stop; done += kChunk) {
+      const int64_t c = done / kChunk;
+      const int len = (int)min((int64_t)kChunk, r.n - done);
+      const uint8_t* unit = p.units + (p.whole ? r.t0 / kChunk + b + c : (b - p.seq0) * p.chunks + c - p.chunk0) * p.unit_bytes;
+      const uint8_t* keys = unit + (int64_t)kh * (key_frags(DK, TK) * kFragBytes) + lane * 16;
+      const uint8_t* tri = unit + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
+      const Scalars* sc = reinterpret_cast<const Scalars*>(tri + tri_frags(3 + OT) * kFragBytes);
+      tri += lane * 16;
+      auto get = [&](const uint8_t* at, int index) { return *reinterpret_cast<const frag*>(at + index * kFragBytes); };
+      const IN* vp = static_cast<const IN*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
+      float v[NT][4][4];  // tokens place(t, 4g + j)
+      bool odd = sc->odd != 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + j;
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            v[m][t][j] = row < len ? (float)vp[row * a.v_token + 16 * m] : 0.f;
+            odd = odd || !(fabsf(v[m][t][j]) < INFINITY);
+          }
+        }
+      if (__any(odd)) {
+        walk<IN, O, DK, NT>(a, r.t0 + done, r.t0 + done + len, h, col, s);
+        continue;
+      }
+      frag sf[NT][KS][3];
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) split_terms<3>(reinterpret_cast<const float*>(&s[m][2 * k]), sf[m][k]);
+      // R = beta V - far_k (K S)
+      frag rf[NT][2][3];
+      {
+        f32x4 acc[NT][4] = {};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            frag kf[TK];
+#pragma unroll
+            for (int e = 0; e < TK; ++e) kf[e] = get(keys, (t * KS + k) * TK + e);
+#pragma unroll
+            for (int m = 0; m < NT; ++m) acc[m][t] = mma_terms<TK, 3>(kf, sf[m][k], acc[m][t]);
+          }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+          const f32x4 be = *reinterpret_cast<const f32x4*>(sc->beta + row), fk = *reinterpret_cast<const f32x4*>(sc->far_k + row);
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][t][j] = fmaf(be[j], v[m][t][j], -fk[j] * acc[m][t][j]);
+        }
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) split_terms<3>(reinterpret_cast<const float*>(&acc[m][2 * k]), rf[m][k]);
+      }
+      // X = T R
+      f32x4 y[NT][4] = {};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k <= t >> 1; ++k) {
+          frag tf[3];
+#pragma unroll
+          for (int e = 0; e < 3; ++e) tf[e] = get(tri, tri_at(t, k) * 3 + e);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) y[m][t] = mma_terms<3, 3>(tf, rf[m][k], y[m][t]);
+        }
+      // out = far_q (Q S) + P X
+      f32x4 o[NT][4] = {};
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          frag qf[TK];
+#pragma unroll
+          for (int e = 0; e < TK; ++e) qf[e] = get(keys + 4 * KS * TK * kFragBytes, (t * KS + k) * TK + e);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) o[m][t] = mma_terms<TK, OT>(qf, sf[m][k], o[m][t]);
+        }
+      frag yf[NT][2][OT], zf[NT][2][3];
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) split_terms<OT>(reinterpret_cast<const float*>(&y[m][2 * k]), yf[m][k]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+        const f32x4 fq = *reinterpret_cast<const f32x4*>(sc->far_q + row), lk = *reinterpret_cast<const f32x4*>(sc->last_k + row);
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[m][t][j] *= fq[j], y[m][t][j] *= lk[j];
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) split_terms<3>(reinterpret_cast<const float*>(&y[m][2 * k]), zf[m][k]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k <= t >> 1; ++k) {
+          frag pf[OT];
+#pragma unroll
+          for (int e = 0; e < OT; ++e) pf[e] = get(tri + tri_frags(3) * kFragBytes, tri_at(t, k) * OT + e);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) o[m][t] = mma_terms<OT, OT>(pf, yf[m][k], o[m][t]);
+        }
+      // S = decay S + K^T Z
+      const float decay = sc->decay;
+#pragma unroll
+      for (int t = 0; t < 2 * KS; ++t) {
+#pragma unroll
+        for (int m = 0; m < NT; ++m) s[m][t] *= decay;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          frag kt[TK];
+#pragma unroll
+          for (int e = 0; e < TK; ++e) kt[e] = get(keys + 8 * KS * TK * kFragBytes, (t * 2 + k) * TK + e);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) s[m][t] = mma_terms<TK, 3>(kt, zf[m][k], s[m][t]);
+        }
+      }
+      O* op = static_cast<O*>(a.out) + ((r.t0 + done) * a.v_heads + h) * a.dv + col + n;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + j;
+          if (row < len)
+#pragma unroll
+            for (int m = 0; m < NT; ++m) op[(int64_t)row * a.v_heads * a.dv + 16 * m] = (O)o[m][t][j];
+        }
+    }
+  }
+  // sequences too short for chunks, and what a wrong max_len left over
+  if (ends && done < r.n) walk<IN, O, DK, NT>(a, r.t0 + done, r.t0 + r.n, h, col, s);
+
+  if (ends && (!kept || (r.n == 0 && a.state_out == a.state))) return;
+  float* dst = ends ? a.state_out + state_at : carry;
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[cell + (32 * (t >> 1) + 4 * (t & 1) + j) * a.dv + 16 * m] = s[m][t][j];
+}
+
+// ---- host ----------------------------------------------------------------------------------------------------------
+
+int64_t unit_bytes(int k_heads, int v_heads, int dk, int tk, int ot) {
+  return (int64_t)k_heads * key_frags(dk, tk) * kFragBytes + (int64_t)v_heads * (tri_frags(3 + ot) * kFragBytes + kScalarBytes);
+}
+int64_t longest(int64_t tokens, int64_t max_len) { return max_len > 0 ? std::min(max_len, tokens) : tokens; }
+
+template <typename IN, typename O, int DK, int NT>
+void launch_walk(const ChunkParams& p, hipStream_t s) {
+  const int group = p.a.v_heads / p.a.k_heads, slices = p.a.dv / (16 * NT);
+  const int64_t heads = (int64_t)p.nseq * p.a.v_heads, together = (int64_t)p.nseq * p.a.k_heads >= 8 ? group : 1;
+  const int64_t blocks = (heads / together + 7) / 8 * 8 * together * slices;
+  hipLaunchKernelGGL((gdn_walk_kernel<IN, O, DK, NT>), dim3((unsigned)blocks), dim3(64), 0, s, p);
+}
+
+template <typename IN, typename O, int DK>
+hipError_t launch_all(const tq_gdn_args& a, hipStream_t s) {
+  constexpr int OT = sizeof(O) == 4 ? 3 : 2;
+  ChunkParams p{a};
+  p.unit_bytes = unit_bytes(a.k_heads, a.v_heads, DK, terms_in<IN>(), OT);
+  p.units = static_cast<uint8_t*>(a.workspace);
+  auto run = [&](bool wide) {
+    hipLaunchKernelGGL((gdn_prepare_kernel<IN, DK, OT>), dim3((unsigned)(p.slots * a.v_heads)), dim3(kPrepThreads), 0, s, p);
+    if (wide) launch_walk<IN, O, DK, 2>(p, s);
+    else launch_walk<IN, O, DK, 1>(p, s);
+    return hipGetLastError();
+  };
+  // 1024 waves occupy every SIMD: more sequences than that share their operands between 32 columns
+  const auto wide = [&](int64_t seqs) { return seqs * a.v_heads * (a.dv / 32) >= 1024; };
+  const int64_t all = a.tokens / kChunk + a.seqs;
+  if (all * p.unit_bytes <= a.workspace_bytes) {
+    p.whole = 1, p.last = 1, p.slots = all, p.nseq = (int)a.seqs, p.chunks = 1 << 24;
+    return run(wide(a.seqs));
+  }
+  // In groups of sequences and, within a group, in runs of chunks: at least 16 at a time if one sequence's fit
+  const int64_t state = (int64_t)a.v_heads * DK * a.dv * 4;
+  const int64_t need = (longest(a.tokens, a.max_len) + kChunk - 1) / kChunk;
+  const int64_t nseq = std::max<int64_t>(1, std::min(a.seqs, a.workspace_bytes / (std::min<int64_t>(16, need) * p.unit_bytes + state)));
+  p.chunks = (int)std::min(need, (a.workspace_bytes / nseq - state) / p.unit_bytes);
+  p.carry = reinterpret_cast<float*>(p.units + nseq * p.chunks * p.unit_bytes);
+  for (p.seq0 = 0; p.seq0 < a.seqs; p.seq0 += nseq) {
+    p.nseq = (int)std::min(nseq, a.seqs - p.seq0);
+    p.slots = (int64_t)p.nseq * p.chunks;
+    for (int64_t c = 0; c < need; c += p.chunks) {
+      p.chunk0 = (int)c, p.last = c + p.chunks >= need;
+      const hipError_t e = run(wide(p.nseq));
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+template <typename IN, typename O>
+hipError_t launch_dk(const tq_gdn_args& a, hipStream_t s) {
+  return a.dk == 64 ? launch_all<IN, O, 64>(a, s) : launch_all<IN, O, 128>(a, s);
+}
+
+}  // namespace
+
+bool gdn_chunked(int64_t tokens, int64_t seqs, int64_t max_len) {
+  return longest(tokens, max_len) >= kStepLen && tokens > seqs;
+}
+
+// Room for one launch, or kBudget; one chunk and one state at least, whatever the types and key heads.
+int64_t gdn_chunk_workspace_bytes(int64_t tokens, int64_t seqs, int64_t, int v_heads, int dk, int dv) {
+  const int64_t unit = unit_bytes(v_heads, v_heads, dk, 3, 3);
+  const int64_t least = unit + (int64_t)v_heads * dk * dv * 4;
+  return std::max(least, std::min((tokens / kChunk + seqs) * unit, kBudget));
+}
+
+hipError_t launch_gdn_chunk(const tq_gdn_args& a, hipStream_t s) {
+  switch (a.in_type) {
+    case TQ_F32: return launch_dk<float, float>(a, s);
+    case TQ_BF16: return a.out_type == TQ_F32 ? launch_dk<bf16, float>(a, s) : launch_dk<bf16, bf16>(a, s);
+    default: return a.out_type == TQ_F32 ? launch_dk<f16, float>(a, s) : launch_dk<f16, f16>(a, s);
+  }
+}
+
+}  // namespace tq

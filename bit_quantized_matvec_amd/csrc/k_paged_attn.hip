@@ -70,10 +70,6 @@ struct AttnParams {
   int group, page_shift, splits, slots;
 };
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-
 template <typename C>
 struct Half;
 template <>
@@ -109,20 +105,6 @@ __device__ inline u32x4 keep_keys(u32x4 x, int k, int begin, int end) {
   return x;
 }
 
-// The largest b with slot0(b) <= slot, slot0(b) = cu[b] * group / rows + b: sequence b's tiles of `rows` query rows are
-// slots slot0(b) and on.  64 candidates at a time.
-__device__ inline int find_seq(const int32_t* cu, int64_t seqs, int group, int rows, int64_t slot, int lane) {
-  int64_t lo = 0, n = seqs;
-  while (n > 1) {
-    const int64_t step = (n + 63) / 64, i = lo + lane * step;
-    const bool ok = lane * step < n && (int64_t)cu[i] * group / rows + i <= slot;
-    const int64_t last = max(1, __popcll(__ballot(ok))) - 1;
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return __builtin_amdgcn_readfirstlane((int)lo);
-}
-
 // What a workgroup computes: query rows row0 .. of sequence b for one key head, and which keys any of them sees.
 struct Tile {
   int64_t t0;       // first token of the sequence
@@ -145,7 +127,7 @@ __device__ inline Tile find_tile(const AttnParams& p, int64_t tile, int lane) {
     r.b = slot / ((p.group + ROWS - 1) / ROWS);
   }
   const SeqRange s = seq_range(a.cu, r.b, a.tokens, a.bad_flag);
-  const int64_t slot0 = a.cu ? (int64_t)a.cu[r.b] * p.group / ROWS + r.b : r.b * ((p.group + ROWS - 1) / ROWS);
+  const int64_t slot0 = a.cu ? first_slot(a.cu, r.b, p.group, ROWS) : r.b * ((p.group + ROWS - 1) / ROWS);
   const int64_t row0 = (slot - slot0) * ROWS, all = (int64_t)s.n * p.group;
   r.t0 = s.t0;
   r.row0 = (int)row0;
@@ -168,20 +150,6 @@ __device__ inline int page_of(const AttnParams& p, const Tile& t, int k) {
     return -1;
   }
   return pg;
-}
-
-// One 8-value slice of P as the terms that the second product takes.
-template <typename C, int TERMS>
-__device__ inline void terms_of(const float* p, Frag<C>* out) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float r = p[j];
-#pragma unroll
-    for (int t = 0; t < TERMS; ++t) {
-      out[t][j] = (C)r;
-      if (t + 1 < TERMS) r -= (float)out[t][j];
-    }
-  }
 }
 
 // acc += V P, where V values that are not finite reach the rows that see their keys and no other.
@@ -455,7 +423,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
       l += pr[j];
     }
     Frag<C> pt[TERMS];
-    terms_of<C, TERMS>(pr, pt);
+    split_terms<TERMS>(pr, pt);
     if (careful) {
       Frag<C> sf;
 #pragma unroll

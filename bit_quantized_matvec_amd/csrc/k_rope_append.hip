@@ -40,11 +40,6 @@ struct RopeParams {
   int page_shift;
 };
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
-  T v[N];
-};
-
 // true and the page, place of a token's slot, if it is to be stored
 __device__ inline bool slot_of(const RopeParams& p, int64_t slot, int64_t* page, int* at) {
   *page = slot >> p.page_shift;

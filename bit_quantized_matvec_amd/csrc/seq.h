@@ -17,6 +17,10 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s);
 
 int64_t gdn_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int v_heads, int dk, int dv);
 hipError_t launch_gdn(const tq_gdn_args& a, hipStream_t s);
+// k_gdn_chunk.hip: whether a call's longest sequence is worth chunks, and the call
+bool gdn_chunked(int64_t tokens, int64_t seqs, int64_t max_len);
+int64_t gdn_chunk_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int v_heads, int dk, int dv);
+hipError_t launch_gdn_chunk(const tq_gdn_args& a, hipStream_t s);
 
 inline int type_bytes(int t) { return t == TQ_F32 ? 4 : 2; }
 
@@ -52,6 +56,46 @@ __device__ inline float wave_max(float v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
   return v;
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+  T v[N];
+};
+
+// 8 fp32 values as TERMS fragments of a 16-bit type whose sum holds as many bits as the terms have together.
+template <int TERMS, typename FRAG>
+__device__ inline void split_terms(const float* p, FRAG* out) {
+  typedef __typeof__(FRAG{}[0]) C;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float r = p[j];
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      out[t][j] = (C)r;
+      if (t + 1 < TERMS) r -= (float)out[t][j];
+    }
+  }
+}
+
+// Tiles of `rows` rows over the sequences, `per` rows per token: sequence b's are the slots from cu[b] * per / rows + b on
+// (an upper bound for what the sequences before it need).  The largest b whose first slot is at most `slot`, 64 candidates
+// at a time.
+__device__ inline int64_t first_slot(const int32_t* cu, int64_t b, int per, int rows) { return (int64_t)cu[b] * per / rows + b; }
+__device__ inline int find_seq(const int32_t* cu, int64_t seqs, int per, int rows, int64_t slot, int lane) {
+  int64_t lo = 0, n = seqs;
+  while (n > 1) {
+    const int64_t step = (n + 63) / 64, i = lo + lane * step;
+    const bool ok = lane * step < n && first_slot(cu, i, per, rows) <= slot;
+    const int64_t last = max(1, __popcll(__ballot(ok))) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return __builtin_amdgcn_readfirstlane((int)lo);
 }
 #endif
 
