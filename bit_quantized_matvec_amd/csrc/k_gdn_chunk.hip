@@ -39,6 +39,7 @@
 // kStepLen tokens).
 #include <algorithm>
 
+#include "kernels.h"
 #include "seq.h"
 
 namespace tq {
@@ -54,11 +55,10 @@ constexpr float kLeastG = -1024.f;  // e^g is 0 in fp32 far above
 
 typedef bf16 frag __attribute__((ext_vector_type(8)));
 
-// Per chunk and value head.
+// Per chunk and value head.  beta is NaN in a chunk that is to be walked.  decay is one value, repeated: as a value that
+// all lanes share the compiler would move it to a scalar register, and wait for it, right after its load.
 struct Scalars {
-  float beta[kChunk], far_k[kChunk], far_q[kChunk], last_k[kChunk];
-  float decay;
-  int odd;
+  float beta[kChunk], far_k[kChunk], far_q[kChunk], last_k[kChunk], decay[kChunk];
 };
 static_assert(sizeof(Scalars) <= kScalarBytes, "");
 
@@ -178,10 +178,7 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
     }
   }
   odd = __syncthreads_or(odd);
-  if (odd) {  // the walk will not look at anything else
-    if (tid == 0) sc->odd = 1;
-    // the other heads' chunks may still want K, Q and K^T: a chunk that is odd by its beta or g alone
-  }
+  if (odd && g == 0) sc->beta[i] = NAN;  // K, Q and K^T are still written: other heads may be odd in nothing
   const double mine = sums[i];
 #pragma unroll 1
   for (int s2 = 0; s2 <= wave >> 1; ++s2) {
@@ -251,8 +248,8 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
     sc->far_k[i] = beta * far * nk;
     sc->far_q[i] = far * nq;
     sc->last_k[i] = expf((float)(all - mine)) * nk;
+    sc->decay[i] = expf((float)all);
   }
-  if (tid == 0) sc->decay = expf((float)all), sc->odd = 0;
 
   // T: the diagonal blocks of 16 by substitution, one column per lane ...
   for (int k = tid; k < kChunk * W; k += kPrepThreads) (&T[0][0])[k] = 0.f;
@@ -317,56 +314,49 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
 
 // ---- the walk over the chunks --------------------------------------------------------------------------------------
 
-// Tokens [t, end) one after another, on the state that lane (n, g) holds: rows 32s + 8g + j of column n (NT columns 16
-// apart).
-template <typename IN, typename O, int DK, int NT>
-__device__ __forceinline__ void walk(const tq_gdn_args& a, int64_t t, int64_t end, int h, int col, f32x4 (&s)[NT][DK / 16]) {
-  constexpr int KS = DK / 32;
-  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int kh = h / (a.v_heads / a.k_heads);
-#pragma unroll 1
-  for (; t < end; ++t) {
-    const IN* qp = static_cast<const IN*>(a.q) + t * a.q_token + kh * a.q_head + 8 * g;
-    const IN* kp = static_cast<const IN*>(a.k) + t * a.k_token + kh * a.k_head + 8 * g;
-    const IN* vp = static_cast<const IN*>(a.v) + t * a.v_token + h * a.v_head + col + n;
-    float q[KS * 8], k[KS * 8], qq = 0.f, kk = 0.f, kq = 0.f;
-#pragma unroll
-    for (int x = 0; x < KS; ++x) load8(qp + 32 * x, q + 8 * x), load8(kp + 32 * x, k + 8 * x);
-#pragma unroll
-    for (int x = 0; x < KS * 8; ++x) qq = fmaf(q[x], q[x], qq), kk = fmaf(k[x], k[x], kk), kq = fmaf(k[x], q[x], kq);
-    float r1[NT] = {}, r2[NT] = {};
-#pragma unroll
-    for (int m = 0; m < NT; ++m)
-#pragma unroll
-      for (int x = 0; x < KS * 8; ++x) {
-        const float v = s[m][x >> 2][x & 3];
-        r1[m] = fmaf(v, k[x], r1[m]), r2[m] = fmaf(v, q[x], r2[m]);
-      }
-#pragma unroll
-    for (int o = 16; o < 64; o <<= 1) {
-      qq += __shfl_xor(qq, o, 64), kk += __shfl_xor(kk, o, 64), kq += __shfl_xor(kq, o, 64);
-#pragma unroll
-      for (int m = 0; m < NT; ++m) r1[m] += __shfl_xor(r1[m], o, 64), r2[m] += __shfl_xor(r2[m], o, 64);
-    }
-    const float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f;
-    const float decay = expf(a.g[t * a.v_heads + h]), beta = a.beta[t * a.v_heads + h];
-#pragma unroll
-    for (int m = 0; m < NT; ++m) {
-      const float d = beta * ((float)vp[16 * m] - decay * (r1[m] * nk));
-      const float o = fmaf(kq * nq * nk, d, decay * (r2[m] * nq));
-#pragma unroll
-      for (int x = 0; x < KS * 8; ++x) s[m][x >> 2][x & 3] = fmaf(k[x] * nk, d, decay * s[m][x >> 2][x & 3]);
-      if (g == 0) static_cast<O*>(a.out)[(t * a.v_heads + h) * a.dv + col + 16 * m + n] = (O)o;
-    }
-  }
+constexpr int kWalkThreads = 256;
+
+// Waits for this wave's LDS traffic alone: loads from memory stay in flight across it.
+__device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+typedef bf16 half_frag __attribute__((ext_vector_type(4)));
+template <int TERMS>
+__device__ inline void split4(f32x4 v, half_frag* out) {
+  const float x[4] = {v[0], v[1], v[2], v[3]};
+  split_terms<TERMS>(x, out);
 }
 
-template <typename IN, typename O, int DK, int NT>
-__global__ __launch_bounds__(64, 1) void gdn_walk_kernel(ChunkParams p) {
-  constexpr int KS = DK / 32, TK = terms_in<IN>(), OT = sizeof(O) == 4 ? 3 : 2;
+// A value as it is loaded, and as a number: 16 bits wait in a register of their own until they are needed.
+template <typename IN>
+struct Raw {
+  typedef unsigned short mem;
+  typedef unsigned type;
+  static __device__ float number(unsigned x) { return (float)__builtin_bit_cast(IN, (unsigned short)x); }
+};
+template <>
+struct Raw<float> {
+  typedef float mem, type;
+  static __device__ float number(float x) { return x; }
+};
+
+// Stores that drop what lies past the `bytes` from `base` on.
+__device__ inline void put_out(__amdgpu_buffer_rsrc_t r, int at, float v) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at * 4, 0, 0); }
+template <typename C>
+__device__ inline void put_out(__amdgpu_buffer_rsrc_t r, int at, C v) {
+  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, at * 2, 0, 0);
+}
+__device__ inline void in_order() { asm volatile("" ::: "memory"); }  // loads before it are issued before it
+
+template <typename IN, typename O, int DK>
+__global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p) {
+  constexpr int KS = DK / 32, HT = KS / 2, TK = terms_in<IN>(), OT = sizeof(O) == 4 ? 3 : 2;
+  // right operands: the state, R, X and X with the decays to the chunk's end
+  __shared__ __attribute__((aligned(16))) frag sf[KS][2][3][64], rf[2][2][3][64], zf[2][2][3][64], yf[2][2][OT][64];
+  __shared__ __attribute__((aligned(16))) float sums[2][4][2][32], norms[2][4][4];
+  __shared__ int odds[4];
   const auto& a = p.a;
-  const int lane = threadIdx.x, n = lane & 15, g = lane >> 4;
-  const int slices = a.dv / (16 * NT);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  const int slices = a.dv / 32;
   // Slices of a head read the same operands, heads of a group the same K and Q: they share an XCD (workgroups go round the
   // 8 of them), unless that left XCDs without work.
   const int group = a.v_heads / a.k_heads, together = (int64_t)p.nseq * a.k_heads >= 8 ? group : 1;
@@ -374,9 +364,8 @@ __global__ __launch_bounds__(64, 1) void gdn_walk_kernel(ChunkParams p) {
   const int in = blockIdx.x / 8 % (slices * together);
   const int64_t head = x * together + in / slices;
   if (head >= (int64_t)p.nseq * a.v_heads) return;
-  const int col = in % slices * (16 * NT), h = (int)(head % a.v_heads);
+  const int col = in % slices * 32, h = (int)(head % a.v_heads), kh = h / group;
   const int64_t b = p.seq0 + head / a.v_heads;
-  const int kh = h / group;
 
   const SeqRange r = seq_range(a.cu, b, a.tokens, a.bad_flag);
   const bool first = p.chunk0 == 0;
@@ -387,174 +376,308 @@ __global__ __launch_bounds__(64, 1) void gdn_walk_kernel(ChunkParams p) {
   if (slot >= a.states) raise_flag(a.bad_flag);
   const bool ends = p.last || from + (int64_t)p.chunks * kChunk >= r.n;
 
-  f32x4 s[NT][2 * KS];
+  // Wave w has tiles w * HT .. of the state's rows and tile w of a chunk's tokens.
+  f32x4 s[HT][2];
   float* carry = p.carry ? p.carry + ((b - p.seq0) * a.v_heads + h) * DK * (int64_t)a.dv : nullptr;
   const int64_t state_at = ((kept ? slot : 0) * a.v_heads + h) * DK * (int64_t)a.dv;
-  const int cell = 8 * g * a.dv + col + n;
+  auto row_of = [&](int e) { return 32 * ((wave * HT + e) >> 1) + 8 * g + 4 * ((wave * HT + e) & 1); };  // 4 rows from there
   {
     const float* src = first ? a.state + state_at : carry;
     const bool there = !first || kept;
 #pragma unroll
-    for (int m = 0; m < NT; ++m)
+    for (int e = 0; e < HT; ++e)
 #pragma unroll
-      for (int t = 0; t < 2 * KS; ++t)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[m][t][j] = there ? src[cell + (32 * (t >> 1) + 4 * (t & 1) + j) * a.dv + 16 * m] : 0.f;
+        for (int j = 0; j < 4; ++j) s[e][m][j] = there ? src[(row_of(e) + j) * a.dv + col + 16 * m + n] : 0.f;
   }
 
-  int64_t done = r.n < kStepLen ? 0 : from;
-  if (r.n >= kStepLen) {
-    const int64_t stop = ends && !p.last ? r.n : min((int64_t)r.n, from + (int64_t)p.chunks * kChunk);
-    for (; done < stop; done += kChunk) {
-      const int64_t c = done / kChunk;
-      const int len = (int)min((int64_t)kChunk, r.n - done);
-      const uint8_t* unit = p.units + (p.whole ? r.t0 / kChunk + b + c : (b - p.seq0) * p.chunks + c - p.chunk0) * p.unit_bytes;
-      const uint8_t* keys = unit + (int64_t)kh * (key_frags(DK, TK) * kFragBytes) + lane * 16;
-      const uint8_t* tri = unit + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
-      const Scalars* sc = reinterpret_cast<const Scalars*>(tri + tri_frags(3 + OT) * kFragBytes);
-      tri += lane * 16;
-      auto get = [&](const uint8_t* at, int index) { return *reinterpret_cast<const frag*>(at + index * kFragBytes); };
-      const IN* vp = static_cast<const IN*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
-      float v[NT][4][4];  // tokens place(t, 4g + j)
-      bool odd = sc->odd != 0;
+  // Tokens [t, end) one after another.
+  int parity = 0;
+  auto walk = [&](int64_t t, int64_t end) {
+#pragma unroll 1
+    for (; t < end; ++t, parity ^= 1) {
+      const IN* qp = static_cast<const IN*>(a.q) + t * a.q_token + kh * a.q_head;
+      const IN* kp = static_cast<const IN*>(a.k) + t * a.k_token + kh * a.k_head;
+      const IN* vp = static_cast<const IN*>(a.v) + t * a.v_token + h * a.v_head + col + n;
+      float q[HT][4], k[HT][4], qq = 0.f, kk = 0.f, kq = 0.f, r1[2] = {}, r2[2] = {};
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int e = 0; e < HT; ++e) {
+        const Vec<IN, 4> qi = *reinterpret_cast<const Vec<IN, 4>*>(qp + row_of(e)), ki = *reinterpret_cast<const Vec<IN, 4>*>(kp + row_of(e));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + j;
+          const float x = q[e][j] = (float)qi.v[j], y = k[e][j] = (float)ki.v[j];
+          qq = fmaf(x, x, qq), kk = fmaf(y, y, kk), kq = fmaf(x, y, kq);
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            v[m][t][j] = row < len ? (float)vp[row * a.v_token + 16 * m] : 0.f;
-            odd = odd || !(fabsf(v[m][t][j]) < INFINITY);
-          }
+          for (int m = 0; m < 2; ++m) r1[m] = fmaf(s[e][m][j], y, r1[m]), r2[m] = fmaf(s[e][m][j], x, r2[m]);
         }
-      if (__any(odd)) {
-        walk<IN, O, DK, NT>(a, r.t0 + done, r.t0 + done + len, h, col, s);
-        continue;
       }
-      frag sf[NT][KS][3];
 #pragma unroll
-      for (int m = 0; m < NT; ++m)
+      for (int o = 16; o < 64; o <<= 1) {
+        qq += __shfl_xor(qq, o, 64), kk += __shfl_xor(kk, o, 64), kq += __shfl_xor(kq, o, 64);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) split_terms<3>(reinterpret_cast<const float*>(&s[m][2 * k]), sf[m][k]);
-      // R = beta V - far_k (K S)
-      frag rf[NT][2][3];
-      {
-        f32x4 acc[NT][4] = {};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            frag kf[TK];
-#pragma unroll
-            for (int e = 0; e < TK; ++e) kf[e] = get(keys, (t * KS + k) * TK + e);
-#pragma unroll
-            for (int m = 0; m < NT; ++m) acc[m][t] = mma_terms<TK, 3>(kf, sf[m][k], acc[m][t]);
-          }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
-          const f32x4 be = *reinterpret_cast<const f32x4*>(sc->beta + row), fk = *reinterpret_cast<const f32x4*>(sc->far_k + row);
-#pragma unroll
-          for (int m = 0; m < NT; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[m][t][j] = fmaf(be[j], v[m][t][j], -fk[j] * acc[m][t][j]);
-        }
-#pragma unroll
-        for (int m = 0; m < NT; ++m)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) split_terms<3>(reinterpret_cast<const float*>(&acc[m][2 * k]), rf[m][k]);
+        for (int m = 0; m < 2; ++m) r1[m] += __shfl_xor(r1[m], o, 64), r2[m] += __shfl_xor(r2[m], o, 64);
       }
-      // X = T R
-      f32x4 y[NT][4] = {};
+      if (g == 0)
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+        for (int m = 0; m < 2; ++m) sums[parity][wave][0][16 * m + n] = r1[m], sums[parity][wave][1][16 * m + n] = r2[m];
+      if (lane == 0) norms[parity][wave][0] = qq, norms[parity][wave][1] = kk, norms[parity][wave][2] = kq;
+      lds_barrier();
+      auto total = [](const float* x, int step) { return (x[0] + x[step]) + (x[2 * step] + x[3 * step]); };
+      qq = total(&norms[parity][0][0], 4), kk = total(&norms[parity][0][1], 4), kq = total(&norms[parity][0][2], 4);
+      const float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f;
+      const float decay = expf(a.g[t * a.v_heads + h]), beta = a.beta[t * a.v_heads + h];
 #pragma unroll
-        for (int k = 0; k <= t >> 1; ++k) {
-          frag tf[3];
+      for (int m = 0; m < 2; ++m) {
+        const float s1 = total(&sums[parity][0][0][16 * m + n], 64) * nk, s2 = total(&sums[parity][0][1][16 * m + n], 64) * nq;
+        const float d = beta * ((float)vp[16 * m] - decay * s1);
+        if (wave == 0 && g == 0) static_cast<O*>(a.out)[(t * a.v_heads + h) * a.dv + col + 16 * m + n] = (O)fmaf(kq * nq * nk, d, decay * s2);
 #pragma unroll
-          for (int e = 0; e < 3; ++e) tf[e] = get(tri, tri_at(t, k) * 3 + e);
+        for (int e = 0; e < HT; ++e)
 #pragma unroll
-          for (int m = 0; m < NT; ++m) y[m][t] = mma_terms<3, 3>(tf, rf[m][k], y[m][t]);
-        }
-      // out = far_q (Q S) + P X
-      f32x4 o[NT][4] = {};
+          for (int j = 0; j < 4; ++j) s[e][m][j] = fmaf(k[e][j] * nk, d, decay * s[e][m][j]);
+      }
+    }
+  };
+  auto half = [&](frag* f, int c) -> half_frag* { return reinterpret_cast<half_frag*>(f + lane) + c; };
+  auto put_state = [&]() {
+#pragma unroll
+    for (int e = 0; e < HT; ++e)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int t = wave * HT + e;
+        half_frag f[3];
+        split4<3>(s[e][m], f);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *half(sf[t >> 1][m][i], t & 1) = f[i];
+      }
+  };
+
+  int64_t done = r.n < kStepLen ? 0 : from;
+  const int64_t stop = r.n < kStepLen ? 0 : min((int64_t)r.n, from + (int64_t)p.chunks * kChunk);
+  if (done < stop) {
+    const int s2 = wave >> 1, c2 = wave & 1, row = 32 * s2 + 8 * g + 4 * c2;  // of this wave's tokens, 4 from there
+    const uint8_t* keys = p.units + (p.whole ? r.t0 / kChunk + b + done / kChunk : (b - p.seq0) * p.chunks) * p.unit_bytes;
+    const uint8_t* tri = keys + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
+    keys += (int64_t)kh * (key_frags(DK, TK) * kFragBytes);
+    typedef typename Raw<IN>::mem mem;
+    const mem* vp = static_cast<const mem*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
+
+    // What a wave takes from memory for a chunk; each part is asked for again, for the next chunk, after its last use.
+    frag kf[KS][TK], qf[KS][TK], xf[HT][2][TK], tf[2][3], pf[2][OT];
+    f32x4 be, fk, fq, lk;
+    typename Raw<IN>::type v[2][4];
+    float decay;
+    auto get = [&](const uint8_t* at, int index) { return *reinterpret_cast<const frag*>(at + index * kFragBytes + lane * 16); };
+    auto scalars = [&]() { return reinterpret_cast<const Scalars*>(tri + tri_frags(3 + OT) * kFragBytes); };
+    auto load_kq = [&](int len) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          frag qf[TK];
-#pragma unroll
-          for (int e = 0; e < TK; ++e) qf[e] = get(keys + 4 * KS * TK * kFragBytes, (t * KS + k) * TK + e);
-#pragma unroll
-          for (int m = 0; m < NT; ++m) o[m][t] = mma_terms<TK, OT>(qf, sf[m][k], o[m][t]);
+        for (int e = 0; e < TK; ++e) {
+          kf[k][e] = get(keys, (wave * KS + k) * TK + e);
+          qf[k][e] = get(keys + 4 * KS * TK * kFragBytes, (wave * KS + k) * TK + e);
         }
-      frag yf[NT][2][OT], zf[NT][2][3];
 #pragma unroll
-      for (int m = 0; m < NT; ++m)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) split_terms<OT>(reinterpret_cast<const float*>(&y[m][2 * k]), yf[m][k]);
+        for (int m = 0; m < 2; ++m) v[m][j] = vp[min(row + j, len - 1) * a.v_token + 16 * m];
+      be = *reinterpret_cast<const f32x4*>(scalars()->beta + row), fk = *reinterpret_cast<const f32x4*>(scalars()->far_k + row);
+    };
+    auto load_t = [&]() {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
-        const f32x4 fq = *reinterpret_cast<const f32x4*>(sc->far_q + row), lk = *reinterpret_cast<const f32x4*>(sc->last_k + row);
+      for (int k = 0; k < 2; ++k)  // (the second k of the upper tiles is not used: loading it keeps the count of loads)
 #pragma unroll
-        for (int m = 0; m < NT; ++m)
+        for (int e = 0; e < 3; ++e) tf[k][e] = get(tri, tri_at(wave, min(k, s2)) * 3 + e);
+      lk = *reinterpret_cast<const f32x4*>(scalars()->last_k + row);
+    };
+    auto load_x = [&]() {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[m][t][j] *= fq[j], y[m][t][j] *= lk[j];
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < TK; ++e) xf[t][k][e] = get(keys + 8 * KS * TK * kFragBytes, ((wave * HT + t) * 2 + k) * TK + e);
+      decay = scalars()->decay[row];
+    };
+    auto load_p = [&]() {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < OT; ++e) pf[k][e] = get(tri + tri_frags(3) * kFragBytes, tri_at(wave, min(k, s2)) * OT + e);
+      fq = *reinterpret_cast<const f32x4*>(scalars()->far_q + row);
+    };
+    int len = (int)min((int64_t)kChunk, stop - done);
+    load_kq(len);
+    load_t();
+    load_x();
+    load_p();
+    put_state();
+    lds_barrier();
+#pragma unroll 1
+    for (; done < stop; done += kChunk) {
+      const int now = len;
+      if (done + kChunk < stop) {  // the next chunk's places (the last chunk's are asked for twice)
+        len = (int)min((int64_t)kChunk, stop - done - kChunk);
+        keys += p.unit_bytes, tri += p.unit_bytes, vp += kChunk * a.v_token;
       }
+      // K S and Q S: each operand is read while the one before it is multiplied
+      f32x4 o[2] = {}, y[2] = {};
+      {
+        frag f[2][2][3];
+        auto read = [&](int k) {
 #pragma unroll
-      for (int m = 0; m < NT; ++m)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) split_terms<3>(reinterpret_cast<const float*>(&y[m][2 * k]), zf[m][k]);
+            for (int e = 0; e < 3; ++e) f[k & 1][m][e] = sf[k][m][e][lane];
+        };
+        read(0);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+        for (int k = 0; k < KS; ++k) {
+          if (k + 1 < KS) read(k + 1);
+          in_order();
 #pragma unroll
-        for (int k = 0; k <= t >> 1; ++k) {
-          frag pf[OT];
+          for (int i = 0; i < TK; ++i)
 #pragma unroll
-          for (int e = 0; e < OT; ++e) pf[e] = get(tri + tri_frags(3) * kFragBytes, tri_at(t, k) * OT + e);
+            for (int e = 0; e < 3; ++e)
 #pragma unroll
-          for (int m = 0; m < NT; ++m) o[m][t] = mma_terms<OT, OT>(pf, yf[m][k], o[m][t]);
-        }
-      // S = decay S + K^T Z
-      const float decay = sc->decay;
-#pragma unroll
-      for (int t = 0; t < 2 * KS; ++t) {
-#pragma unroll
-        for (int m = 0; m < NT; ++m) s[m][t] *= decay;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          frag kt[TK];
-#pragma unroll
-          for (int e = 0; e < TK; ++e) kt[e] = get(keys + 8 * KS * TK * kFragBytes, (t * 2 + k) * TK + e);
-#pragma unroll
-          for (int m = 0; m < NT; ++m) s[m][t] = mma_terms<TK, 3>(kt, zf[m][k], s[m][t]);
+              for (int m = 0; m < 2; ++m) {
+                if (i + e < 3) y[m] = mma(kf[k][i], f[k & 1][m][e], y[m]);
+                if (i + e < 3 && e < OT) o[m] = mma(qf[k][i], f[k & 1][m][e], o[m]);
+              }
         }
       }
-      O* op = static_cast<O*>(a.out) + ((r.t0 + done) * a.v_heads + h) * a.dv + col + n;
+      // R = beta V - far_k (K S)
+      bool bad = false;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int m = 0; m < 2; ++m) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + j;
-          if (row < len)
-#pragma unroll
-            for (int m = 0; m < NT; ++m) op[(int64_t)row * a.v_heads * a.dv + 16 * m] = (O)o[m][t][j];
+          const float vj = row + j < now ? Raw<IN>::number(v[m][j]) : 0.f;
+          bad = bad || !(fabsf(vj) < INFINITY) || !(fabsf(be[j]) < INFINITY);
+          y[m][j] = fmaf(be[j], vj, -fk[j] * y[m][j]);
+          o[m][j] *= fq[j];
         }
+        half_frag f[3];
+        split4<3>(y[m], f);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) *half(rf[s2][m][e], c2) = f[e];
+      }
+      bad = __any(bad);
+      if (lane == 0) odds[wave] = bad;
+      load_kq(len);
+      lds_barrier();
+      if (__builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3])) {
+        walk(r.t0 + done, r.t0 + done + now);
+        put_state();
+        load_t();
+        load_x();
+        load_p();
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // all of them: or the other way's waits are counted from here too
+        lds_barrier();
+        continue;
+      }
+      // X = T R
+      f32x4 y2[2] = {};
+      {
+        frag f[2][2][3];
+        auto read = [&](int k) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 3; ++e) f[k][m][e] = rf[k][m][e][lane];
+        };
+        auto product = [&](int k) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              y[m] = mma(tf[k][e], f[k][m][0], y[m]);
+              y2[m] = mma(tf[k][e == 2 ? 0 : e], f[k][m][e == 2 ? 2 : 1], y2[m]);
+            }
+        };
+#pragma unroll
+        for (int m = 0; m < 2; ++m) y[m] = f32x4{};
+        read(0);
+        if (s2) read(1);
+        in_order();
+        product(0);
+        if (s2) product(1);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        y[m] += y2[m];
+        half_frag f[3];
+        split4<3>(y[m] * lk, f);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) *half(zf[s2][m][e], c2) = f[e];
+        split4<OT>(y[m], f);
+#pragma unroll
+        for (int e = 0; e < OT; ++e) *half(yf[s2][m][e], c2) = f[e];
+      }
+      load_t();
+      lds_barrier();
+      // S = decay S + K^T Z
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) s[t][m] *= decay;
+      {
+        frag f[2][2][3];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 3; ++e) f[k][m][e] = zf[k][m][e][lane];
+        in_order();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < TK; ++i)
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+#pragma unroll
+              for (int t = 0; t < HT; ++t)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                  if (i + e < 3) s[t][m] = mma(xf[t][k][i], f[k][m][e], s[t][m]);
+      }
+      put_state();
+      load_x();
+      // out = far_q (Q S) + P X
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (k <= s2)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            frag f[OT];
+#pragma unroll
+            for (int e = 0; e < OT; ++e) f[e] = yf[k][m][e][lane];
+            o[m] = mma_terms<OT, OT>(pf[k], f, o[m]);
+          }
+      load_p();
+      const auto op = __builtin_amdgcn_make_buffer_rsrc(static_cast<O*>(a.out) + (r.t0 + done) * a.v_heads * a.dv, 0,
+                                                        now * a.v_heads * a.dv * (int)sizeof(O), 0x00027000);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) put_out(op, ((row + j) * a.v_heads + h) * a.dv + col + 16 * m + n, (O)o[m][j]);
+      lds_barrier();
     }
+    done = stop;
   }
   // sequences too short for chunks, and what a wrong max_len left over
-  if (ends && done < r.n) walk<IN, O, DK, NT>(a, r.t0 + done, r.t0 + r.n, h, col, s);
+  if (ends && done < r.n) walk(r.t0 + done, r.t0 + r.n);
 
   if (ends && (!kept || (r.n == 0 && a.state_out == a.state))) return;
   float* dst = ends ? a.state_out + state_at : carry;
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
+  for (int e = 0; e < HT; ++e)
 #pragma unroll
-    for (int t = 0; t < 2 * KS; ++t)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[cell + (32 * (t >> 1) + 4 * (t & 1) + j) * a.dv + 16 * m] = s[m][t][j];
+      for (int j = 0; j < 4; ++j) dst[(row_of(e) + j) * a.dv + col + 16 * m + n] = s[e][m][j];
 }
 
 // ---- host ----------------------------------------------------------------------------------------------------------
@@ -564,12 +687,12 @@ int64_t unit_bytes(int k_heads, int v_heads, int dk, int tk, int ot) {
 }
 int64_t longest(int64_t tokens, int64_t max_len) { return max_len > 0 ? std::min(max_len, tokens) : tokens; }
 
-template <typename IN, typename O, int DK, int NT>
+template <typename IN, typename O, int DK>
 void launch_walk(const ChunkParams& p, hipStream_t s) {
-  const int group = p.a.v_heads / p.a.k_heads, slices = p.a.dv / (16 * NT);
+  const int group = p.a.v_heads / p.a.k_heads, slices = p.a.dv / 32;
   const int64_t heads = (int64_t)p.nseq * p.a.v_heads, together = (int64_t)p.nseq * p.a.k_heads >= 8 ? group : 1;
   const int64_t blocks = (heads / together + 7) / 8 * 8 * together * slices;
-  hipLaunchKernelGGL((gdn_walk_kernel<IN, O, DK, NT>), dim3((unsigned)blocks), dim3(64), 0, s, p);
+  hipLaunchKernelGGL((gdn_walk_kernel<IN, O, DK>), dim3((unsigned)blocks), dim3(kWalkThreads), 0, s, p);
 }
 
 template <typename IN, typename O, int DK>
@@ -578,18 +701,15 @@ hipError_t launch_all(const tq_gdn_args& a, hipStream_t s) {
   ChunkParams p{a};
   p.unit_bytes = unit_bytes(a.k_heads, a.v_heads, DK, terms_in<IN>(), OT);
   p.units = static_cast<uint8_t*>(a.workspace);
-  auto run = [&](bool wide) {
+  auto run = [&]() {
     hipLaunchKernelGGL((gdn_prepare_kernel<IN, DK, OT>), dim3((unsigned)(p.slots * a.v_heads)), dim3(kPrepThreads), 0, s, p);
-    if (wide) launch_walk<IN, O, DK, 2>(p, s);
-    else launch_walk<IN, O, DK, 1>(p, s);
+    launch_walk<IN, O, DK>(p, s);
     return hipGetLastError();
   };
-  // 1024 waves occupy every SIMD: more sequences than that share their operands between 32 columns
-  const auto wide = [&](int64_t seqs) { return seqs * a.v_heads * (a.dv / 32) >= 1024; };
   const int64_t all = a.tokens / kChunk + a.seqs;
   if (all * p.unit_bytes <= a.workspace_bytes) {
     p.whole = 1, p.last = 1, p.slots = all, p.nseq = (int)a.seqs, p.chunks = 1 << 24;
-    return run(wide(a.seqs));
+    return run();
   }
   // In groups of sequences and, within a group, in runs of chunks: at least 16 at a time if one sequence's fit
   const int64_t state = (int64_t)a.v_heads * DK * a.dv * 4;
@@ -602,7 +722,7 @@ hipError_t launch_all(const tq_gdn_args& a, hipStream_t s) {
     p.slots = (int64_t)p.nseq * p.chunks;
     for (int64_t c = 0; c < need; c += p.chunks) {
       p.chunk0 = (int)c, p.last = c + p.chunks >= need;
-      const hipError_t e = run(wide(p.nseq));
+      const hipError_t e = run();
       if (e != hipSuccess) return e;
     }
   }

@@ -67,19 +67,46 @@ struct alignas(sizeof(T) * N) Vec {
   T v[N];
 };
 
-// 8 fp32 values as TERMS fragments of a 16-bit type whose sum holds as many bits as the terms have together.
-template <int TERMS, typename FRAG>
-__device__ inline void split_terms(const float* p, FRAG* out) {
-  typedef __typeof__(FRAG{}[0]) C;
+// Two fp32 values rounded to a 16-bit type, and back.
+template <typename C>
+__device__ inline unsigned pack2(float x, float y) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef C c2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x, y}), c2));
+}
+template <typename C>
+__device__ inline void unpack2(unsigned u, float* x, float* y) {
+  if constexpr (__is_same(C, bf16)) {
+    *x = __uint_as_float(u << 16), *y = __uint_as_float(u & 0xFFFF0000u);
+  } else {
+    typedef C c2 __attribute__((ext_vector_type(2)));
+    const c2 v = __builtin_bit_cast(c2, u);
+    *x = (float)v[0], *y = (float)v[1];
+  }
+}
+
+// N fp32 values (a multiple of 2) as TERMS vectors of a 16-bit type whose sum holds as many bits as the terms have together.
+template <int TERMS, typename VEC>
+__device__ inline void split_terms(const float* p, VEC* out) {
+  typedef __typeof__(VEC{}[0]) C;
+  constexpr int N = sizeof(VEC) / 4;
+  typedef unsigned words __attribute__((ext_vector_type(N)));
+  words w[TERMS];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float r = p[j];
+  for (int i = 0; i < N; ++i) {
+    float x = p[2 * i], y = p[2 * i + 1];
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
-      out[t][j] = (C)r;
-      if (t + 1 < TERMS) r -= (float)out[t][j];
+      w[t][i] = pack2<C>(x, y);
+      if (t + 1 < TERMS) {
+        float u, v;
+        unpack2<C>(w[t][i], &u, &v);
+        x -= u, y -= v;
+      }
     }
   }
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) out[t] = __builtin_bit_cast(VEC, w[t]);
 }
 
 // Tiles of `rows` rows over the sequences, `per` rows per token: sequence b's are the slots from cu[b] * per / rows + b on
