@@ -38,6 +38,7 @@
 // g > 0 is walked token after token instead (as are sequences of less than
 // kStepLen tokens).
 #include <algorithm>
+#include <cstddef>
 
 #include "kernels.h"
 #include "seq.h"
@@ -367,7 +368,8 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
   const int col = in % slices * 32, h = (int)(head % a.v_heads), kh = h / group;
   const int64_t b = p.seq0 + head / a.v_heads;
 
-  const SeqRange r = seq_range(a.cu, b, a.tokens, a.bad_flag);
+  SeqRange r = seq_range(a.cu, b, a.tokens, a.bad_flag);
+  r.t0 = __builtin_amdgcn_readfirstlane((int)r.t0), r.n = __builtin_amdgcn_readfirstlane(r.n);  // for scalar addresses
   const bool first = p.chunk0 == 0;
   const int64_t from = (int64_t)p.chunk0 * kChunk;
   if (!first && from >= r.n) return;
@@ -455,11 +457,15 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
 
   int64_t done = r.n < kStepLen ? 0 : from;
   const int64_t stop = r.n < kStepLen ? 0 : min((int64_t)r.n, from + (int64_t)p.chunks * kChunk);
-  if (done < stop) {
+  while (true) {
+    // Chunks up to `stop`, or to one that has to be walked; then that, or the rest (sequences too short for chunks, and what
+    // a wrong max_len left over).
+    int64_t walk_to = ends ? r.n : done;
+    bool odd = false;
+    f32x4 before[HT][2];
+    if (done < stop) {
     const int s2 = wave >> 1, c2 = wave & 1, row = 32 * s2 + 8 * g + 4 * c2;  // of this wave's tokens, 4 from there
-    const uint8_t* keys = p.units + (p.whole ? r.t0 / kChunk + b + done / kChunk : (b - p.seq0) * p.chunks) * p.unit_bytes;
-    const uint8_t* tri = keys + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
-    keys += (int64_t)kh * (key_frags(DK, TK) * kFragBytes);
+    uint8_t* unit = p.units + (p.whole ? r.t0 / kChunk + b + done / kChunk : (b - p.seq0) * p.chunks + done / kChunk - p.chunk0) * p.unit_bytes;
     typedef typename Raw<IN>::mem mem;
     const mem* vp = static_cast<const mem*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
 
@@ -468,28 +474,43 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
     f32x4 be, fk, fq, lk;
     typename Raw<IN>::type v[2][4];
     float decay;
-    auto get = [&](const uint8_t* at, int index) { return *reinterpret_cast<const frag*>(at + index * kFragBytes + lane * 16); };
-    auto scalars = [&]() { return reinterpret_cast<const Scalars*>(tri + tri_frags(3 + OT) * kFragBytes); };
+    // Places in a chunk's unit are scalar offsets beside a lane's own: no vector arithmetic for addresses.
+    const int kq_at = kh * key_frags(DK, TK) * kFragBytes, tri_pos = (a.k_heads * key_frags(DK, TK) + h * tri_frags(3 + OT)) * kFragBytes + h * kScalarBytes;
+    const int p_at = tri_pos + tri_frags(3) * kFragBytes, sc_at = tri_pos + tri_frags(3 + OT) * kFragBytes;
+    const int tri1 = lane * 16 + (tri_at(wave, min(1, s2)) - tri_at(wave, 0)) * 3 * kFragBytes;  // (the upper tiles have no second one: the first again)
+    const int tri1p = lane * 16 + (tri_at(wave, min(1, s2)) - tri_at(wave, 0)) * OT * kFragBytes;
+    auto get = [&](int at, int index, int own) {
+      return __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), own,
+                                                                            at + index * kFragBytes, 0));
+    };
+    auto row4 = [&](int at) {
+      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), row * 4,
+                                                                             sc_at + at, 0));
+    };
+    int64_t v_at[4];
     auto load_kq = [&](int len) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < TK; ++e) {
-          kf[k][e] = get(keys, (wave * KS + k) * TK + e);
-          qf[k][e] = get(keys + 4 * KS * TK * kFragBytes, (wave * KS + k) * TK + e);
+          kf[k][e] = get(kq_at, (wave * KS + k) * TK + e, lane * 16);
+          qf[k][e] = get(kq_at + 4 * KS * TK * kFragBytes, (wave * KS + k) * TK + e, lane * 16);
         }
+      if (len < kChunk)  // rows past the end: the last one again
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v_at[j] = min(row + j, len - 1) * a.v_token;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) v[m][j] = vp[min(row + j, len - 1) * a.v_token + 16 * m];
-      be = *reinterpret_cast<const f32x4*>(scalars()->beta + row), fk = *reinterpret_cast<const f32x4*>(scalars()->far_k + row);
+        for (int m = 0; m < 2; ++m) v[m][j] = vp[v_at[j] + 16 * m];
+      be = row4(offsetof(Scalars, beta)), fk = row4(offsetof(Scalars, far_k));
     };
     auto load_t = [&]() {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)  // (the second k of the upper tiles is not used: loading it keeps the count of loads)
+      for (int k = 0; k < 2; ++k)  // (not used, but loaded, where there is no second one: the waits count loads)
 #pragma unroll
-        for (int e = 0; e < 3; ++e) tf[k][e] = get(tri, tri_at(wave, min(k, s2)) * 3 + e);
-      lk = *reinterpret_cast<const f32x4*>(scalars()->last_k + row);
+        for (int e = 0; e < 3; ++e) tf[k][e] = get(tri_pos, tri_at(wave, 0) * 3 + e, k ? tri1 : lane * 16);
+      lk = row4(offsetof(Scalars, last_k));
     };
     auto load_x = [&]() {
 #pragma unroll
@@ -497,29 +518,33 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int e = 0; e < TK; ++e) xf[t][k][e] = get(keys + 8 * KS * TK * kFragBytes, ((wave * HT + t) * 2 + k) * TK + e);
-      decay = scalars()->decay[row];
+          for (int e = 0; e < TK; ++e) xf[t][k][e] = get(kq_at + 8 * KS * TK * kFragBytes, ((wave * HT + t) * 2 + k) * TK + e, lane * 16);
+      decay = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), row * 4,
+                                                                   sc_at + (int)offsetof(Scalars, decay), 0));
     };
     auto load_p = [&]() {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < OT; ++e) pf[k][e] = get(tri + tri_frags(3) * kFragBytes, tri_at(wave, min(k, s2)) * OT + e);
-      fq = *reinterpret_cast<const f32x4*>(scalars()->far_q + row);
+        for (int e = 0; e < OT; ++e) pf[k][e] = get(p_at, tri_at(wave, 0) * OT + e, k ? tri1p : lane * 16);
+      fq = row4(offsetof(Scalars, far_q));
     };
     int len = (int)min((int64_t)kChunk, stop - done);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v_at[j] = (row + j) * a.v_token;
     load_kq(len);
     load_t();
     load_x();
     load_p();
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // or the loop's waits would count from here, in whatever order these were issued
     put_state();
     lds_barrier();
 #pragma unroll 1
-    for (; done < stop; done += kChunk) {
+    do {
       const int now = len;
       if (done + kChunk < stop) {  // the next chunk's places (the last chunk's are asked for twice)
         len = (int)min((int64_t)kChunk, stop - done - kChunk);
-        keys += p.unit_bytes, tri += p.unit_bytes, vp += kChunk * a.v_token;
+        unit += p.unit_bytes, vp += kChunk * a.v_token;
       }
       // K S and Q S: each operand is read while the one before it is multiplied
       f32x4 o[2] = {}, y[2] = {};
@@ -548,13 +573,14 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
         }
       }
       // R = beta V - far_k (K S)
-      bool bad = false;
+      float spoil = 0.f;  // NaN if anything is not finite
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float vj = row + j < now ? Raw<IN>::number(v[m][j]) : 0.f;
-          bad = bad || !(fabsf(vj) < INFINITY) || !(fabsf(be[j]) < INFINITY);
+          spoil = fmaf(vj, 0.f, spoil);
+          if (m == 0) spoil = fmaf(be[j], 0.f, spoil);
           y[m][j] = fmaf(be[j], vj, -fk[j] * y[m][j]);
           o[m][j] *= fq[j];
         }
@@ -563,20 +589,17 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
 #pragma unroll
         for (int e = 0; e < 3; ++e) *half(rf[s2][m][e], c2) = f[e];
       }
-      bad = __any(bad);
+      const bool bad = __any(spoil != 0.f);
       if (lane == 0) odds[wave] = bad;
       load_kq(len);
       lds_barrier();
-      if (__builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3])) {
-        walk(r.t0 + done, r.t0 + done + now);
-        put_state();
-        load_t();
-        load_x();
-        load_p();
-        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // all of them: or the other way's waits are counted from here too
-        lds_barrier();
-        continue;
-      }
+      // A chunk that has to be walked still goes on to the end of the loop's body, whose results are dropped: another way out
+      // would have the compiler move what is being loaded, and wait for it.
+      odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) before[t][m] = s[t][m];
       // X = T R
       f32x4 y2[2] = {};
       {
@@ -658,17 +681,29 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
           }
       load_p();
       const auto op = __builtin_amdgcn_make_buffer_rsrc(static_cast<O*>(a.out) + (r.t0 + done) * a.v_heads * a.dv, 0,
-                                                        now * a.v_heads * a.dv * (int)sizeof(O), 0x00027000);
+                                                        odd ? 0 : now * a.v_heads * a.dv * (int)sizeof(O), 0x00027000);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int m = 0; m < 2; ++m) put_out(op, ((row + j) * a.v_heads + h) * a.dv + col + 16 * m + n, (O)o[m][j]);
       lds_barrier();
+      done += kChunk;
+    } while (!odd && done < stop);
+    if (odd) {
+      done -= kChunk;
+      walk_to = min(done + kChunk, stop);
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) s[t][m] = before[t][m];
+    } else {
+      done = stop;
+      walk_to = ends ? r.n : stop;
     }
-    done = stop;
+    }
+    if (walk_to > done) walk(r.t0 + done, r.t0 + walk_to), done = walk_to;
+    if (!odd) break;
   }
-  // sequences too short for chunks, and what a wrong max_len left over
-  if (ends && done < r.n) walk(r.t0 + done, r.t0 + r.n);
 
   if (ends && (!kept || (r.n == 0 && a.state_out == a.state))) return;
   float* dst = ends ? a.state_out + state_at : carry;
