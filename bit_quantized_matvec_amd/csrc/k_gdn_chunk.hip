@@ -315,7 +315,7 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
 
 // ---- the walk over the chunks --------------------------------------------------------------------------------------
 
-constexpr int kWalkThreads = 256;
+constexpr int kWalkThreads = 512;
 
 // Waits for this wave's LDS traffic alone: loads from memory stay in flight across it.
 __device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -348,15 +348,21 @@ __device__ inline void put_out(__amdgpu_buffer_rsrc_t r, int at, C v) {
 }
 __device__ inline void in_order() { asm volatile("" ::: "memory"); }  // loads before it are issued before it
 
+// A workgroup has 32 columns of one head's state.  Four waves, one per SIMD, carry the recurrence from chunk to chunk; four
+// more, beside them, compute the outputs, which nothing waits for.  A chunk is three steps between barriers:
+//   1  K S, R            |  P X and the stores of the chunk before
+//   2  X = T R           |  Q S
+//   3  the next state    |  X as right operands of P X
 template <typename IN, typename O, int DK>
-__global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p) {
+__global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p) {
   constexpr int KS = DK / 32, HT = KS / 2, TK = terms_in<IN>(), OT = sizeof(O) == 4 ? 3 : 2;
-  // right operands: the state, R, X and X with the decays to the chunk's end
-  __shared__ __attribute__((aligned(16))) frag sf[KS][2][3][64], rf[2][2][3][64], zf[2][2][3][64], yf[2][2][OT][64];
-  __shared__ __attribute__((aligned(16))) float sums[2][4][2][32], norms[2][4][4];
-  __shared__ int odds[4];
+  // right operands: the state, R and X with the decays to the chunk's end; X itself, the 8 values of an operand's lane together
+  __shared__ __attribute__((aligned(16))) frag sf[KS][2][3][64], rf[2][2][3][64], zf[2][2][3][64];
+  __shared__ __attribute__((aligned(16))) float xs[2][2][64][8], sums[2][4][2][32], norms[2][4][4];
+  __shared__ __attribute__((aligned(16))) int odds[4];
   const auto& a = p.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = waves & 3, n = lane & 15, g = lane >> 4;
+  const bool carries = waves < 4;
   const int slices = a.dv / 32;
   // Slices of a head read the same operands, heads of a group the same K and Q: they share an XCD (workgroups go round the
   // 8 of them), unless that left XCDs without work.
@@ -378,25 +384,28 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
   if (slot >= a.states) raise_flag(a.bad_flag);
   const bool ends = p.last || from + (int64_t)p.chunks * kChunk >= r.n;
 
-  // Wave w has tiles w * HT .. of the state's rows and tile w of a chunk's tokens.
-  f32x4 s[HT][2];
+  // Wave w of either four has tiles w * HT .. of the state's rows and tile w of a chunk's tokens.
+  f32x4 s[HT][2] = {};
   float* carry = p.carry ? p.carry + ((b - p.seq0) * a.v_heads + h) * DK * (int64_t)a.dv : nullptr;
   const int64_t state_at = ((kept ? slot : 0) * a.v_heads + h) * DK * (int64_t)a.dv;
   auto row_of = [&](int e) { return 32 * ((wave * HT + e) >> 1) + 8 * g + 4 * ((wave * HT + e) & 1); };  // 4 rows from there
-  {
+  if (carries && (!first || kept)) {
     const float* src = first ? a.state + state_at : carry;
-    const bool there = !first || kept;
 #pragma unroll
     for (int e = 0; e < HT; ++e)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[e][m][j] = there ? src[(row_of(e) + j) * a.dv + col + 16 * m + n] : 0.f;
+        for (int j = 0; j < 4; ++j) s[e][m][j] = src[(row_of(e) + j) * a.dv + col + 16 * m + n];
   }
 
   // Tokens [t, end) one after another.
   int parity = 0;
   auto walk = [&](int64_t t, int64_t end) {
+    if (!carries) {
+      for (; t < end; ++t) lds_barrier();
+      return;
+    }
 #pragma unroll 1
     for (; t < end; ++t, parity ^= 1) {
       const IN* qp = static_cast<const IN*>(a.q) + t * a.q_token + kh * a.q_head;
@@ -462,250 +471,296 @@ __global__ __launch_bounds__(kWalkThreads, 1) void gdn_walk_kernel(ChunkParams p
     // a wrong max_len left over).
     int64_t walk_to = ends ? r.n : done;
     bool odd = false;
-    f32x4 before[HT][2];
     if (done < stop) {
-    const int s2 = wave >> 1, c2 = wave & 1, row = 32 * s2 + 8 * g + 4 * c2;  // of this wave's tokens, 4 from there
-    uint8_t* unit = p.units + (p.whole ? r.t0 / kChunk + b + done / kChunk : (b - p.seq0) * p.chunks + done / kChunk - p.chunk0) * p.unit_bytes;
-    typedef typename Raw<IN>::mem mem;
-    const mem* vp = static_cast<const mem*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
-
-    // What a wave takes from memory for a chunk; each part is asked for again, for the next chunk, after its last use.
-    frag kf[KS][TK], qf[KS][TK], xf[HT][2][TK], tf[2][3], pf[2][OT];
-    f32x4 be, fk, fq, lk;
-    typename Raw<IN>::type v[2][4];
-    float decay;
-    // Places in a chunk's unit are scalar offsets beside a lane's own: no vector arithmetic for addresses.
-    const int kq_at = kh * key_frags(DK, TK) * kFragBytes, tri_pos = (a.k_heads * key_frags(DK, TK) + h * tri_frags(3 + OT)) * kFragBytes + h * kScalarBytes;
-    const int p_at = tri_pos + tri_frags(3) * kFragBytes, sc_at = tri_pos + tri_frags(3 + OT) * kFragBytes;
-    const int tri1 = lane * 16 + (tri_at(wave, min(1, s2)) - tri_at(wave, 0)) * 3 * kFragBytes;  // (the upper tiles have no second one: the first again)
-    const int tri1p = lane * 16 + (tri_at(wave, min(1, s2)) - tri_at(wave, 0)) * OT * kFragBytes;
-    auto get = [&](int at, int index, int own) {
-      return __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), own,
-                                                                            at + index * kFragBytes, 0));
-    };
-    auto row4 = [&](int at) {
-      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), row * 4,
-                                                                             sc_at + at, 0));
-    };
-    int64_t v_at[4];
-    auto load_kq = [&](int len) {
+      const int s2 = wave >> 1, c2 = wave & 1, row = 32 * s2 + 8 * g + 4 * c2;  // of this wave's tokens, 4 from there
+      uint8_t* unit = p.units + (p.whole ? r.t0 / kChunk + b + done / kChunk : (b - p.seq0) * p.chunks + done / kChunk - p.chunk0) * p.unit_bytes;
+      // Places in a chunk's unit are scalar offsets beside a lane's own: no vector arithmetic for addresses.
+      const int kq_at = kh * key_frags(DK, TK) * kFragBytes;
+      const int t_at = (a.k_heads * key_frags(DK, TK) + h * tri_frags(3 + OT)) * kFragBytes + h * kScalarBytes;
+      const int p_at = t_at + tri_frags(3) * kFragBytes, sc_at = t_at + tri_frags(3 + OT) * kFragBytes;
+      const int second = s2 ? kFragBytes : 0;  // from a tile's first part of T or P, and per term, to its second (the upper tiles: the first again)
+      auto get = [&](int own, int at) {
+        return __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), own, at, 0));
+      };
+      auto row4 = [&](int at) {
+        return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000),
+                                                                               row * 4, sc_at + at, 0));
+      };
+      // Each role keeps what it takes from memory for a chunk in registers, and asks for a part again, for the next chunk,
+      // after its last use.  The loops have one way out: any other would have the compiler move registers that are being
+      // loaded, and wait for them.  So a chunk that has to be walked goes on to the end of the body, and its results are
+      // dropped.
+      if (carries) {
+        typedef typename Raw<IN>::mem mem;
+        const mem* vp = static_cast<const mem*>(a.v) + (r.t0 + done) * a.v_token + h * a.v_head + col + n;
+        frag kf[KS][TK], xf[HT][2][TK], tf[2][3];
+        f32x4 be, fk, lk;
+        typename Raw<IN>::type v[2][4];
+        float decay;
+        int64_t v_at[4];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int j = 0; j < 4; ++j) v_at[j] = (row + j) * a.v_token;
+        auto load_k = [&](int len) {
 #pragma unroll
-        for (int e = 0; e < TK; ++e) {
-          kf[k][e] = get(kq_at, (wave * KS + k) * TK + e, lane * 16);
-          qf[k][e] = get(kq_at + 4 * KS * TK * kFragBytes, (wave * KS + k) * TK + e, lane * 16);
-        }
-      if (len < kChunk)  // rows past the end: the last one again
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v_at[j] = min(row + j, len - 1) * a.v_token;
+            for (int e = 0; e < TK; ++e) kf[k][e] = get(lane * 16, kq_at + ((wave * KS + k) * TK + e) * kFragBytes);
+          if (len < kChunk)  // rows past the end: the last one again
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) v_at[j] = min(row + j, len - 1) * a.v_token;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) v[m][j] = vp[v_at[j] + 16 * m];
-      be = row4(offsetof(Scalars, beta)), fk = row4(offsetof(Scalars, far_k));
-    };
-    auto load_t = [&]() {
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)  // (not used, but loaded, where there is no second one: the waits count loads)
+            for (int m = 0; m < 2; ++m) v[m][j] = vp[v_at[j] + 16 * m];
+          be = row4(offsetof(Scalars, beta)), fk = row4(offsetof(Scalars, far_k));
+        };
+        auto load_t = [&]() {
 #pragma unroll
-        for (int e = 0; e < 3; ++e) tf[k][e] = get(tri_pos, tri_at(wave, 0) * 3 + e, k ? tri1 : lane * 16);
-      lk = row4(offsetof(Scalars, last_k));
-    };
-    auto load_x = [&]() {
+          for (int k = 0; k < 2; ++k)  // (not used, but loaded, where there is no second one: the waits count loads)
 #pragma unroll
-      for (int t = 0; t < HT; ++t)
+            for (int e = 0; e < 3; ++e) tf[k][e] = get(lane * 16 + k * 3 * second, t_at + (tri_at(wave, 0) * 3 + e) * kFragBytes);
+          lk = row4(offsetof(Scalars, last_k));
+        };
+        auto load_x = [&]() {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int t = 0; t < HT; ++t)
 #pragma unroll
-          for (int e = 0; e < TK; ++e) xf[t][k][e] = get(kq_at + 8 * KS * TK * kFragBytes, ((wave * HT + t) * 2 + k) * TK + e, lane * 16);
-      decay = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), row * 4,
-                                                                   sc_at + (int)offsetof(Scalars, decay), 0));
-    };
-    auto load_p = [&]() {
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < OT; ++e) pf[k][e] = get(p_at, tri_at(wave, 0) * OT + e, k ? tri1p : lane * 16);
-      fq = row4(offsetof(Scalars, far_q));
-    };
-    int len = (int)min((int64_t)kChunk, stop - done);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v_at[j] = (row + j) * a.v_token;
-    load_kq(len);
-    load_t();
-    load_x();
-    load_p();
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // or the loop's waits would count from here, in whatever order these were issued
-    put_state();
-    lds_barrier();
+              for (int e = 0; e < TK; ++e)
+                xf[t][k][e] = get(lane * 16, kq_at + (8 * KS * TK + ((wave * HT + t) * 2 + k) * TK + e) * kFragBytes);
+          decay = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(__builtin_amdgcn_make_buffer_rsrc(unit, 0, (int)p.unit_bytes, 0x00027000), row * 4,
+                                                                       sc_at + (int)offsetof(Scalars, decay), 0));
+        };
+        int len = (int)min((int64_t)kChunk, stop - done);
+        load_k(len);
+        load_t();
+        load_x();
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // or the loop's waits would count from here, in whatever order these were issued
+        put_state();
+        lds_barrier();
 #pragma unroll 1
-    do {
-      const int now = len;
-      if (done + kChunk < stop) {  // the next chunk's places (the last chunk's are asked for twice)
-        len = (int)min((int64_t)kChunk, stop - done - kChunk);
-        unit += p.unit_bytes, vp += kChunk * a.v_token;
-      }
-      // K S and Q S: each operand is read while the one before it is multiplied
-      f32x4 o[2] = {}, y[2] = {};
-      {
-        frag f[2][2][3];
-        auto read = [&](int k) {
+        do {
+          const int now = len;
+          if (done + kChunk < stop) {  // the next chunk's places (the last chunk's are asked for twice)
+            len = (int)min((int64_t)kChunk, stop - done - kChunk);
+            unit += p.unit_bytes, vp += kChunk * a.v_token;
+          }
+          // K S: each operand is read while the one before it is multiplied
+          f32x4 y[2] = {}, y2[2] = {};
+          {
+            frag f[2][2][3];
+            auto read = [&](int k) {
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+              for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 3; ++e) f[k & 1][m][e] = sf[k][m][e][lane];
-        };
-        read(0);
+                for (int e = 0; e < 3; ++e) f[k & 1][m][e] = sf[k][m][e][lane];
+            };
+            read(0);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if (k + 1 < KS) read(k + 1);
-          in_order();
+            for (int k = 0; k < KS; ++k) {
+              if (k + 1 < KS) read(k + 1);
+              in_order();
 #pragma unroll
-          for (int i = 0; i < TK; ++i)
+              for (int i = 0; i < TK; ++i)
 #pragma unroll
-            for (int e = 0; e < 3; ++e)
+                for (int e = 0; e < 3; ++e)
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                if (i + e < 3) y[m] = mma(kf[k][i], f[k & 1][m][e], y[m]);
-                if (i + e < 3 && e < OT) o[m] = mma(qf[k][i], f[k & 1][m][e], o[m]);
-              }
-        }
-      }
-      // R = beta V - far_k (K S)
-      float spoil = 0.f;  // NaN if anything is not finite
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float vj = row + j < now ? Raw<IN>::number(v[m][j]) : 0.f;
-          spoil = fmaf(vj, 0.f, spoil);
-          if (m == 0) spoil = fmaf(be[j], 0.f, spoil);
-          y[m][j] = fmaf(be[j], vj, -fk[j] * y[m][j]);
-          o[m][j] *= fq[j];
-        }
-        half_frag f[3];
-        split4<3>(y[m], f);
-#pragma unroll
-        for (int e = 0; e < 3; ++e) *half(rf[s2][m][e], c2) = f[e];
-      }
-      const bool bad = __any(spoil != 0.f);
-      if (lane == 0) odds[wave] = bad;
-      load_kq(len);
-      lds_barrier();
-      // A chunk that has to be walked still goes on to the end of the loop's body, whose results are dropped: another way out
-      // would have the compiler move what is being loaded, and wait for it.
-      odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
-#pragma unroll
-      for (int t = 0; t < HT; ++t)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) before[t][m] = s[t][m];
-      // X = T R
-      f32x4 y2[2] = {};
-      {
-        frag f[2][2][3];
-        auto read = [&](int k) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int e = 0; e < 3; ++e) f[k][m][e] = rf[k][m][e][lane];
-        };
-        auto product = [&](int k) {
-#pragma unroll
-          for (int e = 0; e < 3; ++e)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              y[m] = mma(tf[k][e], f[k][m][0], y[m]);
-              y2[m] = mma(tf[k][e == 2 ? 0 : e], f[k][m][e == 2 ? 2 : 1], y2[m]);
+                  for (int m = 0; m < 2; ++m)
+                    if (i + e < 3) (k & 1 ? y2 : y)[m] = mma(kf[k][i], f[k & 1][m][e], (k & 1 ? y2 : y)[m]);
             }
-        };
-#pragma unroll
-        for (int m = 0; m < 2; ++m) y[m] = f32x4{};
-        read(0);
-        if (s2) read(1);
-        in_order();
-        product(0);
-        if (s2) product(1);
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        y[m] += y2[m];
-        half_frag f[3];
-        split4<3>(y[m] * lk, f);
-#pragma unroll
-        for (int e = 0; e < 3; ++e) *half(zf[s2][m][e], c2) = f[e];
-        split4<OT>(y[m], f);
-#pragma unroll
-        for (int e = 0; e < OT; ++e) *half(yf[s2][m][e], c2) = f[e];
-      }
-      load_t();
-      lds_barrier();
-      // S = decay S + K^T Z
-#pragma unroll
-      for (int t = 0; t < HT; ++t)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) s[t][m] *= decay;
-      {
-        frag f[2][2][3];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int e = 0; e < 3; ++e) f[k][m][e] = zf[k][m][e][lane];
-        in_order();
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < TK; ++i)
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-#pragma unroll
-              for (int t = 0; t < HT; ++t)
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  if (i + e < 3) s[t][m] = mma(xf[t][k][i], f[k][m][e], s[t][m]);
-      }
-      put_state();
-      load_x();
-      // out = far_q (Q S) + P X
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (k <= s2)
+          }
+          // R = beta V - far_k (K S)
+          float spoil = 0.f;  // NaN if anything is not finite
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            frag f[OT];
 #pragma unroll
-            for (int e = 0; e < OT; ++e) f[e] = yf[k][m][e][lane];
-            o[m] = mma_terms<OT, OT>(pf[k], f, o[m]);
+            for (int j = 0; j < 4; ++j) {
+              const float vj = row + j < now ? Raw<IN>::number(v[m][j]) : 0.f;
+              spoil = fmaf(vj, 0.f, spoil);
+              if (m == 0) spoil = fmaf(be[j], 0.f, spoil);
+              y[m][j] = fmaf(be[j], vj, -fk[j] * (y[m][j] + y2[m][j]));
+            }
+            half_frag f[3];
+            split4<3>(y[m], f);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) *half(rf[s2][m][e], c2) = f[e];
           }
-      load_p();
-      const auto op = __builtin_amdgcn_make_buffer_rsrc(static_cast<O*>(a.out) + (r.t0 + done) * a.v_heads * a.dv, 0,
-                                                        odd ? 0 : now * a.v_heads * a.dv * (int)sizeof(O), 0x00027000);
+          const bool bad = __any(spoil != 0.f);
+          if (lane == 0) odds[wave] = bad;
+          load_k(len);
+          lds_barrier();
+          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
+          // X = T R
+          {
+            frag f[2][2][3];
+            auto read = [&](int k) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+              for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) put_out(op, ((row + j) * a.v_heads + h) * a.dv + col + 16 * m + n, (O)o[m][j]);
-      lds_barrier();
-      done += kChunk;
-    } while (!odd && done < stop);
-    if (odd) {
-      done -= kChunk;
-      walk_to = min(done + kChunk, stop);
+                for (int e = 0; e < 3; ++e) f[k][m][e] = rf[k][m][e][lane];
+            };
+            auto product = [&](int k) {
 #pragma unroll
-      for (int t = 0; t < HT; ++t)
+              for (int e = 0; e < 3; ++e)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) s[t][m] = before[t][m];
-    } else {
-      done = stop;
-      walk_to = ends ? r.n : stop;
-    }
+                for (int m = 0; m < 2; ++m) {
+                  y[m] = mma(tf[k][e], f[k][m][0], y[m]);
+                  y2[m] = mma(tf[k][e == 2 ? 0 : e], f[k][m][e == 2 ? 2 : 1], y2[m]);
+                }
+            };
+#pragma unroll
+            for (int m = 0; m < 2; ++m) y[m] = f32x4{}, y2[m] = f32x4{};
+            read(0);
+            if (s2) read(1);
+            in_order();
+            product(0);
+            if (s2) product(1);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            y[m] += y2[m];
+            half_frag f[3];
+            split4<3>(y[m] * lk, f);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) *half(zf[s2][m][e], c2) = f[e];
+            *reinterpret_cast<f32x4*>(&xs[s2][m][lane][4 * c2]) = y[m];
+          }
+          load_t();
+          lds_barrier();
+          // S = decay S + K^T Z
+#pragma unroll
+          for (int t = 0; t < HT; ++t)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) s[t][m] *= decay;
+          {
+            frag f[2][2][3];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 3; ++e) f[k][m][e] = zf[k][m][e][lane];
+            in_order();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < TK; ++i)
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+#pragma unroll
+                  for (int t = 0; t < HT; ++t)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                      if (i + e < 3) s[t][m] = mma(xf[t][k][i], f[k][m][e], s[t][m]);
+          }
+          if (!odd) put_state();
+          load_x();
+          lds_barrier();
+          done += kChunk;
+        } while (!odd && done < stop);
+        if (odd)  // the state before the chunk: its terms' sum, which is exact
+#pragma unroll
+          for (int e = 0; e < HT; ++e)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const int t = wave * HT + e;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                auto term = [&](int i) { return (float)(*half(sf[t >> 1][m][i], t & 1))[j]; };
+                s[e][m][j] = (term(2) + term(1)) + term(0);
+              }
+            }
+      } else {
+        frag qf[KS][TK], pf[2][OT];
+        f32x4 fq;
+        auto load_q = [&]() {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < TK; ++e) qf[k][e] = get(lane * 16, kq_at + (4 * KS * TK + (wave * KS + k) * TK + e) * kFragBytes);
+          fq = row4(offsetof(Scalars, far_q));
+        };
+        auto load_p = [&]() {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < OT; ++e) pf[k][e] = get(lane * 16 + k * OT * second, p_at + (tri_at(wave, 0) * OT + e) * kFragBytes);
+        };
+        load_q();
+        load_p();
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+        lds_barrier();
+#pragma unroll 1
+        do {
+          const int now = (int)min((int64_t)kChunk, stop - done);
+          if (done + kChunk < stop) unit += p.unit_bytes;
+          lds_barrier();
+          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
+          // far_q (Q S)
+          f32x4 o[2] = {};
+          {
+            frag f[2][2][OT];
+            auto read = [&](int k) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < OT; ++e) f[k & 1][m][e] = sf[k][m][e][lane];
+            };
+            read(0);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              if (k + 1 < KS) read(k + 1);
+              in_order();
+#pragma unroll
+              for (int i = 0; i < TK; ++i)
+#pragma unroll
+                for (int e = 0; e < OT; ++e)
+#pragma unroll
+                  for (int m = 0; m < 2; ++m)
+                    if (i + e < 3) o[m] = mma(qf[k][i], f[k & 1][m][e], o[m]);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) o[m] *= fq;
+          load_q();
+          lds_barrier();
+          frag f[2][2][OT];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (k <= s2)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) split_terms<OT>(&xs[k][m][lane][0], f[k][m]);
+          lds_barrier();
+          // out = far_q (Q S) + P X
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (k <= s2)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) o[m] = mma_terms<OT, OT>(pf[k], f[k][m], o[m]);
+          load_p();
+          const auto op = __builtin_amdgcn_make_buffer_rsrc(static_cast<O*>(a.out) + (r.t0 + done) * a.v_heads * a.dv, 0,
+                                                            odd ? 0 : now * a.v_heads * a.dv * (int)sizeof(O), 0x00027000);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) put_out(op, ((row + j) * a.v_heads + h) * a.dv + col + 16 * m + n, (O)o[m][j]);
+          done += kChunk;
+        } while (!odd && done < stop);
+      }
+      if (odd) {
+        done -= kChunk;
+        walk_to = min(done + kChunk, stop);
+      } else {
+        done = stop;
+        walk_to = ends ? r.n : stop;
+      }
     }
     if (walk_to > done) walk(r.t0 + done, r.t0 + walk_to), done = walk_to;
     if (!odd) break;
   }
 
-  if (ends && (!kept || (r.n == 0 && a.state_out == a.state))) return;
+  if (!carries || (ends && (!kept || (r.n == 0 && a.state_out == a.state)))) return;
   float* dst = ends ? a.state_out + state_at : carry;
 #pragma unroll
   for (int e = 0; e < HT; ++e)
