@@ -108,9 +108,13 @@ __device__ inline void load8(const IN* p, float* x) {
 // ---- T, P and the operands of every chunk --------------------------------------------------------------------------
 
 template <typename IN, int DK, int OT>
-__global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p) {
+__global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParams p) {
   constexpr int KS = DK / 32, TK = terms_in<IN>(), W = kChunk + 4;
-  __shared__ __attribute__((aligned(16))) float A[kChunk][W], T[kChunk][W];
+  constexpr int kStage = std::max<int>(4 * KS * TK * kFragBytes, kChunk * W * 4);
+  __shared__ __attribute__((aligned(16))) float A[kChunk][W];
+  __shared__ __attribute__((aligned(16))) char stage[kStage];  // K's operands, then T
+  frag(*ks)[KS][TK][64] = reinterpret_cast<frag(*)[KS][TK][64]>(stage);
+  float(*T)[W] = reinterpret_cast<float(*)[W]>(stage);
   __shared__ double sums[kChunk];
   __shared__ float norms[kChunk];
   const auto& a = p.a;
@@ -152,6 +156,8 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
       }
       split_terms<TK>(x, qf[s]);
       split_terms<TK>(y, kf[s]);
+#pragma unroll
+      for (int t = 0; t < TK; ++t) ks[wave][s][t][lane] = kf[s][t];
     }
   }
   qq += __shfl_xor(qq, 16, 64), kk += __shfl_xor(kk, 16, 64);
@@ -183,25 +189,16 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
   const double mine = sums[i];
 #pragma unroll 1
   for (int s2 = 0; s2 <= wave >> 1; ++s2) {
-    frag kt[2][KS][TK];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int row = place(2 * s2 + t, n), at = min(row, len - 1);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        float y[8];
-        load8(kp + at * a.k_token + 32 * s, y);
-        if (row >= len)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = 0.f;
-        split_terms<TK>(y, kt[t][s]);
-      }
-    }
     f32x4 akk[2] = {}, aqk[2] = {};
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int s = 0; s < KS; ++s) akk[t] = mma_terms<TK, TK>(kt[t][s], kf[s], akk[t]), aqk[t] = mma_terms<TK, TK>(kt[t][s], qf[s], aqk[t]);
+      for (int s = 0; s < KS; ++s) {
+        frag kt[TK];
+#pragma unroll
+        for (int e = 0; e < TK; ++e) kt[e] = ks[2 * s2 + t][s][e][lane];
+        akk[t] = mma_terms<TK, TK>(kt, kf[s], akk[t]), aqk[t] = mma_terms<TK, TK>(kt, qf[s], aqk[t]);
+      }
     float ra[8], rp[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -225,7 +222,7 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < TK; ++t) {
-          const f32x4 lo = mma(kt[0][s][t], one, f32x4{}), hi = mma(kt[1][s][t], one, f32x4{});
+          const f32x4 lo = mma(ks[2 * s2][s][t][lane], one, f32x4{}), hi = mma(ks[2 * s2 + 1][s][t][lane], one, f32x4{});
           frag f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) f[j] = (bf16)lo[j], f[4 + j] = (bf16)hi[j];
@@ -252,21 +249,26 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
     sc->decay[i] = expf((float)all);
   }
 
-  // T: the diagonal blocks of 16 by substitution, one column per lane ...
-  for (int k = tid; k < kChunk * W; k += kPrepThreads) (&T[0][0])[k] = 0.f;
+  // T: the diagonal blocks of 16 by substitution, a column per lane, the rows of A from the lanes that hold them ...
   __syncthreads();
-  if (lane < 16) {
-    float x[16];
+  float x[16];
+  {
+    float row[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float v = k == lane ? 1.f : 0.f;
+    for (int k = 0; k < 16; k += 4) *reinterpret_cast<f32x4*>(row + k) = *reinterpret_cast<const f32x4*>(&A[16 * wave + n][16 * wave + k]);
 #pragma unroll
-      for (int j = 0; j < k; ++j) v = fmaf(-A[16 * wave + k][16 * wave + j], x[j], v);
-      x[k] = v;
-    }
+    for (int k = 0; k < 16; ++k) x[k] = k == n ? 1.f : 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) T[16 * wave + k][16 * wave + lane] = x[k];
+    for (int j = 0; j < 15; ++j)
+#pragma unroll
+      for (int k = j + 1; k < 16; ++k) x[k] = fmaf(-__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row[j]), k)), x[j], x[k]);
   }
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if ((k & 3) == g) T[16 * wave + k][16 * wave + n] = x[k];
+  if (wave < 2)  // the blocks above the diagonal that operands of 32 columns reach
+#pragma unroll
+    for (int k = 0; k < 4; ++k) T[32 * wave + 4 * g + k][32 * wave + 16 + n] = 0.f;
   __syncthreads();
   // ... then T21 = -T22 (A21 T11), for blocks of 16 and of 32.  A step's 4 summed indices are 4g + s: what a result holds.
   auto block = [&](const float(*l)[W], int li, int lj, f32x4 right, f32x4 sum, float sign) {
@@ -293,6 +295,7 @@ __global__ __launch_bounds__(kPrepThreads) void gdn_prepare_kernel(ChunkParams p
     f32x4 m[2] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      if (k < wave) continue;
       const f32x4 v = column(k, wave);
 #pragma unroll
       for (int t = 0; t < 2; ++t) m[t] = block(A, 2 + t, k, v, m[t], 1.f);
