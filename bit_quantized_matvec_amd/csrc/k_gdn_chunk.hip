@@ -105,6 +105,25 @@ __device__ inline void load8(const IN* p, float* x) {
   for (int j = 0; j < 8; ++j) x[j] = (float)v.v[j];
 }
 
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x[k] -= A[k][j] x[j] for k > j, lane k of each 16 holding row k of A.
+template <int J, int K>
+__device__ inline void step(const float* row, float* x) {
+  if constexpr (K < 16) {
+    const int a = __builtin_amdgcn_update_dpp(0, __float_as_int(row[J]), 0x150 + K, 0xF, 0xF, true);  // row_newbcast:K
+    x[K] = fmaf(-__int_as_float(a), x[J], x[K]);
+    step<J, K + 1>(row, x);
+  }
+}
+template <int J>
+__device__ inline void steps(const float* row, float* x) {
+  if constexpr (J < 15) {
+    step<J, J + 1>(row, x);
+    steps<J + 1>(row, x);
+  }
+}
+
 // ---- T, P and the operands of every chunk --------------------------------------------------------------------------
 
 template <typename IN, int DK, int OT>
@@ -143,7 +162,6 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   float qq = 0.f, kk = 0.f;
   {
     const int at = min(i, len - 1);
-    const float live = i < len ? 1.f : 0.f;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       float x[8], y[8];
@@ -152,7 +170,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         qq = fmaf(x[j], x[j], qq), kk = fmaf(y[j], y[j], kk);
-        if (live == 0.f) x[j] = y[j] = 0.f;
+        if (len < kChunk && i >= len) x[j] = y[j] = 0.f;
       }
       split_terms<TK>(x, qf[s]);
       split_terms<TK>(y, kf[s]);
@@ -175,7 +193,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
     const float x = lane < len ? a.g[(t0 + lane) * a.v_heads + h] : 0.f;
     odd = odd || !(x <= 0.f);
     if (wave == 0) {
-      double sum = fmaxf(x, kLeastG);
+      double sum = fmaxf(x, kLeastG) * 1.4426950408889634074;  // in powers of two
 #pragma unroll
       for (int o = 1; o < kChunk; o <<= 1) {
         const double y = __shfl_up(sum, o, 64);
@@ -187,6 +205,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   odd = __syncthreads_or(odd);
   if (odd && g == 0) sc->beta[i] = NAN;  // K, Q and K^T are still written: other heads may be odd in nothing
   const double mine = sums[i];
+  const float nb = beta * nk;
 #pragma unroll 1
   for (int s2 = 0; s2 <= wave >> 1; ++s2) {
     f32x4 akk[2] = {}, aqk[2] = {};
@@ -203,9 +222,10 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = 32 * s2 + 8 * g + j;
-      const float e = row <= i ? expf((float)(mine - sums[row])) * norms[row] : 0.f;
-      rp[j] = row <= i ? nq * e * aqk[j >> 2][j & 3] : 0.f;
-      ra[j] = row < i ? beta * nk * e * akk[j >> 2][j & 3] : 0.f;
+      const float e = exp2_(fminf((float)(mine - sums[row]), 0.f)) * norms[row];
+      const float q = nq * e * aqk[j >> 2][j & 3], k = nb * e * akk[j >> 2][j & 3];
+      rp[j] = row <= i ? q : 0.f;
+      ra[j] = row < i ? k : 0.f;
     }
     *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g]) = float4{ra[0], ra[1], ra[2], ra[3]};
     *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g + 4]) = float4{ra[4], ra[5], ra[6], ra[7]};
@@ -241,34 +261,30 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   if (odd) return;
   const double all = sums[kChunk - 1];
   if (g == 0) {
-    const float far = expf((float)mine);
+    const float far = exp2_((float)mine);
     sc->beta[i] = beta;
     sc->far_k[i] = beta * far * nk;
     sc->far_q[i] = far * nq;
-    sc->last_k[i] = expf((float)(all - mine)) * nk;
-    sc->decay[i] = expf((float)all);
+    sc->last_k[i] = exp2_((float)(all - mine)) * nk;
+    sc->decay[i] = exp2_((float)all);
   }
 
-  // T: the diagonal blocks of 16 by substitution, a column per lane, the rows of A from the lanes that hold them ...
+  // T: the diagonal blocks of 16 by substitution, one block in 16 lanes of the first wave: a lane holds row n of A and
+  // column n of T, and a step takes A's row k from lane k ...
   __syncthreads();
-  float x[16];
-  {
-    float row[16];
+  if (wave == 0) {
+    float row[16], x[16];
 #pragma unroll
-    for (int k = 0; k < 16; k += 4) *reinterpret_cast<f32x4*>(row + k) = *reinterpret_cast<const f32x4*>(&A[16 * wave + n][16 * wave + k]);
+    for (int k = 0; k < 16; k += 4) *reinterpret_cast<f32x4*>(row + k) = *reinterpret_cast<const f32x4*>(&A[16 * g + n][16 * g + k]);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] = k == n ? 1.f : 0.f;
+    steps<0>(row, x);
 #pragma unroll
-    for (int j = 0; j < 15; ++j)
+    for (int k = 0; k < 16; ++k) T[16 * g + k][16 * g + n] = x[k];
+  } else if (wave < 3) {  // the blocks above the diagonal that operands of 32 columns reach
 #pragma unroll
-      for (int k = j + 1; k < 16; ++k) x[k] = fmaf(-__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row[j]), k)), x[j], x[k]);
+    for (int k = 0; k < 4; ++k) T[32 * (wave - 1) + 4 * g + k][32 * (wave - 1) + 16 + n] = 0.f;
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    if ((k & 3) == g) T[16 * wave + k][16 * wave + n] = x[k];
-  if (wave < 2)  // the blocks above the diagonal that operands of 32 columns reach
-#pragma unroll
-    for (int k = 0; k < 4; ++k) T[32 * wave + 4 * g + k][32 * wave + 16 + n] = 0.f;
   __syncthreads();
   // ... then T21 = -T22 (A21 T11), for blocks of 16 and of 32.  A step's 4 summed indices are 4g + s: what a result holds.
   auto block = [&](const float(*l)[W], int li, int lj, f32x4 right, f32x4 sum, float sign) {
