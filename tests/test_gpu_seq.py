@@ -408,6 +408,77 @@ def test_gdn_bad_offsets_stay_in_bounds(tq, cu):
             assert torch.equal(gs.cpu(), state)
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("where", ["v", "k", "q", "beta", "g"])
+def test_gdn_a_late_token_stays_late(tq, bad, where):
+    """What is not finite at token 100 reaches no token before it, no other head and, through v, no other column."""
+    n, late, vh, dk, dv = 170, 100, 2, 128, 64
+    q, k, v, g, beta, state, cu = gdn_inputs([n], vh, vh, dk, dv, BF)
+    bad_at = {"v": v, "k": k, "q": q}
+    if where in bad_at:
+        bad_at[where][late, 0, 5] = bad
+    else:
+        {"beta": beta, "g": g}[where][late, 0] = abs(bad)
+    c = lambda x: x.cuda()  # noqa: E731
+    gs = state.cuda()
+    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=True, out_dtype=F32, max_len=n,
+                 ws=tq.gdn_workspace(n, 1, vh, dk, dv, max_len=n)).cpu()
+    ok = {"v": v, "k": k, "q": q, "beta": beta, "g": g}
+    clean = {x: torch.nan_to_num(y, 0.0, 0.0, 0.0) for x, y in ok.items()}
+    want, states, big = so.gdn(clean["q"], clean["k"], clean["v"], clean["g"], clean["beta"], state, cu, dk**-0.5, True, 1e-6)
+    bound = so.gdn_bound(n, dk, big) * dk**-0.5
+    limit = so.HALF_STEP[F32] * want.abs() + bound
+    near(got[:late], want[:late], limit[:late], "tokens before it")
+    near(got[:, 1], want[:, 1], limit[:, 1], "the other head")
+    near(gs[0, 1], states[0, 1], torch.full_like(states[0, 1], so.gdn_bound(n, dk, big)), "the other head's state")
+    if where == "v":
+        rest = [x for x in range(dv) if x != 5]
+        near(got[:, 0][:, rest], want[:, 0][:, rest], limit[:, 0][:, rest], "other columns")
+    assert not bool(torch.isfinite(got[late, 0]).all())
+    if where == "q":  # only its own token
+        near(got[late + 1 :], want[late + 1 :], limit[late + 1 :], "tokens after it")
+        near(gs, states, torch.full_like(states, so.gdn_bound(n, dk, big)), "state")
+
+
+@pytest.mark.parametrize("hint", ["right", "none", "short"])
+@pytest.mark.parametrize("slots", [False, True])
+def test_gdn_in_several_launches(tq, hint, slots):
+    """More chunks than the workspace holds: states go from launch to launch, also those of sequences without a slot."""
+    n, heads, dk, dv = [1500, 700, 0, 40, 5, 130], 64, 128, 32
+    q, k, v, g, beta, state, cu = gdn_inputs(n, heads, heads, dk, dv, F32)
+    max_len = {"right": max(n), "none": 0, "short": 64}[hint]
+    c = lambda x: x.cuda()  # noqa: E731
+    ws = tq.gdn_workspace(sum(n), len(n), heads, dk, dv, max_len=max_len)
+    assert ws.numel() == 256 << 20
+    order = [0, -1, 2, 3, -1, 5] if slots else None
+    gs, after = state.cuda(), torch.full(state.shape, 9.0, device="cuda")
+    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=True, ws=ws, max_len=max_len, state_out=after,
+                 slots=torch.tensor(order, dtype=torch.int32, device="cuda") if slots else None)
+    torch.cuda.synchronize()
+    some = [0, 17, 63]
+    start = state.clone()
+    if slots:
+        start[1] = start[4] = 0
+    want, states, big = so.gdn(q[:, some], k[:, some], v[:, some], g[:, some], beta[:, some], start[:, some], cu, dk**-0.5, True, 1e-6)
+    bound = so.gdn_bound(max(n), dk, big)
+    near(got[:, some], want, so.HALF_STEP[F32] * want.abs() + bound * dk**-0.5, "out")
+    stored = [0, 2, 3, 5] if slots else [0, 1, 2, 3, 4, 5]
+    near(after[stored][:, some], states[stored], torch.full_like(states[stored], bound), "state")
+    if slots:
+        assert bool((after[[1, 4]] == 9.0).all())
+
+
+@pytest.mark.parametrize("cu", [[0, 150, 90, 200], [-64, 90, 900, 200], [70, 200, -200, 130], [200, 0, 200, 0]])
+def test_gdn_chunks_with_bad_offsets_stay_in_bounds(tq, cu):
+    q, k, v, g, beta, state, _ = gdn_inputs([200], 1, 2, 64, 64, F32, states=3)
+    c = lambda x: x.cuda()  # noqa: E731
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = tq.gdn_workspace(200, 3, 2, 64, 64, max_len=200)
+    tq.gdn(c(q), c(k), c(v), c(g), c(beta), state.cuda(), torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=True, ws=ws, max_len=200, bad_flag=flag)
+    torch.cuda.synchronize()
+    assert int(flag) == 1
+
+
 # ---- streams and graphs --------------------------------------------------------------------------------------------
 
 def block(tq, s):
