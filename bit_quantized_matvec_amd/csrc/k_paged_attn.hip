@@ -18,8 +18,10 @@
 // Rounding.  Q, K, V enter as they are; products are exact and summed in
 // fp32.  P enters the second product in the cache's type when the output has
 // that type, and as 2 (fp16) or 3 (bf16) terms whose sum holds 22 or 24 bits
-// when the output is fp32.  fp16 P is scaled by 2^15 (removed by the division
-// by l, which carries it too), so that small probabilities stay normal.
+// when the output is fp32.  fp16 P is scaled by 2^11 (removed by the division
+// by l, which carries it too), so that small probabilities stay normal.  attn_chunk
+// moves a row's maximum, and so rescales O, only when a score passes it by more
+// than kSlack (base 2): P is at most 2^kSlack, 2^15 with the scaling in fp16.
 //
 // Unseen keys.  Their scores become -inf; their V values are made zero where
 // no row of the workgroup sees them, as 0 * NaN would spoil a sum.  A value
@@ -43,6 +45,8 @@
 // (m, l, O) go to the workspace.  The last to arrive of each 16 joins them, the
 // last of those joins the joined ones (a tree of two levels, up to 256 parts).
 #include <algorithm>
+#include <cfloat>
+#include <cmath>
 
 #include "kernels.h"
 #include "seq.h"
@@ -77,7 +81,7 @@ struct Half<bf16> {
   typedef bf16 frag __attribute__((ext_vector_type(8)));
   static constexpr unsigned kExp = 0x7F807F80u;  // exponent bits of both halves of a dword
   static constexpr unsigned short kOne = 0x3F80;
-  static constexpr float kShift = 0.f;
+  static constexpr float kShift = 0.f, kSlack = 8.f;
   static constexpr int kTerms = 3;
   static __device__ f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
   static __device__ f32x16 mma(frag a, frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
@@ -87,7 +91,7 @@ struct Half<f16> {
   typedef f16 frag __attribute__((ext_vector_type(8)));
   static constexpr unsigned kExp = 0x7C007C00u;
   static constexpr unsigned short kOne = 0x3C00;
-  static constexpr float kShift = 15.f;
+  static constexpr float kShift = 11.f, kSlack = 4.f;
   static constexpr int kTerms = 2;
   static __device__ f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
   static __device__ f32x16 mma(frag a, frag b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
@@ -488,6 +492,260 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   if (dst) join_tree<C, O, kRowsTile, D>(p, t, tile, part, active, &shared);
 }
 
+// ---- many rows -----------------------------------------------------------------------------------------------------
+
+// 16 bytes per lane from memory straight into LDS, lane i's at dst + 16 i.
+__device__ inline void to_lds(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) unsigned*)src, (__attribute__((address_space(3))) unsigned*)dst, 16, 0, 0);
+}
+__device__ inline float max_halves(float x) {  // over lanes i and i + 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 64 KB of LDS at most
+
+// The rows and places that one wave works on.
+template <typename C, int D, int RT>
+struct ChunkRows {
+  Frag<C> q[RT][D / 16];
+  int pos[RT], least[RT];
+};
+
+// Tiles [lo, hi) of KT keys for the 32 RT rows of each wave and DT tiles of 32 columns from column 32 d0 on.  CAREFUL: with
+// pv_each.
+template <typename C, int D, int RT, int TERMS, int DT, bool CAREFUL>
+__device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, int lo, int hi, const ChunkRows<C, D, RT>& rows, C* kbuf, C* vbuf, int d0,
+                                           f32x16 (&o)[RT][DT], float (&m)[RT], float (&l)[RT]) {
+  typedef Half<C> H;
+  constexpr int KT = chunk_keys(D), KK = D / 16, SB = KT / 32;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
+  }
+  constexpr int KC = D / 8, VC = KT / 8;                      // 16-byte pieces per row of K and V
+  constexpr int NI = KT * D / 8 / kThreads;                   // DMA instructions per wave, for K and for V
+  constexpr int KSTEP = 64 / KC, VSTEP = 64 / VC;             // rows per instruction
+  const auto& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
+  // The piece of V that this lane moves: row d0 + i * VSTEP, place pos, keys 8 * vchunk ..
+  const int v_d0 = wave * NI * VSTEP + lane / VC, vchunk = lane % VC ^ (KT == 64 ? v_d0 & 7 : v_d0 >> 1 & 3);
+  const int k_row0 = wave * NI * KSTEP + lane / KC;
+  const C* kc = static_cast<const C*>(a.k_cache);
+  const C* vc = static_cast<const C*>(a.v_cache);
+  const int32_t* table = a.block_table + t.b * a.table_stride;
+  const int first_page = t.begin >> p.page_shift;
+
+  auto look = [&](int tile) {  // the page of this lane's keys of V; lane 2 q's is that of the tile's q-th 16 keys
+    const int key = tile * KT + 8 * vchunk, at = key >> p.page_shift;
+    int pg = -1;
+    if (key < t.end && at >= first_page && tile < hi) {
+      pg = table[at];
+      if (pg < 0 || pg >= a.pages) raise_flag(a.bad_flag), pg = -1;
+    }
+    return pg;
+  };
+  auto fetch = [&](int tile, int pg, int buf) {
+    const int64_t kpg = max(__builtin_amdgcn_readlane(pg, 2 * (wave * NI * KSTEP / 16)), 0), vpg = max(pg, 0);
+    const C* ks = kc + ((kpg * a.kv_heads + t.kvh) * a.page + ((tile * KT + k_row0) & (a.page - 1))) * (int64_t)D;
+    const C* vs = vc + ((vpg * a.kv_heads + t.kvh) * D + v_d0) * (int64_t)a.page + ((tile * KT + 8 * vchunk) & (a.page - 1));
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int row = k_row0 + i * KSTEP, swap = (row & 3) | (row >> 1 & 4);
+      to_lds(ks + i * KSTEP * D + (lane % KC ^ swap) * 8, kbuf + buf * KT * D + (wave * NI + i) * 512);
+      to_lds(vs + (int64_t)i * VSTEP * a.page, vbuf + buf * KT * D + (wave * NI + i) * 512);
+    }
+  };
+
+  int pg = look(lo), next_pg = -1;
+  if (lo < hi) fetch(lo, pg, 0);
+  next_pg = look(lo + 1);
+  const int pos_lo = t.first_pos + t.row0 / p.group, pos_hi = t.end - 1;
+  const float slack = H::kSlack;
+#pragma unroll 1
+  for (int tile = lo, buf = 0; tile < hi; ++tile, buf ^= 1) {
+    // the tile has arrived, and every wave has left the other buffer
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    const uint64_t there = __ballot(pg >= 0);
+    pg = next_pg;
+    if (tile + 1 < hi) fetch(tile + 1, pg, buf ^ 1);
+    next_pg = look(tile + 2);
+    const C* kt = kbuf + buf * KT * D;
+    const C* vt = vbuf + buf * KT * D;
+    const int k0 = tile * KT;
+    f32x16 s[RT][SB];
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r][b] = f32x16{};
+      const int key = 32 * b + (n & 0x13) + ((n & 4) << 1) + ((n & 8) >> 1), swap = (key & 3) | (key >> 1 & 4);
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const Frag<C> f = *reinterpret_cast<const Frag<C>*>(kt + key * D + ((2 * kk + g) ^ swap) * 8);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][b] = H::mma(f, rows.q[r][kk], s[r][b]);
+      }
+    }
+    const bool whole = there == ~uint64_t(0) && k0 + KT - 1 <= pos_lo && (a.window <= 0 || k0 > pos_hi - a.window);
+    if (!whole) {
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
+          const bool ok = there >> (2 * (at >> 4)) & 1;
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            if (!(ok && key <= rows.pos[r] && key >= rows.least[r])) s[r][b][i] = -INFINITY;
+        }
+    }
+    Frag<C> pf[RT][SB][2][TERMS], sf[RT][SB][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float mx = s[r][0][0];
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[r][b][i]);
+      mx = max_halves(mx) * p.scale2;
+      if (__any(mx > m[r] + slack)) {
+        const float mn = fmaxf(m[r], mx), keep = m[r] == -INFINITY ? 0.f : exp2_(m[r] - mn);
+        m[r] = mn;
+        l[r] *= keep;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[r][d] *= keep;
+      }
+      const float base = (m[r] == -INFINITY ? 0.f : m[r]) - H::kShift;
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          e[i] = exp2_(fmaf(s[r][b][i], p.scale2, -base));
+          l[r] += e[i];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          split_terms<TERMS>(e + 8 * h, pf[r][b][h]);
+          if constexpr (CAREFUL)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sf[r][b][h][j] = (C)(s[r][b][8 * h + j] == -INFINITY ? 0.f : 1.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < SB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int chunk = 4 * b + 2 * h + g, key = k0 + 8 * chunk;
+        const bool ok = there >> (2 * (2 * b + h)) & 1;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          u32x4 v = *reinterpret_cast<const u32x4*>(vt + (32 * (d0 + d) + n) * KT + (chunk ^ (KT == 64 ? n & 7 : n >> 1 & 3)) * 8);
+          if (!whole) v = ok ? keep_keys(v, key, t.begin, t.end) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            if constexpr (CAREFUL) {
+              o[r][d] = pv_each<C, TERMS>(v, pf[r][b][h], sf[r][b][h], o[r][d]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v), pf[r][b][h][e], o[r][d]);
+            }
+          }
+        }
+      }
+  }
+  __syncthreads();  // the buffers are free again
+}
+
+template <typename C, typename O, int D, int RT>
+__global__ __launch_bounds__(kThreads, D < 256 && RT == 1 ? 2 : 1) void attn_chunk_kernel(AttnParams p) {
+  constexpr int KT = chunk_keys(D), KK = D / 16, DT = D / 32, ROWS = 128 * RT;
+  constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
+  __shared__ __attribute__((aligned(128))) C kbuf[2 * KT * D], vbuf[2 * KT * D];
+  __shared__ int shared;
+  const auto& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
+  const int part = blockIdx.x % p.splits;
+  const int64_t tile = blockIdx.x / p.splits;
+  const Tile t = find_tile<ROWS>(p, tile, lane);
+  if (t.rows <= 0) return;
+  const int first = t.begin / KT, blocks = t.end > 0 ? (t.end + KT - 1) / KT - first : 0;
+  const int active = max(1, min(p.splits, blocks));
+  if (part >= active) return;
+  const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
+
+  ChunkRows<C, D, RT> rows;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int in = (wave * RT + r) * 32 + n;
+    const bool ok = in < t.rows;
+    const int row = t.row0 + (ok ? in : 0);
+    rows.pos[r] = t.first_pos + row / p.group;
+    rows.least[r] = a.window > 0 ? rows.pos[r] - a.window + 1 : 0;
+    const C* src = static_cast<const C*>(a.q) + (t.t0 + row / p.group) * a.q_token + (int64_t)(t.kvh * p.group + row % p.group) * a.q_head + 8 * g;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      u32x4 x = *reinterpret_cast<const u32x4*>(src + 16 * kk);
+      if (!ok) x = u32x4{0u, 0u, 0u, 0u};
+      if (a.scale < 0.f) x ^= 0x80008000u;  // p.scale2 is positive
+      rows.q[r][kk] = __builtin_bit_cast(Frag<C>, x);
+    }
+  }
+  float* dst = nullptr;
+  if (active > 1)
+    dst = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kHeader) + (tile * p.splits + part) * part_floats<ROWS, D>();
+  auto store = [&](int r, int d, const f32x16& o, float m, float sum) {
+    const int in = (wave * RT + r) * 32 + n;
+    if (in >= t.rows) return;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int col = 32 * d + 2 * i + 4 * g;
+      const float v[4] = {o[i], o[i + 1], o[i + 2], o[i + 3]};
+      if (!dst) {
+        finish<C, O, D>(p, t, in, col, m, sum, v);
+      } else {
+        put4(dst + 2 * ROWS + in * D + col, v);
+        if (col == 0) put(dst + in, m), put(dst + ROWS + in, sum);
+      }
+    }
+  };
+  f32x16 o[RT][DT];
+  float m[RT], l[RT];
+  chunk_pass<C, D, RT, TERMS, DT, false>(p, t, lo, hi, rows, kbuf, vbuf, 0, o, m, l);
+  bool odd = false;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    l[r] = sum_halves(l[r]);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) odd = odd || o[r][d][i] != o[r][d][i];
+  }
+  if (!__syncthreads_or(odd)) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) store(r, d, o[r][d], m[r], l[r]);
+  } else {  // a NaN: once more, with care, 32 columns at a time
+#pragma unroll 1
+    for (int d = 0; d < DT; ++d) {
+      f32x16 x[RT][1];
+      chunk_pass<C, D, RT, TERMS, 1, true>(p, t, lo, hi, rows, kbuf, vbuf, d, x, m, l);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) store(r, d, x[r][0], m[r], sum_halves(l[r]));
+    }
+  }
+  if (dst) join_tree<C, O, ROWS, D>(p, t, tile, part, active, &shared);
+}
+
 // ---- host ----------------------------------------------------------------------------------------------------------
 
 // Tiles of `rows` query rows over all sequences (an upper bound; what is left over finds no rows) and key heads.
@@ -502,34 +760,50 @@ int splits_of(int64_t tiles, int64_t units, int64_t target) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits));
 }
 
+// attn_chunk from 64 rows per sequence on.
+bool in_chunks(int64_t tokens, int64_t seqs, int group, int64_t max_len) {
+  const int64_t longest = max_len > 0 ? std::min(max_len, tokens) : (tokens + seqs - 1) / seqs;
+  return longest * group >= 64 && tokens > seqs;
+}
+int64_t parts_bytes(int rows, int dim) { return (int64_t)(kMaxParts + kMaxParts / kFan + kMaxParts) * rows * (dim + 2) * 4; }
+
 template <typename C, typename O, int D>
-hipError_t launch_rows(AttnParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((attn_rows_kernel<C, O, D>), dim3((unsigned)((int64_t)p.slots * p.a.kv_heads * p.splits)), dim3(kThreads), 0, s, p);
+hipError_t launch_dim(AttnParams& p, hipStream_t s) {
+  const auto& a = p.a;
+  const bool chunks = in_chunks(a.tokens, a.seqs, p.group, a.max_len);
+  const int rows = chunks ? kChunkTile : kRowsTile, unit = chunks ? chunk_keys(D) : kWaves * kBlock;
+  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, rows, a.cu != nullptr);
+  const int64_t tiles = (int64_t)p.slots * a.kv_heads;
+  p.splits = a.workspace ? splits_of(tiles, (a.table_width * a.page + unit - 1) / unit, kMaxParts) : 1;
+  const dim3 grid((unsigned)(tiles * p.splits));
+  if (chunks) {
+    hipLaunchKernelGGL((attn_chunk_kernel<C, O, D, 1>), grid, dim3(kThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((attn_rows_kernel<C, O, D>), grid, dim3(kThreads), 0, s, p);
+  }
   return hipGetLastError();
 }
 
 template <typename C, typename O>
 hipError_t launch_type(AttnParams& p, hipStream_t s) {
-  return p.a.dim == 64 ? launch_rows<C, O, 64>(p, s) : p.a.dim == 128 ? launch_rows<C, O, 128>(p, s) : launch_rows<C, O, 256>(p, s);
+  return p.a.dim == 64 ? launch_dim<C, O, 64>(p, s) : p.a.dim == 128 ? launch_dim<C, O, 128>(p, s) : launch_dim<C, O, 256>(p, s);
 }
 
 }  // namespace
 
 int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int kv_heads, int dim) {
   if (tokens == 0) return 0;
-  (void)heads, (void)kv_heads, (void)seqs;
-  return kHeader + (int64_t)(kMaxParts + kMaxParts / kFan + kMaxParts) * kRowsTile * (dim + 2) * 4;
+  // whether attn_chunk runs depends on the lengths too: room for it where it may
+  return kHeader + parts_bytes(tokens > seqs && tokens * (heads / kv_heads) >= 64 ? kChunkTile : kRowsTile, dim);
 }
 
 hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   AttnParams p{a};
+  // attn_chunk takes a negative scale's sign into Q, and masks by -inf before the scaling: a scale of zero is the least
   p.scale2 = a.scale * kLog2e;
   p.group = a.heads / a.kv_heads;
   p.page_shift = __builtin_ctz(a.page);
-  const int64_t keys = a.table_width * a.page;
-  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, kRowsTile, a.cu != nullptr);
-  const int64_t tiles = (int64_t)p.slots * a.kv_heads;
-  p.splits = a.workspace ? splits_of(tiles, (keys + kWaves * kBlock - 1) / (kWaves * kBlock), kMaxParts) : 1;
+  if (in_chunks(a.tokens, a.seqs, p.group, a.max_len)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
   if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch_type<bf16, float>(p, s) : launch_type<bf16, bf16>(p, s);
   return a.out_type == TQ_F32 ? launch_type<f16, float>(p, s) : launch_type<f16, f16>(p, s);
 }
