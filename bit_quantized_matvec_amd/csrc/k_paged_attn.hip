@@ -507,7 +507,27 @@ __device__ inline float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 64 KB of LDS at most
+constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 68 KB of LDS at most
+
+// Places in LDS, of 16-byte pieces.  A read of 16 bytes takes 16 lanes at a time from 64 banks, so 16 consecutive rows'
+// pieces of one column have to lie on 16 different places of 256 bytes.  K row by row, pieces exchanged by k_swap; V^T
+// (rows of 64 or 128 bytes) as the loads leave it, 1 KB per instruction, pieces exchanged by v_swap, which is the same for a
+// lane in every instruction (a lane's keys lie in one page then), and every second KB of 8 rows shifted by 128 bytes.
+template <int D>
+__device__ inline int k_swap(int key) {
+  return D == 64 ? key >> 1 & 7 : key & 15;
+}
+template <int D>
+__device__ inline int v_swap(int row) {
+  return D == 256 ? row >> 2 & 3 : row & 7;
+}
+constexpr int v_block(int dim) { return dim == 256 ? 512 : 576; }  // values from one instruction's place to the next's
+constexpr int v_values(int dim) { return dim * chunk_keys(dim) / 512 * v_block(dim); }
+template <int D>
+__device__ inline int v_place(int row, int piece) {
+  constexpr int KT = chunk_keys(D), ROWS = 512 / KT;
+  return row / ROWS * v_block(D) + row % ROWS * KT + (piece ^ v_swap<D>(row)) * 8;
+}
 
 // The rows and places that one wave works on.
 template <typename C, int D, int RT>
@@ -535,7 +555,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
   // The piece of V that this lane moves: row d0 + i * VSTEP, place pos, keys 8 * vchunk ..
-  const int v_d0 = wave * NI * VSTEP + lane / VC, vchunk = lane % VC ^ (KT == 64 ? v_d0 & 7 : v_d0 >> 1 & 3);
+  const int v_d0 = wave * NI * VSTEP + lane / VC, vchunk = lane % VC ^ v_swap<D>(v_d0);
   const int k_row0 = wave * NI * KSTEP + lane / KC;
   const C* kc = static_cast<const C*>(a.k_cache);
   const C* vc = static_cast<const C*>(a.v_cache);
@@ -557,9 +577,8 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
     const C* vs = vc + ((vpg * a.kv_heads + t.kvh) * D + v_d0) * (int64_t)a.page + ((tile * KT + 8 * vchunk) & (a.page - 1));
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int row = k_row0 + i * KSTEP, swap = (row & 3) | (row >> 1 & 4);
-      to_lds(ks + i * KSTEP * D + (lane % KC ^ swap) * 8, kbuf + buf * KT * D + (wave * NI + i) * 512);
-      to_lds(vs + (int64_t)i * VSTEP * a.page, vbuf + buf * KT * D + (wave * NI + i) * 512);
+      to_lds(ks + i * KSTEP * D + (lane % KC ^ k_swap<D>(k_row0 + i * KSTEP)) * 8, kbuf + buf * KT * D + (wave * NI + i) * 512);
+      to_lds(vs + (int64_t)i * VSTEP * a.page, vbuf + buf * v_values(D) + (wave * NI + i) * v_block(D));
     }
   };
 
@@ -567,7 +586,6 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
   if (lo < hi) fetch(lo, pg, 0);
   next_pg = look(lo + 1);
   const int pos_lo = t.first_pos + t.row0 / p.group, pos_hi = t.end - 1;
-  const float slack = H::kSlack;
 #pragma unroll 1
   for (int tile = lo, buf = 0; tile < hi; ++tile, buf ^= 1) {
     // the tile has arrived, and every wave has left the other buffer
@@ -578,89 +596,97 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
     if (tile + 1 < hi) fetch(tile + 1, pg, buf ^ 1);
     next_pg = look(tile + 2);
     const C* kt = kbuf + buf * KT * D;
-    const C* vt = vbuf + buf * KT * D;
+    const C* vt = vbuf + buf * v_values(D);
     const int k0 = tile * KT;
-    f32x16 s[RT][SB];
-#pragma unroll
-    for (int b = 0; b < SB; ++b) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) s[r][b] = f32x16{};
-      const int key = 32 * b + (n & 0x13) + ((n & 4) << 1) + ((n & 8) >> 1), swap = (key & 3) | (key >> 1 & 4);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        const Frag<C> f = *reinterpret_cast<const Frag<C>*>(kt + key * D + ((2 * kk + g) ^ swap) * 8);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][b] = H::mma(f, rows.q[r][kk], s[r][b]);
-      }
-    }
     const bool whole = there == ~uint64_t(0) && k0 + KT - 1 <= pos_lo && (a.window <= 0 || k0 > pos_hi - a.window);
-    if (!whole) {
-#pragma unroll
-      for (int b = 0; b < SB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
-          const bool ok = there >> (2 * (at >> 4)) & 1;
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            if (!(ok && key <= rows.pos[r] && key >= rows.least[r])) s[r][b][i] = -INFINITY;
-        }
-    }
-    Frag<C> pf[RT][SB][2][TERMS], sf[RT][SB][2];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float mx = s[r][0][0];
-#pragma unroll
-      for (int b = 0; b < SB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[r][b][i]);
-      mx = max_halves(mx) * p.scale2;
-      if (__any(mx > m[r] + slack)) {
-        const float mn = fmaxf(m[r], mx), keep = m[r] == -INFINITY ? 0.f : exp2_(m[r] - mn);
-        m[r] = mn;
-        l[r] *= keep;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[r][d] *= keep;
+    if (!whole) {  // V of keys that no row sees: zeros
+      for (int i = threadIdx.x; i < D * VC; i += kThreads) {
+        const int piece = i % VC, key = k0 + 8 * piece;
+        u32x4* v = reinterpret_cast<u32x4*>(vbuf + buf * v_values(D) + v_place<D>(i / VC, piece));
+        *v = there >> (piece & ~1) & 1 ? keep_keys(*v, key, t.begin, t.end) : u32x4{0u, 0u, 0u, 0u};
       }
-      const float base = (m[r] == -INFINITY ? 0.f : m[r]) - H::kShift;
+      __syncthreads();
+    }
+    {
+      f32x16 s[RT][SB];
 #pragma unroll
       for (int b = 0; b < SB; ++b) {
-        float e[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          e[i] = exp2_(fmaf(s[r][b][i], p.scale2, -base));
-          l[r] += e[i];
-        }
+        for (int r = 0; r < RT; ++r) s[r][b] = f32x16{};
+        const int key = 32 * b + (n & 0x13) + ((n & 4) << 1) + ((n & 8) >> 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          split_terms<TERMS>(e + 8 * h, pf[r][b][h]);
-          if constexpr (CAREFUL)
+        for (int kk = 0; kk < KK; ++kk) {
+          const Frag<C> f = *reinterpret_cast<const Frag<C>*>(kt + key * D + ((2 * kk + g) ^ k_swap<D>(key)) * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sf[r][b][h][j] = (C)(s[r][b][8 * h + j] == -INFINITY ? 0.f : 1.f);
+          for (int r = 0; r < RT; ++r) s[r][b] = H::mma(f, rows.q[r][kk], s[r][b]);
         }
       }
-    }
+      if (!whole)
 #pragma unroll
-    for (int b = 0; b < SB; ++b)
+        for (int b = 0; b < SB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int chunk = 4 * b + 2 * h + g, key = k0 + 8 * chunk;
-        const bool ok = there >> (2 * (2 * b + h)) & 1;
+          for (int i = 0; i < 16; ++i) {
+            const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
+            const bool ok = there >> (2 * (at >> 4)) & 1;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          u32x4 v = *reinterpret_cast<const u32x4*>(vt + (32 * (d0 + d) + n) * KT + (chunk ^ (KT == 64 ? n & 7 : n >> 1 & 3)) * 8);
-          if (!whole) v = ok ? keep_keys(v, key, t.begin, t.end) : u32x4{0u, 0u, 0u, 0u};
+            for (int r = 0; r < RT; ++r)
+              if (!(ok && key <= rows.pos[r] && key >= rows.least[r])) s[r][b][i] = -INFINITY;
+          }
+      Frag<C> pf[RT][SB][2][TERMS], sf[RT][SB][2];
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if constexpr (CAREFUL) {
-              o[r][d] = pv_each<C, TERMS>(v, pf[r][b][h], sf[r][b][h], o[r][d]);
-            } else {
+      for (int r = 0; r < RT; ++r) {
+        float mx = s[r][0][0];
 #pragma unroll
-              for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v), pf[r][b][h][e], o[r][d]);
-            }
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[r][b][i]);
+        mx = max_halves(mx) * p.scale2;
+        if (__any(mx > m[r] + H::kSlack)) {
+          const float mn = fmaxf(m[r], mx), keep = m[r] == -INFINITY ? 0.f : exp2_(m[r] - mn);
+          m[r] = mn;
+          l[r] *= keep;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[r][d] *= keep;
+        }
+        const float base = (m[r] == -INFINITY ? 0.f : m[r]) - H::kShift;
+#pragma unroll
+        for (int b = 0; b < SB; ++b) {
+          float e[16], sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            e[i] = exp2_(fmaf(s[r][b][i], p.scale2, -base));
+            sum += e[i];
+          }
+          l[r] += sum;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            split_terms<TERMS>(e + 8 * h, pf[r][b][h]);
+            if constexpr (CAREFUL)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) sf[r][b][h][j] = (C)(s[r][b][8 * h + j] == -INFINITY ? 0.f : 1.f);
           }
         }
       }
+#pragma unroll
+      for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int piece = 4 * b + 2 * h + g;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(vt + v_place<D>(32 * (d0 + d) + n, piece));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              if constexpr (CAREFUL) {
+                o[r][d] = pv_each<C, TERMS>(v, pf[r][b][h], sf[r][b][h], o[r][d]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v), pf[r][b][h][e], o[r][d]);
+              }
+            }
+          }
+        }
+    }
   }
   __syncthreads();  // the buffers are free again
 }
@@ -669,7 +695,7 @@ template <typename C, typename O, int D, int RT>
 __global__ __launch_bounds__(kThreads, D < 256 && RT == 1 ? 2 : 1) void attn_chunk_kernel(AttnParams p) {
   constexpr int KT = chunk_keys(D), KK = D / 16, DT = D / 32, ROWS = 128 * RT;
   constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
-  __shared__ __attribute__((aligned(128))) C kbuf[2 * KT * D], vbuf[2 * KT * D];
+  __shared__ __attribute__((aligned(128))) C kbuf[2 * KT * D], vbuf[2 * v_values(D)];
   __shared__ int shared;
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
