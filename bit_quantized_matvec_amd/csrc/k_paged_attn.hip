@@ -507,6 +507,8 @@ __device__ inline float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ inline void in_order() { asm volatile("" ::: "memory"); }  // reads before it are issued before it
+
 constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 68 KB of LDS at most
 
 // Places in LDS, of 16-byte pieces.  A read of 16 bytes takes 16 lanes at a time from 64 banks, so 16 consecutive rows'
@@ -608,19 +610,36 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
       __syncthreads();
     }
     {
-      f32x16 s[RT][SB];
+      // Operands are read from LDS one group ahead of the products that take them.
+      f32x16 s[RT][SB] = {};
+      {
+        constexpr int G = 4, GROUPS = SB * KK / G;
+        Frag<C> f[2][G];
+        auto read = [&](int q) {
 #pragma unroll
-      for (int b = 0; b < SB; ++b) {
+          for (int i = 0; i < G; ++i) {
+            const int key = 32 * (q * G / KK) + (n & 0x13) + ((n & 4) << 1) + ((n & 8) >> 1), kk = q * G % KK + i;
+            f[q & 1][i] = *reinterpret_cast<const Frag<C>*>(kt + key * D + ((2 * kk + g) ^ k_swap<D>(key)) * 8);
+          }
+        };
+        read(0);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][b] = f32x16{};
-        const int key = 32 * b + (n & 0x13) + ((n & 4) << 1) + ((n & 8) >> 1);
+        for (int q = 0; q < GROUPS; ++q) {
+          if (q + 1 < GROUPS) read(q + 1);
+          in_order();
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          const Frag<C> f = *reinterpret_cast<const Frag<C>*>(kt + key * D + ((2 * kk + g) ^ k_swap<D>(key)) * 8);
+          for (int i = 0; i < G; ++i)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) s[r][b] = H::mma(f, rows.q[r][kk], s[r][b]);
+            for (int r = 0; r < RT; ++r) s[r][q * G / KK] = H::mma(f[q & 1][i], rows.q[r][q * G % KK + i], s[r][q * G / KK]);
         }
       }
+      u32x4 v[2][DT];
+      auto read_v = [&](int q) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) v[q & 1][d] = *reinterpret_cast<const u32x4*>(vt + v_place<D>(32 * (d0 + d) + n, 2 * q + g));
+      };
+      read_v(0);
+      in_order();
       if (!whole)
 #pragma unroll
         for (int b = 0; b < SB; ++b)
@@ -668,24 +687,21 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
         }
       }
 #pragma unroll
-      for (int b = 0; b < SB; ++b)
+      for (int q = 0; q < 2 * SB; ++q) {
+        if (q + 1 < 2 * SB) read_v(q + 1);
+        in_order();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int piece = 4 * b + 2 * h + g;
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(vt + v_place<D>(32 * (d0 + d) + n, piece));
+          for (int r = 0; r < RT; ++r) {
+            if constexpr (CAREFUL) {
+              o[r][d] = pv_each<C, TERMS>(v[q & 1][d], pf[r][q >> 1][q & 1], sf[r][q >> 1][q & 1], o[r][d]);
+            } else {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              if constexpr (CAREFUL) {
-                o[r][d] = pv_each<C, TERMS>(v, pf[r][b][h], sf[r][b][h], o[r][d]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v), pf[r][b][h][e], o[r][d]);
-              }
+              for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v[q & 1][d]), pf[r][q >> 1][q & 1][e], o[r][d]);
             }
           }
-        }
+      }
     }
   }
   __syncthreads();  // the buffers are free again
