@@ -255,7 +255,7 @@ __device__ inline void finish(const AttnParams& p, const Tile& t, int row, int c
 template <typename C, typename O, int ROWS, int D>
 __device__ void join(const AttnParams& p, const Tile& t, const float* src, int count, float* dst) {
   constexpr int64_t step = part_floats<ROWS, D>();
-  for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
+  for (int i = threadIdx.x; i < t.rows * (D / 4); i += blockDim.x) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
     float ms[kFan], ls[kFan];
     float4 os[kFan];
@@ -509,6 +509,9 @@ __device__ inline float sum_halves(float x) {
 
 __device__ inline void in_order() { asm volatile("" ::: "memory"); }  // reads before it are issued before it
 
+// A wave holds 32 rows of Q and of O: at 256 columns those leave no room for a second wave on its SIMD, so two waves share
+// the rows, compute the scores both and take half of O's columns each.
+constexpr int chunk_threads(int dim) { return dim == 256 ? 512 : 256; }
 constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 68 KB of LDS at most
 
 // Places in LDS, of 16-byte pieces.  A read of 16 bytes takes 16 lanes at a time from 64 banks, so 16 consecutive rows'
@@ -532,27 +535,26 @@ __device__ inline int v_place(int row, int piece) {
 }
 
 // The rows and places that one wave works on.
-template <typename C, int D, int RT>
+template <typename C, int D>
 struct ChunkRows {
-  Frag<C> q[RT][D / 16];
-  int pos[RT], least[RT];
+  Frag<C> q[D / 16];
+  int pos, least;
 };
 
-// Tiles [lo, hi) of KT keys for the 32 RT rows of each wave and DT tiles of 32 columns from column 32 d0 on.  CAREFUL: with
+// Tiles [lo, hi) of KT keys for the 32 rows of each wave and DT tiles of 32 columns from column 32 d0 on.  CAREFUL: with
 // pv_each.
-template <typename C, int D, int RT, int TERMS, int DT, bool CAREFUL>
-__device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, int lo, int hi, const ChunkRows<C, D, RT>& rows, C* kbuf, C* vbuf, int d0,
-                                           f32x16 (&o)[RT][DT], float (&m)[RT], float (&l)[RT]) {
+template <typename C, int D, int TERMS, int DT, bool CAREFUL>
+__device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, int lo, int hi, const ChunkRows<C, D>& rows, C* kbuf, C* vbuf, int d0,
+                                           f32x16 (&o)[DT], float& m, float& l) {
   typedef Half<C> H;
   constexpr int KT = chunk_keys(D), KK = D / 16, SB = KT / 32;
+  {
+    m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY, l[r] = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
+    for (int d = 0; d < DT; ++d) o[d] = f32x16{};
   }
   constexpr int KC = D / 8, VC = KT / 8;                      // 16-byte pieces per row of K and V
-  constexpr int NI = KT * D / 8 / kThreads;                   // DMA instructions per wave, for K and for V
+  constexpr int NI = KT * D / 8 / chunk_threads(D);           // DMA instructions per wave, for K and for V
   constexpr int KSTEP = 64 / KC, VSTEP = 64 / VC;             // rows per instruction
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
@@ -602,7 +604,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
     const int k0 = tile * KT;
     const bool whole = there == ~uint64_t(0) && k0 + KT - 1 <= pos_lo && (a.window <= 0 || k0 > pos_hi - a.window);
     if (!whole) {  // V of keys that no row sees: zeros
-      for (int i = threadIdx.x; i < D * VC; i += kThreads) {
+      for (int i = threadIdx.x; i < D * VC; i += chunk_threads(D)) {
         const int piece = i % VC, key = k0 + 8 * piece;
         u32x4* v = reinterpret_cast<u32x4*>(vbuf + buf * v_values(D) + v_place<D>(i / VC, piece));
         *v = there >> (piece & ~1) & 1 ? keep_keys(*v, key, t.begin, t.end) : u32x4{0u, 0u, 0u, 0u};
@@ -611,7 +613,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
     }
     {
       // Operands are read from LDS one group ahead of the products that take them.
-      f32x16 s[RT][SB] = {};
+      f32x16 s[SB] = {};
       {
         constexpr int G = 4, GROUPS = SB * KK / G;
         Frag<C> f[2][G];
@@ -629,8 +631,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
           in_order();
 #pragma unroll
           for (int i = 0; i < G; ++i)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) s[r][q * G / KK] = H::mma(f[q & 1][i], rows.q[r][q * G % KK + i], s[r][q * G / KK]);
+            s[q * G / KK] = H::mma(f[q & 1][i], rows.q[q * G % KK + i], s[q * G / KK]);
         }
       }
       u32x4 v[2][DT];
@@ -647,42 +648,39 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
           for (int i = 0; i < 16; ++i) {
             const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
             const bool ok = there >> (2 * (at >> 4)) & 1;
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-              if (!(ok && key <= rows.pos[r] && key >= rows.least[r])) s[r][b][i] = -INFINITY;
+              if (!(ok && key <= rows.pos && key >= rows.least)) s[b][i] = -INFINITY;
           }
-      Frag<C> pf[RT][SB][2][TERMS], sf[RT][SB][2];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float mx = s[r][0][0];
+      Frag<C> pf[SB][2][TERMS], sf[SB][2];
+      {
+        float mx = s[0][0];
 #pragma unroll
         for (int b = 0; b < SB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[r][b][i]);
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
         mx = max_halves(mx) * p.scale2;
-        if (__any(mx > m[r] + H::kSlack)) {
-          const float mn = fmaxf(m[r], mx), keep = m[r] == -INFINITY ? 0.f : exp2_(m[r] - mn);
-          m[r] = mn;
-          l[r] *= keep;
+        if (__any(mx > m + H::kSlack)) {
+          const float mn = fmaxf(m, mx), keep = m == -INFINITY ? 0.f : exp2_(m - mn);
+          m = mn;
+          l *= keep;
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[r][d] *= keep;
+          for (int d = 0; d < DT; ++d) o[d] *= keep;
         }
-        const float base = (m[r] == -INFINITY ? 0.f : m[r]) - H::kShift;
+        const float base = (m == -INFINITY ? 0.f : m) - H::kShift;
 #pragma unroll
         for (int b = 0; b < SB; ++b) {
           float e[16], sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            e[i] = exp2_(fmaf(s[r][b][i], p.scale2, -base));
+            e[i] = exp2_(fmaf(s[b][i], p.scale2, -base));
             sum += e[i];
           }
-          l[r] += sum;
+          l += sum;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            split_terms<TERMS>(e + 8 * h, pf[r][b][h]);
+            split_terms<TERMS>(e + 8 * h, pf[b][h]);
             if constexpr (CAREFUL)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) sf[r][b][h][j] = (C)(s[r][b][8 * h + j] == -INFINITY ? 0.f : 1.f);
+              for (int j = 0; j < 8; ++j) sf[b][h][j] = (C)(s[b][8 * h + j] == -INFINITY ? 0.f : 1.f);
           }
         }
       }
@@ -692,13 +690,12 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
         in_order();
 #pragma unroll
         for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
+          {
             if constexpr (CAREFUL) {
-              o[r][d] = pv_each<C, TERMS>(v[q & 1][d], pf[r][q >> 1][q & 1], sf[r][q >> 1][q & 1], o[r][d]);
+              o[d] = pv_each<C, TERMS>(v[q & 1][d], pf[q >> 1][q & 1], sf[q >> 1][q & 1], o[d]);
             } else {
 #pragma unroll
-              for (int e = 0; e < TERMS; ++e) o[r][d] = H::mma(__builtin_bit_cast(Frag<C>, v[q & 1][d]), pf[r][q >> 1][q & 1][e], o[r][d]);
+              for (int e = 0; e < TERMS; ++e) o[d] = H::mma(__builtin_bit_cast(Frag<C>, v[q & 1][d]), pf[q >> 1][q & 1][e], o[d]);
             }
           }
       }
@@ -707,14 +704,15 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
   __syncthreads();  // the buffers are free again
 }
 
-template <typename C, typename O, int D, int RT>
-__global__ __launch_bounds__(kThreads, D < 256 && RT == 1 ? 2 : 1) void attn_chunk_kernel(AttnParams p) {
-  constexpr int KT = chunk_keys(D), KK = D / 16, DT = D / 32, ROWS = 128 * RT;
+template <typename C, typename O, int D>
+__global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnParams p) {
+  constexpr int KT = chunk_keys(D), KK = D / 16, DT = D / 32 * 256 / chunk_threads(D), ROWS = kChunkTile;
   constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
   __shared__ __attribute__((aligned(128))) C kbuf[2 * KT * D], vbuf[2 * v_values(D)];
   __shared__ int shared;
   const auto& a = p.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, g = lane >> 5;
+  const int lane = threadIdx.x & 63, waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = waves & 3, n = lane & 31, g = lane >> 5;
+  const int d0 = waves / 4 * DT;  // this wave's first 32 columns
   const int part = blockIdx.x % p.splits;
   const int64_t tile = blockIdx.x / p.splits;
   const Tile t = find_tile<ROWS>(p, tile, lane);
@@ -724,28 +722,27 @@ __global__ __launch_bounds__(kThreads, D < 256 && RT == 1 ? 2 : 1) void attn_chu
   if (part >= active) return;
   const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
 
-  ChunkRows<C, D, RT> rows;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int in = (wave * RT + r) * 32 + n;
+  ChunkRows<C, D> rows;
+  {
+    const int in = wave * 32 + n;
     const bool ok = in < t.rows;
     const int row = t.row0 + (ok ? in : 0);
-    rows.pos[r] = t.first_pos + row / p.group;
-    rows.least[r] = a.window > 0 ? rows.pos[r] - a.window + 1 : 0;
+    rows.pos = t.first_pos + row / p.group;
+    rows.least = a.window > 0 ? rows.pos - a.window + 1 : 0;
     const C* src = static_cast<const C*>(a.q) + (t.t0 + row / p.group) * a.q_token + (int64_t)(t.kvh * p.group + row % p.group) * a.q_head + 8 * g;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       u32x4 x = *reinterpret_cast<const u32x4*>(src + 16 * kk);
       if (!ok) x = u32x4{0u, 0u, 0u, 0u};
       if (a.scale < 0.f) x ^= 0x80008000u;  // p.scale2 is positive
-      rows.q[r][kk] = __builtin_bit_cast(Frag<C>, x);
+      rows.q[kk] = __builtin_bit_cast(Frag<C>, x);
     }
   }
   float* dst = nullptr;
   if (active > 1)
     dst = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kHeader) + (tile * p.splits + part) * part_floats<ROWS, D>();
-  auto store = [&](int r, int d, const f32x16& o, float m, float sum) {
-    const int in = (wave * RT + r) * 32 + n;
+  auto store = [&](int d, const f32x16& o, float m, float sum) {
+    const int in = wave * 32 + n;
     if (in >= t.rows) return;
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -759,30 +756,26 @@ __global__ __launch_bounds__(kThreads, D < 256 && RT == 1 ? 2 : 1) void attn_chu
       }
     }
   };
-  f32x16 o[RT][DT];
-  float m[RT], l[RT];
-  chunk_pass<C, D, RT, TERMS, DT, false>(p, t, lo, hi, rows, kbuf, vbuf, 0, o, m, l);
+  f32x16 o[DT];
+  float m, l;
+  chunk_pass<C, D, TERMS, DT, false>(p, t, lo, hi, rows, kbuf, vbuf, d0, o, m, l);
   bool odd = false;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    l[r] = sum_halves(l[r]);
+  {
+    l = sum_halves(l);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) odd = odd || o[r][d][i] != o[r][d][i];
+      for (int i = 0; i < 16; ++i) odd = odd || o[d][i] != o[d][i];
   }
   if (!__syncthreads_or(odd)) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int d = 0; d < DT; ++d) store(r, d, o[r][d], m[r], l[r]);
+      for (int d = 0; d < DT; ++d) store(d0 + d, o[d], m, l);
   } else {  // a NaN: once more, with care, 32 columns at a time
 #pragma unroll 1
     for (int d = 0; d < DT; ++d) {
-      f32x16 x[RT][1];
-      chunk_pass<C, D, RT, TERMS, 1, true>(p, t, lo, hi, rows, kbuf, vbuf, d, x, m, l);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) store(r, d, x[r][0], m[r], sum_halves(l[r]));
+      f32x16 x[1];
+      chunk_pass<C, D, TERMS, 1, true>(p, t, lo, hi, rows, kbuf, vbuf, d0 + d, x, m, l);
+      store(d0 + d, x[0], m, sum_halves(l));
     }
   }
   if (dst) join_tree<C, O, ROWS, D>(p, t, tile, part, active, &shared);
@@ -819,7 +812,7 @@ hipError_t launch_dim(AttnParams& p, hipStream_t s) {
   p.splits = a.workspace ? splits_of(tiles, (a.table_width * a.page + unit - 1) / unit, kMaxParts) : 1;
   const dim3 grid((unsigned)(tiles * p.splits));
   if (chunks) {
-    hipLaunchKernelGGL((attn_chunk_kernel<C, O, D, 1>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((attn_chunk_kernel<C, O, D>), grid, dim3(chunk_threads(D)), 0, s, p);
   } else {
     hipLaunchKernelGGL((attn_rows_kernel<C, O, D>), grid, dim3(kThreads), 0, s, p);
   }
