@@ -61,17 +61,23 @@ constexpr int kChunkTile = 128;  // query rows of an attn_chunk workgroup
 constexpr int kBlock = 32;       // keys per step of an attn_rows wave
 constexpr int kFan = 16;         // parts joined at once
 constexpr int kMaxSplits = kFan * kFan;
-constexpr int kMaxParts = 512;   // parts of all tiles together
+constexpr int kMaxParts = 2048;  // parts of all tiles together
+constexpr int kMaxChunkParts = 512;
+constexpr int kLong = 16;
 constexpr int kCounters = kFan + 1;
 constexpr int64_t kHeader = (int64_t)kMaxParts * kCounters * 4;  // the counters, before the parts
 static_assert(kHeader % 256 == 0, "");
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// A wave holds 32 rows of Q and of O: at 256 columns those leave no room for a second wave on its SIMD, so two waves share
+// the rows, compute the scores both and take half of O's columns each.
+constexpr int chunk_threads(int dim) { return dim == 256 ? 512 : 256; }
+
 struct AttnParams {
   tq_paged_attn_args a;
   float scale2;  // scale * log2 e
-  int group, page_shift, splits, slots;
+  int group, page_shift, splits, slots, places;  // places: workgroups that the card holds at once
 };
 
 template <typename C>
@@ -187,6 +193,7 @@ __device__ __forceinline__ ACC pv_each(u32x4 v, const Frag<C>* p, Frag<C> seen, 
   return acc;
 }
 
+__device__ inline void in_order() { asm volatile("" ::: "memory"); }  // loads before it are issued before it
 __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- joining parts -------------------------------------------------------------------------------------------------
@@ -252,41 +259,55 @@ __device__ inline void finish(const AttnParams& p, const Tile& t, int row, int c
 }
 
 // Joins `count` parts from `src` on, into `dst` or, if that is NULL, into the output.
-template <typename C, typename O, int ROWS, int D>
+template <typename C, typename O, int ROWS, int D, int THREADS>
 __device__ void join(const AttnParams& p, const Tile& t, const float* src, int count, float* dst) {
   constexpr int64_t step = part_floats<ROWS, D>();
-  for (int i = threadIdx.x; i < t.rows * (D / 4); i += blockDim.x) {
-    const int row = i / (D / 4), col = i % (D / 4) * 4;
-    float ms[kFan], ls[kFan];
-    float4 os[kFan];
+  constexpr int ITEMS = ROWS == kRowsTile ? std::max(1, ROWS * (D / 4) / THREADS) : 1;  // groups of 4 columns that a thread asks for at once
+  const int all = t.rows * (D / 4);
+#pragma unroll 1
+  for (int first = threadIdx.x; first < all; first += ITEMS * THREADS) {
+    float ms[ITEMS][kFan], ls[ITEMS][kFan];
+    float4 os[ITEMS][kFan];
+    // Everything is asked for before the first use: a load goes to the memory that all XCDs share, 1 to 2 us away.  Past the
+    // last part and the last row it repeats the last.
 #pragma unroll
-    for (int e = 0; e < kFan; ++e) {  // everything is asked for before the first use; past the last part it repeats the last
-      const float* q = src + min(e, count - 1) * step;
-      ms[e] = get(q + row);
-      ls[e] = get(q + ROWS + row);
-      os[e] = get4(q + 2 * ROWS + row * D + col);
-    }
-    float m = -INFINITY, l = 0.f, o[4] = {};
+    for (int x = 0; x < ITEMS; ++x) {
+      const int i = min(first + x * THREADS, all - 1), row = i / (D / 4), col = i % (D / 4) * 4;
 #pragma unroll
-    for (int e = 0; e < kFan; ++e) m = fmaxf(m, ms[e]);
+      for (int e = 0; e < kFan; ++e) {
+        const float* q = src + min(e, count - 1) * step;
+        ms[x][e] = get(q + row);
+        ls[x][e] = get(q + ROWS + row);
+        os[x][e] = get4(q + 2 * ROWS + row * D + col);
+      }
+    }
+    in_order();
 #pragma unroll
-    for (int e = 0; e < kFan; ++e) {
-      const float w = e >= count || ms[e] == -INFINITY ? 0.f : exp2_(ms[e] - m);
-      if (e >= count || (w == 0.f && ls[e] == 0.f)) continue;  // (an infinite or NaN part keeps its say)
-      l = fmaf(w, ls[e], l);
-      o[0] = fmaf(w, os[e].x, o[0]), o[1] = fmaf(w, os[e].y, o[1]), o[2] = fmaf(w, os[e].z, o[2]), o[3] = fmaf(w, os[e].w, o[3]);
+    for (int x = 0; x < ITEMS; ++x) {
+      const int i = first + x * THREADS, row = i / (D / 4), col = i % (D / 4) * 4;
+      float m = -INFINITY, l = 0.f, o[4] = {};
+#pragma unroll
+      for (int e = 0; e < kFan; ++e) m = fmaxf(m, ms[x][e]);
+#pragma unroll
+      for (int e = 0; e < kFan; ++e) {
+        const float w = e >= count || ms[x][e] == -INFINITY ? 0.f : exp2_(ms[x][e] - m);
+        if (e >= count || (w == 0.f && ls[x][e] == 0.f)) continue;  // (an infinite or NaN part keeps its say)
+        l = fmaf(w, ls[x][e], l);
+        o[0] = fmaf(w, os[x][e].x, o[0]), o[1] = fmaf(w, os[x][e].y, o[1]), o[2] = fmaf(w, os[x][e].z, o[2]), o[3] = fmaf(w, os[x][e].w, o[3]);
+      }
+      if (i >= all) continue;
+      if (!dst) {
+        finish<C, O, D>(p, t, row, col, m, l, o);
+      } else {
+        put4(dst + 2 * ROWS + row * D + col, o);
+        if (col == 0) put(dst + row, m), put(dst + ROWS + row, l);
+      }
     }
-    if (!dst) {
-      finish<C, O, D>(p, t, row, col, m, l, o);
-      continue;
-    }
-    put4(dst + 2 * ROWS + row * D + col, o);
-    if (col == 0) put(dst + row, m), put(dst + ROWS + row, l);
   }
 }
 
 // Two-level join over the `active` parts of a tile; called by every one of them after it has stored its part.
-template <typename C, typename O, int ROWS, int D>
+template <typename C, typename O, int ROWS, int D, int THREADS>
 __device__ void join_tree(const AttnParams& p, const Tile& t, int64_t tile, int part, int active, int* shared) {
   uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
   unsigned* counters = reinterpret_cast<unsigned*>(ws) + tile * kCounters;
@@ -296,10 +317,10 @@ __device__ void join_tree(const AttnParams& p, const Tile& t, int64_t tile, int 
   float* joined = parts + ((int64_t)p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
   const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
   if (!last_of(counters + set, in_set, shared)) return;
-  join<C, O, ROWS, D>(p, t, mine + set * kFan * step, in_set, sets == 1 ? nullptr : joined + set * step);
+  join<C, O, ROWS, D, THREADS>(p, t, mine + set * kFan * step, in_set, sets == 1 ? nullptr : joined + set * step);
   if (sets == 1) return;
   if (!last_of(counters + kFan, sets, shared)) return;
-  join<C, O, ROWS, D>(p, t, joined, sets, nullptr);
+  join<C, O, ROWS, D, THREADS>(p, t, joined, sets, nullptr);
 }
 
 // ---- few rows ------------------------------------------------------------------------------------------------------
@@ -320,7 +341,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   if (t.rows <= 0) return;
   // blocks of 32 keys; every wave of a part has at least one
   const int first = t.begin / kBlock, blocks = t.end > 0 ? (t.end + kBlock - 1) / kBlock - first : 0;
-  const int active = max(1, min(p.splits, (blocks + kWaves - 1) / kWaves));
+  // Parts of equal length that fill the places once; of kLong blocks at most where sequences may differ in length, so that
+  // the longest does not hold up the end (32 streams of 2096 to 8192 keys, 128 columns: 144 us in one round, XX in parts of 16).
+  const int64_t tiles = (int64_t)p.slots * a.kv_heads, even = (blocks * tiles + p.places - 1) / p.places;
+  const int unit = (int)max((int64_t)kWaves, a.seqs == 1 ? even : min(even, (int64_t)kLong));
+  const int active = max(1, min(p.splits, (blocks + unit - 1) / unit));
   if (part >= active) return;
   const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
 
@@ -489,7 +514,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
       if (col == 0) put(dst + rr, M), put(dst + kRowsTile + rr, L);
     }
   }
-  if (dst) join_tree<C, O, kRowsTile, D>(p, t, tile, part, active, &shared);
+  if (dst) join_tree<C, O, kRowsTile, D, kThreads>(p, t, tile, part, active, &shared);
 }
 
 // ---- many rows -----------------------------------------------------------------------------------------------------
@@ -507,11 +532,6 @@ __device__ inline float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-__device__ inline void in_order() { asm volatile("" ::: "memory"); }  // reads before it are issued before it
-
-// A wave holds 32 rows of Q and of O: at 256 columns those leave no room for a second wave on its SIMD, so two waves share
-// the rows, compute the scores both and take half of O's columns each.
-constexpr int chunk_threads(int dim) { return dim == 256 ? 512 : 256; }
 constexpr int chunk_keys(int dim) { return dim == 256 ? 32 : 64; }  // keys of a tile: two tiles of K and V take 68 KB of LDS at most
 
 // Places in LDS, of 16-byte pieces.  A read of 16 bytes takes 16 lanes at a time from 64 banks, so 16 consecutive rows'
@@ -778,7 +798,7 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
       store(d0 + d, x[0], m, sum_halves(l));
     }
   }
-  if (dst) join_tree<C, O, ROWS, D>(p, t, tile, part, active, &shared);
+  if (dst) join_tree<C, O, ROWS, D, chunk_threads(D)>(p, t, tile, part, active, &shared);
 }
 
 // ---- host ----------------------------------------------------------------------------------------------------------
@@ -788,28 +808,29 @@ int64_t slots_of(int64_t tokens, int64_t seqs, int group, int rows, bool offsets
   return offsets ? tokens * group / rows + seqs : seqs * ((group + rows - 1) / rows);
 }
 
-// Parts per tile: enough workgroups to fill the card, none for tiles that fill it alone.
-int splits_of(int64_t tiles, int64_t units, int64_t target) {
-  if (tiles * 2 > target) return 1;
-  const int64_t s = std::min<int64_t>(target / tiles, units);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits));
-}
-
 // attn_chunk from 64 rows per sequence on.
 bool in_chunks(int64_t tokens, int64_t seqs, int group, int64_t max_len) {
   const int64_t longest = max_len > 0 ? std::min(max_len, tokens) : (tokens + seqs - 1) / seqs;
   return longest * group >= 64 && tokens > seqs;
 }
-int64_t parts_bytes(int rows, int dim) { return (int64_t)(kMaxParts + kMaxParts / kFan + kMaxParts) * rows * (dim + 2) * 4; }
+// `parts` and what joins them: one per kFan of a tile's.
+int64_t parts_bytes(int64_t parts, int rows, int dim) { return (parts + parts / 2 + kFan) * rows * (dim + 2) * 4; }
 
 template <typename C, typename O, int D>
 hipError_t launch_dim(AttnParams& p, hipStream_t s) {
   const auto& a = p.a;
   const bool chunks = in_chunks(a.tokens, a.seqs, p.group, a.max_len);
-  const int rows = chunks ? kChunkTile : kRowsTile, unit = chunks ? chunk_keys(D) : kWaves * kBlock;
-  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, rows, a.cu != nullptr);
-  const int64_t tiles = (int64_t)p.slots * a.kv_heads;
-  p.splits = a.workspace ? splits_of(tiles, (a.table_width * a.page + unit - 1) / unit, kMaxParts) : 1;
+  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, chunks ? kChunkTile : kRowsTile, a.cu != nullptr);
+  const int64_t tiles = (int64_t)p.slots * a.kv_heads, keys = a.table_width * a.page;
+  // Registers and LDS allow two workgroups of four waves per compute unit, one of eight (or of four at 256 columns).
+  p.places = D == 256 ? 256 : 512;
+  p.splits = 1;
+  if (a.workspace) {
+    const int64_t units = chunks ? (keys + chunk_keys(D) - 1) / chunk_keys(D) : (keys + kWaves * kBlock - 1) / (kWaves * kBlock);
+    // attn_chunk: parts only while they find free places; attn_rows decides in the kernel, from the lengths
+    const int64_t room = chunks ? p.places / tiles : kMaxParts / tiles;
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, units, kMaxSplits}));
+  }
   const dim3 grid((unsigned)(tiles * p.splits));
   if (chunks) {
     hipLaunchKernelGGL((attn_chunk_kernel<C, O, D>), grid, dim3(chunk_threads(D)), 0, s, p);
@@ -829,7 +850,8 @@ hipError_t launch_type(AttnParams& p, hipStream_t s) {
 int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int kv_heads, int dim) {
   if (tokens == 0) return 0;
   // whether attn_chunk runs depends on the lengths too: room for it where it may
-  return kHeader + parts_bytes(tokens > seqs && tokens * (heads / kv_heads) >= 64 ? kChunkTile : kRowsTile, dim);
+  const bool chunks = tokens > seqs && tokens * (heads / kv_heads) >= 64;
+  return kHeader + std::max(parts_bytes(kMaxParts, kRowsTile, dim), chunks ? parts_bytes(kMaxChunkParts, kChunkTile, dim) : 0);
 }
 
 hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
