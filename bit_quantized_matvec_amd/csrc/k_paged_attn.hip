@@ -198,27 +198,23 @@ __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- joining parts -------------------------------------------------------------------------------------------------
 
-// A part: m [ROWS], l [ROWS], O [ROWS][D].  Stores and loads go through to the level that all XCDs share.
+// A part: m [ROWS], l [ROWS], O [ROWS][D].  Stores and loads go through to the level that all XCDs share (sc1).
 template <int ROWS, int D>
-constexpr int64_t part_floats() {
-  return (int64_t)ROWS * (D + 2);
+constexpr int part_floats() {
+  return ROWS * (D + 2);
 }
-__device__ inline void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ inline float get(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ inline void put4(float* p, const float* v) {
-  uint64_t* q = reinterpret_cast<uint64_t*>(p);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t w = (uint64_t)__float_as_uint(v[2 * i]) | (uint64_t)__float_as_uint(v[2 * i + 1]) << 32;
-    __hip_atomic_store(q + i, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+struct Parts {
+  __amdgpu_buffer_rsrc_t r;
+  static constexpr int kThrough = 16;
+  __device__ Parts(const AttnParams& p)
+      : r(__builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(p.a.workspace) + kHeader, 0, (int)min(p.a.workspace_bytes - kHeader, (int64_t)INT32_MAX), 0x00027000)) {}
+  __device__ void put(int at, float v) const { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at * 4, 0, kThrough); }
+  __device__ void put4(int at, const float* v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, r, at * 4, 0, kThrough);
   }
-}
-__device__ inline float4 get4(const float* p) {
-  const uint64_t* q = reinterpret_cast<const uint64_t*>(p);
-  const uint64_t x = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const uint64_t y = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return {__uint_as_float((unsigned)x), __uint_as_float((unsigned)(x >> 32)), __uint_as_float((unsigned)y), __uint_as_float((unsigned)(y >> 32))};
-}
+  __device__ float get(int at) const { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, kThrough)); }
+  __device__ f32x4 get4(int at) const { return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at * 4, 0, kThrough)); }
+};
 
 // Called by the whole workgroup after its stores to the workspace: whether it is the last of `count` to arrive.  The
 // counter goes back to zero.
@@ -258,69 +254,69 @@ __device__ inline void finish(const AttnParams& p, const Tile& t, int row, int c
   if (p.a.lse && col == 0) p.a.lse[at] = l == 0.f ? -INFINITY : (m - Half<C>::kShift + log2f(l)) * kLn2;
 }
 
-// Joins `count` parts from `src` on, into `dst` or, if that is NULL, into the output.
+// Joins `count` parts from place `src` on, to the part at `dst` or, if that is negative, into the output.  `lds` has room for
+// 2 kFan ROWS values.
 template <typename C, typename O, int ROWS, int D, int THREADS>
-__device__ void join(const AttnParams& p, const Tile& t, const float* src, int count, float* dst) {
-  constexpr int64_t step = part_floats<ROWS, D>();
+__device__ void join(const AttnParams& p, const Tile& t, const Parts& parts, int src, int count, int dst, float* lds) {
+  constexpr int step = part_floats<ROWS, D>();
   constexpr int ITEMS = ROWS == kRowsTile ? std::max(1, ROWS * (D / 4) / THREADS) : 1;  // groups of 4 columns that a thread asks for at once
   const int all = t.rows * (D / 4);
+  f32x4 os[ITEMS][kFan];
+  auto ask = [&](int first) {  // everything before the first use: the memory is 1 to 2 us away
+#pragma unroll
+    for (int e = 0; e < kFan; ++e)
+      if (e < count)
+#pragma unroll
+        for (int x = 0; x < ITEMS; ++x) os[x][e] = parts.get4(src + e * step + 2 * ROWS + min(first + x * THREADS, all - 1) * 4);
+  };
+  int first = threadIdx.x;
+  ask(first);
+  for (int i = threadIdx.x; i < 2 * ROWS * count; i += THREADS) lds[i] = parts.get(src + i / (2 * ROWS) * step + i % (2 * ROWS));
+  __syncthreads();
 #pragma unroll 1
-  for (int first = threadIdx.x; first < all; first += ITEMS * THREADS) {
-    float ms[ITEMS][kFan], ls[ITEMS][kFan];
-    float4 os[ITEMS][kFan];
-    // Everything is asked for before the first use: a load goes to the memory that all XCDs share, 1 to 2 us away.  Past the
-    // last part and the last row it repeats the last.
+  while (first < all) {
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
-      const int i = min(first + x * THREADS, all - 1), row = i / (D / 4), col = i % (D / 4) * 4;
-#pragma unroll
-      for (int e = 0; e < kFan; ++e) {
-        const float* q = src + min(e, count - 1) * step;
-        ms[x][e] = get(q + row);
-        ls[x][e] = get(q + ROWS + row);
-        os[x][e] = get4(q + 2 * ROWS + row * D + col);
-      }
-    }
-    in_order();
-#pragma unroll
-    for (int x = 0; x < ITEMS; ++x) {
-      const int i = first + x * THREADS, row = i / (D / 4), col = i % (D / 4) * 4;
+      const int i = first + x * THREADS, row = min(i, all - 1) / (D / 4), col = i % (D / 4) * 4;
       float m = -INFINITY, l = 0.f, o[4] = {};
 #pragma unroll
-      for (int e = 0; e < kFan; ++e) m = fmaxf(m, ms[x][e]);
+      for (int e = 0; e < kFan; ++e)
+        if (e < count) m = fmaxf(m, lds[e * 2 * ROWS + row]);
 #pragma unroll
       for (int e = 0; e < kFan; ++e) {
-        const float w = e >= count || ms[x][e] == -INFINITY ? 0.f : exp2_(ms[x][e] - m);
-        if (e >= count || (w == 0.f && ls[x][e] == 0.f)) continue;  // (an infinite or NaN part keeps its say)
-        l = fmaf(w, ls[x][e], l);
-        o[0] = fmaf(w, os[x][e].x, o[0]), o[1] = fmaf(w, os[x][e].y, o[1]), o[2] = fmaf(w, os[x][e].z, o[2]), o[3] = fmaf(w, os[x][e].w, o[3]);
+        if (e >= count) continue;
+        const float me = lds[e * 2 * ROWS + row], le = lds[e * 2 * ROWS + ROWS + row], w = me == -INFINITY ? 0.f : exp2_(me - m);
+        if (w == 0.f && le == 0.f) continue;  // (an infinite or NaN part keeps its say)
+        l = fmaf(w, le, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = fmaf(w, os[x][e][j], o[j]);
       }
       if (i >= all) continue;
-      if (!dst) {
+      if (dst < 0) {
         finish<C, O, D>(p, t, row, col, m, l, o);
       } else {
-        put4(dst + 2 * ROWS + row * D + col, o);
-        if (col == 0) put(dst + row, m), put(dst + ROWS + row, l);
+        parts.put4(dst + 2 * ROWS + row * D + col, o);
+        if (col == 0) parts.put(dst + row, m), parts.put(dst + ROWS + row, l);
       }
     }
+    first += ITEMS * THREADS;
+    if (first < all) ask(first);
   }
 }
 
 // Two-level join over the `active` parts of a tile; called by every one of them after it has stored its part.
 template <typename C, typename O, int ROWS, int D, int THREADS>
-__device__ void join_tree(const AttnParams& p, const Tile& t, int64_t tile, int part, int active, int* shared) {
-  uint8_t* ws = static_cast<uint8_t*>(p.a.workspace);
-  unsigned* counters = reinterpret_cast<unsigned*>(ws) + tile * kCounters;
-  float* parts = reinterpret_cast<float*>(ws + kHeader);
-  const int64_t step = part_floats<ROWS, D>();
-  float* mine = parts + tile * p.splits * step;
-  float* joined = parts + ((int64_t)p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
+__device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts, int64_t tile, int part, int active, int* shared, float* lds) {
+  unsigned* counters = static_cast<unsigned*>(p.a.workspace) + tile * kCounters;
+  constexpr int step = part_floats<ROWS, D>();
+  const int mine = (int)tile * p.splits * step;
+  const int joined = (int)((int64_t)p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
   const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
   if (!last_of(counters + set, in_set, shared)) return;
-  join<C, O, ROWS, D, THREADS>(p, t, mine + set * kFan * step, in_set, sets == 1 ? nullptr : joined + set * step);
+  join<C, O, ROWS, D, THREADS>(p, t, parts, mine + set * kFan * step, in_set, sets == 1 ? -1 : joined + set * step, lds);
   if (sets == 1) return;
   if (!last_of(counters + kFan, sets, shared)) return;
-  join<C, O, ROWS, D, THREADS>(p, t, joined, sets, nullptr);
+  join<C, O, ROWS, D, THREADS>(p, t, parts, joined, sets, -1, lds);
 }
 
 // ---- few rows ------------------------------------------------------------------------------------------------------
@@ -490,9 +486,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(&stage[wave][r][16 * d + 4 * g]) = o[d];
   if (g == 0) stat[wave][0][r] = m, stat[wave][1][r] = l;
   __syncthreads();
-  float* dst = nullptr;
-  if (active > 1)
-    dst = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kHeader) + (tile * p.splits + part) * part_floats<kRowsTile, D>();
+  const Parts parts(p);
+  const int dst = active > 1 ? (int)(tile * p.splits + part) * part_floats<kRowsTile, D>() : -1;
   for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
     const int rr = i / (D / 4), col = i % (D / 4) * 4;
     float M = -INFINITY, L = 0.f, out[4] = {};
@@ -507,14 +502,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
 #pragma unroll
       for (int j = 0; j < 4; ++j) out[j] = fmaf(f, x[j], out[j]);
     }
-    if (!dst) {
+    if (dst < 0) {
       finish<C, O, D>(p, t, rr, col, M, L, out);
     } else {
-      put4(dst + 2 * kRowsTile + rr * D + col, out);
-      if (col == 0) put(dst + rr, M), put(dst + kRowsTile + rr, L);
+      parts.put4(dst + 2 * kRowsTile + rr * D + col, out);
+      if (col == 0) parts.put(dst + rr, M), parts.put(dst + kRowsTile + rr, L);
     }
   }
-  if (dst) join_tree<C, O, kRowsTile, D, kThreads>(p, t, tile, part, active, &shared);
+  if (dst >= 0) join_tree<C, O, kRowsTile, D, kThreads>(p, t, parts, tile, part, active, &shared, &stage[0][0][0]);
 }
 
 // ---- many rows -----------------------------------------------------------------------------------------------------
@@ -758,9 +753,8 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
       rows.q[kk] = __builtin_bit_cast(Frag<C>, x);
     }
   }
-  float* dst = nullptr;
-  if (active > 1)
-    dst = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kHeader) + (tile * p.splits + part) * part_floats<ROWS, D>();
+  const Parts parts(p);
+  const int dst = active > 1 ? (int)(tile * p.splits + part) * part_floats<ROWS, D>() : -1;
   auto store = [&](int d, const f32x16& o, float m, float sum) {
     const int in = wave * 32 + n;
     if (in >= t.rows) return;
@@ -768,11 +762,11 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
     for (int i = 0; i < 16; i += 4) {
       const int col = 32 * d + 2 * i + 4 * g;
       const float v[4] = {o[i], o[i + 1], o[i + 2], o[i + 3]};
-      if (!dst) {
+      if (dst < 0) {
         finish<C, O, D>(p, t, in, col, m, sum, v);
       } else {
-        put4(dst + 2 * ROWS + in * D + col, v);
-        if (col == 0) put(dst + in, m), put(dst + ROWS + in, sum);
+        parts.put4(dst + 2 * ROWS + in * D + col, v);
+        if (col == 0) parts.put(dst + in, m), parts.put(dst + ROWS + in, sum);
       }
     }
   };
@@ -798,7 +792,7 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
       store(d0 + d, x[0], m, sum_halves(l));
     }
   }
-  if (dst) join_tree<C, O, ROWS, D, chunk_threads(D)>(p, t, tile, part, active, &shared);
+  if (dst >= 0) join_tree<C, O, ROWS, D, chunk_threads(D)>(p, t, parts, tile, part, active, &shared, reinterpret_cast<float*>(kbuf));
 }
 
 // ---- host ----------------------------------------------------------------------------------------------------------
