@@ -77,7 +77,12 @@ constexpr int chunk_threads(int dim) { return dim == 256 ? 512 : 256; }
 struct AttnParams {
   tq_paged_attn_args a;
   float scale2;  // scale * log2 e
-  int group, page_shift, splits, slots, places;  // places: workgroups that the card holds at once
+  int group, page_shift, splits, slots;
+  int places_shift;  // log2 of the workgroups that the card holds at once
+  int tiles_each;    // tiles per sequence of one token
+  unsigned group_mul, group_shift;
+  // row / group for 0 <= row < 2^31
+  __device__ int token_of(int row) const { return (int)(__umulhi((unsigned)row << 1, group_mul) >> group_shift); }
 };
 
 template <typename C>
@@ -126,18 +131,14 @@ struct Tile {
 };
 
 template <int ROWS>
-__device__ inline Tile find_tile(const AttnParams& p, int64_t tile, int lane) {
+__device__ inline Tile find_tile(const AttnParams& p, int tile, int lane) {
   const auto& a = p.a;
   Tile r;
-  r.kvh = (int)(tile % a.kv_heads);
-  const int64_t slot = tile / a.kv_heads;
-  if (a.cu) {
-    r.b = find_seq(a.cu, a.seqs, p.group, ROWS, slot, lane);
-  } else {
-    r.b = slot / ((p.group + ROWS - 1) / ROWS);
-  }
+  const int slot = tile / (unsigned)a.kv_heads;
+  r.kvh = tile - slot * a.kv_heads;
+  r.b = a.cu ? find_seq(a.cu, a.seqs, p.group, ROWS, slot, lane) : p.tiles_each == 1 ? slot : slot / p.tiles_each;
   const SeqRange s = seq_range(a.cu, r.b, a.tokens, a.bad_flag);
-  const int64_t slot0 = a.cu ? first_slot(a.cu, r.b, p.group, ROWS) : r.b * ((p.group + ROWS - 1) / ROWS);
+  const int64_t slot0 = a.cu ? first_slot(a.cu, r.b, p.group, ROWS) : r.b * p.tiles_each;
   const int64_t row0 = (slot - slot0) * ROWS, all = (int64_t)s.n * p.group;
   r.t0 = s.t0;
   r.row0 = (int)row0;
@@ -145,21 +146,10 @@ __device__ inline Tile find_tile(const AttnParams& p, int64_t tile, int lane) {
   const int64_t want = a.kv_len[r.b], len = min(max(want, (int64_t)0), a.table_width << p.page_shift);
   if (want != len) raise_flag(a.bad_flag);
   r.first_pos = (int)(len - s.n);
-  const int lo = r.first_pos + r.row0 / p.group, hi = r.first_pos + (r.row0 + r.rows - 1) / p.group;
+  const int lo = r.first_pos + p.token_of(r.row0), hi = r.first_pos + p.token_of(max(0, r.row0 + r.rows - 1));
   r.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
   r.end = r.rows > 0 ? hi + 1 : 0;
   return r;
-}
-
-// The page of the 16 keys from k on; -1 if nobody sees its page or the table's entry is no page.
-__device__ inline int page_of(const AttnParams& p, const Tile& t, int k) {
-  if (k >= t.end || (k >> p.page_shift) < (t.begin >> p.page_shift)) return -1;
-  const int pg = p.a.block_table[t.b * p.a.table_stride + (k >> p.page_shift)];
-  if (pg < 0 || pg >= p.a.pages) {
-    raise_flag(p.a.bad_flag);
-    return -1;
-  }
-  return pg;
 }
 
 // acc += V P, where V values that are not finite reach the rows that see their keys and no other.
@@ -246,7 +236,7 @@ __device__ inline void store4(O* dst, const float* v) {
 // Final values of 4 columns of a row.
 template <typename C, typename O, int D>
 __device__ inline void finish(const AttnParams& p, const Tile& t, int row, int col, float m, float l, const float* o) {
-  const int r = t.row0 + row, i = r / p.group, h = t.kvh * p.group + r % p.group;
+  const int r = t.row0 + row, i = p.token_of(r), h = t.kvh * p.group + r - i * p.group;
   const int64_t at = (t.t0 + i) * p.a.heads + h;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
@@ -255,7 +245,7 @@ __device__ inline void finish(const AttnParams& p, const Tile& t, int row, int c
 }
 
 // Joins `count` parts from place `src` on, to the part at `dst` or, if that is negative, into the output.  `lds` has room for
-// 2 kFan ROWS values.
+// 2 (kFan + 1) ROWS values.
 template <typename C, typename O, int ROWS, int D, int THREADS>
 __device__ void join(const AttnParams& p, const Tile& t, const Parts& parts, int src, int count, int dst, float* lds) {
   constexpr int step = part_floats<ROWS, D>();
@@ -273,30 +263,39 @@ __device__ void join(const AttnParams& p, const Tile& t, const Parts& parts, int
   ask(first);
   for (int i = threadIdx.x; i < 2 * ROWS * count; i += THREADS) lds[i] = parts.get(src + i / (2 * ROWS) * step + i % (2 * ROWS));
   __syncthreads();
+  // each row's maximum and sum, and in the place of the parts' maxima their weights
+  float m = -INFINITY, l = 0.f;
+  if (threadIdx.x < ROWS) {
+    float* row = lds + threadIdx.x;
+    for (int e = 0; e < count; ++e) m = fmaxf(m, row[e * 2 * ROWS]);
+    for (int e = 0; e < count; ++e) {
+      const float w = row[e * 2 * ROWS] == -INFINITY ? 0.f : exp2_(row[e * 2 * ROWS] - m);
+      l = fmaf(w, row[e * 2 * ROWS + ROWS], l);
+      row[e * 2 * ROWS] = w;
+    }
+    lds[2 * ROWS * kFan + threadIdx.x] = m, lds[2 * ROWS * kFan + ROWS + threadIdx.x] = l;
+  }
+  __syncthreads();
 #pragma unroll 1
   while (first < all) {
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
       const int i = first + x * THREADS, row = min(i, all - 1) / (D / 4), col = i % (D / 4) * 4;
-      float m = -INFINITY, l = 0.f, o[4] = {};
-#pragma unroll
-      for (int e = 0; e < kFan; ++e)
-        if (e < count) m = fmaxf(m, lds[e * 2 * ROWS + row]);
+      float o[4] = {};
 #pragma unroll
       for (int e = 0; e < kFan; ++e) {
         if (e >= count) continue;
-        const float me = lds[e * 2 * ROWS + row], le = lds[e * 2 * ROWS + ROWS + row], w = me == -INFINITY ? 0.f : exp2_(me - m);
-        if (w == 0.f && le == 0.f) continue;  // (an infinite or NaN part keeps its say)
-        l = fmaf(w, le, l);
+        const float w = lds[e * 2 * ROWS + row];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = fmaf(w, os[x][e][j], o[j]);
       }
       if (i >= all) continue;
+      const float mr = lds[2 * ROWS * kFan + row], lr = lds[2 * ROWS * kFan + ROWS + row];
       if (dst < 0) {
-        finish<C, O, D>(p, t, row, col, m, l, o);
+        finish<C, O, D>(p, t, row, col, mr, lr, o);
       } else {
         parts.put4(dst + 2 * ROWS + row * D + col, o);
-        if (col == 0) parts.put(dst + row, m), parts.put(dst + ROWS + row, l);
+        if (col == 0) parts.put(dst + row, mr), parts.put(dst + ROWS + row, lr);
       }
     }
     first += ITEMS * THREADS;
@@ -306,11 +305,11 @@ __device__ void join(const AttnParams& p, const Tile& t, const Parts& parts, int
 
 // Two-level join over the `active` parts of a tile; called by every one of them after it has stored its part.
 template <typename C, typename O, int ROWS, int D, int THREADS>
-__device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts, int64_t tile, int part, int active, int* shared, float* lds) {
-  unsigned* counters = static_cast<unsigned*>(p.a.workspace) + tile * kCounters;
+__device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts, int tile, int part, int active, int* shared, float* lds) {
+  unsigned* counters = static_cast<unsigned*>(p.a.workspace) + (int64_t)tile * kCounters;
   constexpr int step = part_floats<ROWS, D>();
-  const int mine = (int)tile * p.splits * step;
-  const int joined = (int)((int64_t)p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
+  const int mine = tile * p.splits * step;
+  const int joined = (p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
   const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
   if (!last_of(counters + set, in_set, shared)) return;
   join<C, O, ROWS, D, THREADS>(p, t, parts, mine + set * kFan * step, in_set, sets == 1 ? -1 : joined + set * step, lds);
@@ -331,30 +330,30 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   __shared__ int shared;
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = blockIdx.x % p.splits;
-  const int64_t tile = blockIdx.x / p.splits;
+  const int tile = blockIdx.x / (unsigned)p.splits, part = blockIdx.x - tile * p.splits;
   const Tile t = find_tile<kRowsTile>(p, tile, lane);
   if (t.rows <= 0) return;
   // blocks of 32 keys; every wave of a part has at least one
   const int first = t.begin / kBlock, blocks = t.end > 0 ? (t.end + kBlock - 1) / kBlock - first : 0;
   // Parts of equal length that fill the places once; of kLong blocks at most where sequences may differ in length, so that
   // the longest does not hold up the end (32 streams of 2096 to 8192 keys, 128 columns: 144 us in one round, XX in parts of 16).
-  const int64_t tiles = (int64_t)p.slots * a.kv_heads, even = (blocks * tiles + p.places - 1) / p.places;
-  const int unit = (int)max((int64_t)kWaves, a.seqs == 1 ? even : min(even, (int64_t)kLong));
-  const int active = max(1, min(p.splits, (blocks + unit - 1) / unit));
-  if (part >= active) return;
-  const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
+  const int even = (int)(((int64_t)blocks * (p.slots * a.kv_heads) + (1 << p.places_shift) - 1) >> p.places_shift);
+  const unsigned unit = max(kWaves, a.seqs == 1 ? even : min(even, kLong));
+  const unsigned active = max(1u, min((unsigned)p.splits, (blocks + unit - 1) / unit));
+  if ((unsigned)part >= active) return;
+  const int each = blocks / active, more = blocks - each * active;  // the first `more` parts have one more
+  const int lo = first + each * part + min(part, more), hi = lo + each + (part < more ? 1 : 0);
 
   const int r = lane & 15, g = lane >> 4;
   const bool row_ok = r < t.rows;
   const int row = t.row0 + (row_ok ? r : 0);
-  const int pos = t.first_pos + row / p.group;
+  const int token = p.token_of(row), pos = t.first_pos + token;
   const int least = a.window > 0 ? pos - a.window + 1 : 0;  // first key that this row sees
-  const int pos_lo = t.first_pos + t.row0 / p.group, pos_hi = t.end - 1;
+  const int pos_lo = t.first_pos + p.token_of(t.row0), pos_hi = t.end - 1;
 
   Frag<C> q[KK];
   {
-    const C* src = static_cast<const C*>(a.q) + (t.t0 + row / p.group) * a.q_token + (int64_t)(t.kvh * p.group + row % p.group) * a.q_head + 8 * g;
+    const C* src = static_cast<const C*>(a.q) + (t.t0 + token) * a.q_token + (int64_t)(t.kvh * p.group + row - token * p.group) * a.q_head + 8 * g;
     const Frag<C> zero = {};
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) q[kk] = row_ok ? *reinterpret_cast<const Frag<C>*>(src + 32 * kk) : zero;
@@ -363,10 +362,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   const C* kc = static_cast<const C*>(a.k_cache);
   const C* vc = static_cast<const C*>(a.v_cache);
   u32x4 k[2][KK], v[DT];
-  int pages[2];
+  // Pages of the two halves of a block's keys, -1 where the table's entry is no page.  Entries outside those of keys that
+  // somebody sees are not read.
+  int pages[2], ahead[2];
+  const int32_t* table = a.block_table + t.b * a.table_stride;
   auto look = [&](int block) {
-    pages[0] = page_of(p, t, block * kBlock);
-    pages[1] = page_of(p, t, block * kBlock + 16);
+    const int low = t.begin >> p.page_shift, high = (t.end - 1) >> p.page_shift;
+    int x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[h] = table[min(max((block * kBlock + 16 * h) >> p.page_shift, low), high)];
+    if (min(x[0], x[1]) < 0 || max(x[0], x[1]) >= a.pages) raise_flag(a.bad_flag);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ahead[h] = x[h] < 0 || x[h] >= a.pages ? -1 : x[h];
   };
   auto load_k = [&](int block) {  // A row r of tile c is key 8 (r / 4) + 4 c + r % 4
     const int pg = max(r < 8 ? pages[0] : pages[1], 0);
@@ -393,8 +400,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   auto begin = [&]() {
     if (block < hi) {
       look(block);
+      pages[0] = ahead[0], pages[1] = ahead[1];
       load_k(block);
       load_v(block);
+      look(block + kWaves);
     }
   };
   bool careful = false;
@@ -409,8 +418,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
       for (int kk = 0; kk < KK; ++kk) s[c] = H::mma(__builtin_bit_cast(Frag<C>, k[c][kk]), q[kk], s[c]);
     }
     if (next < hi) {
-      look(next);
+      pages[0] = ahead[0], pages[1] = ahead[1];
       load_k(next);
+      look(next + kWaves);  // a block ahead of its use
     }
     float x[8];
 #pragma unroll
@@ -487,7 +497,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   if (g == 0) stat[wave][0][r] = m, stat[wave][1][r] = l;
   __syncthreads();
   const Parts parts(p);
-  const int dst = active > 1 ? (int)(tile * p.splits + part) * part_floats<kRowsTile, D>() : -1;
+  const int dst = active > 1 ? (tile * p.splits + part) * part_floats<kRowsTile, D>() : -1;
   for (int i = threadIdx.x; i < t.rows * (D / 4); i += kThreads) {
     const int rr = i / (D / 4), col = i % (D / 4) * 4;
     float M = -INFINITY, L = 0.f, out[4] = {};
@@ -604,7 +614,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
   int pg = look(lo), next_pg = -1;
   if (lo < hi) fetch(lo, pg, 0);
   next_pg = look(lo + 1);
-  const int pos_lo = t.first_pos + t.row0 / p.group, pos_hi = t.end - 1;
+  const int pos_lo = t.first_pos + p.token_of(t.row0), pos_hi = t.end - 1;
 #pragma unroll 1
   for (int tile = lo, buf = 0; tile < hi; ++tile, buf ^= 1) {
     // the tile has arrived, and every wave has left the other buffer
@@ -723,28 +733,30 @@ template <typename C, typename O, int D>
 __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnParams p) {
   constexpr int KT = chunk_keys(D), KK = D / 16, DT = D / 32 * 256 / chunk_threads(D), ROWS = kChunkTile;
   constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
-  __shared__ __attribute__((aligned(128))) C kbuf[2 * KT * D], vbuf[2 * v_values(D)];
+  __shared__ __attribute__((aligned(128))) C buffers[2 * (KT * D + v_values(D))];
+  C *kbuf = buffers, *vbuf = buffers + 2 * KT * D;
   __shared__ int shared;
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = waves & 3, n = lane & 31, g = lane >> 5;
   const int d0 = waves / 4 * DT;  // this wave's first 32 columns
-  const int part = blockIdx.x % p.splits;
-  const int64_t tile = blockIdx.x / p.splits;
+  const int tile = blockIdx.x / (unsigned)p.splits, part = blockIdx.x - tile * p.splits;
   const Tile t = find_tile<ROWS>(p, tile, lane);
   if (t.rows <= 0) return;
   const int first = t.begin / KT, blocks = t.end > 0 ? (t.end + KT - 1) / KT - first : 0;
   const int active = max(1, min(p.splits, blocks));
   if (part >= active) return;
-  const int lo = first + (int)((int64_t)blocks * part / active), hi = first + (int)((int64_t)blocks * (part + 1) / active);
+  const int each = (unsigned)blocks / (unsigned)active, more = blocks - each * active;  // the first `more` parts have one more
+  const int lo = first + each * part + min(part, more), hi = lo + each + (part < more ? 1 : 0);
 
   ChunkRows<C, D> rows;
   {
     const int in = wave * 32 + n;
     const bool ok = in < t.rows;
     const int row = t.row0 + (ok ? in : 0);
-    rows.pos = t.first_pos + row / p.group;
+    const int token = p.token_of(row);
+    rows.pos = t.first_pos + token;
     rows.least = a.window > 0 ? rows.pos - a.window + 1 : 0;
-    const C* src = static_cast<const C*>(a.q) + (t.t0 + row / p.group) * a.q_token + (int64_t)(t.kvh * p.group + row % p.group) * a.q_head + 8 * g;
+    const C* src = static_cast<const C*>(a.q) + (t.t0 + token) * a.q_token + (int64_t)(t.kvh * p.group + row - token * p.group) * a.q_head + 8 * g;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       u32x4 x = *reinterpret_cast<const u32x4*>(src + 16 * kk);
@@ -754,7 +766,7 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
     }
   }
   const Parts parts(p);
-  const int dst = active > 1 ? (int)(tile * p.splits + part) * part_floats<ROWS, D>() : -1;
+  const int dst = active > 1 ? (tile * p.splits + part) * part_floats<ROWS, D>() : -1;
   auto store = [&](int d, const f32x16& o, float m, float sum) {
     const int in = wave * 32 + n;
     if (in >= t.rows) return;
@@ -792,7 +804,8 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
       store(d0 + d, x[0], m, sum_halves(l));
     }
   }
-  if (dst >= 0) join_tree<C, O, ROWS, D, chunk_threads(D)>(p, t, parts, tile, part, active, &shared, reinterpret_cast<float*>(kbuf));
+  if (dst >= 0) join_tree<C, O, ROWS, D, chunk_threads(D)>(p, t, parts, tile, part, active, &shared, reinterpret_cast<float*>(buffers));
+  static_assert(sizeof(buffers) >= 2 * (kFan + 1) * ROWS * 4, "");
 }
 
 // ---- host ----------------------------------------------------------------------------------------------------------
@@ -817,12 +830,14 @@ hipError_t launch_dim(AttnParams& p, hipStream_t s) {
   p.slots = (int)slots_of(a.tokens, a.seqs, p.group, chunks ? kChunkTile : kRowsTile, a.cu != nullptr);
   const int64_t tiles = (int64_t)p.slots * a.kv_heads, keys = a.table_width * a.page;
   // Registers and LDS allow two workgroups of four waves per compute unit, one of eight (or of four at 256 columns).
-  p.places = D == 256 ? 256 : 512;
+  p.places_shift = D == 256 ? 8 : 9;
+  const int rows = chunks ? kChunkTile : kRowsTile;
+  p.tiles_each = (p.group + rows - 1) / rows;
   p.splits = 1;
   if (a.workspace) {
     const int64_t units = chunks ? (keys + chunk_keys(D) - 1) / chunk_keys(D) : (keys + kWaves * kBlock - 1) / (kWaves * kBlock);
     // attn_chunk: parts only while they find free places; attn_rows decides in the kernel, from the lengths
-    const int64_t room = chunks ? p.places / tiles : kMaxParts / tiles;
+    const int64_t room = chunks ? (1 << p.places_shift) / tiles : kMaxParts / tiles;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, units, kMaxSplits}));
   }
   const dim3 grid((unsigned)(tiles * p.splits));
@@ -854,6 +869,10 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   p.scale2 = a.scale * kLog2e;
   p.group = a.heads / a.kv_heads;
   p.page_shift = __builtin_ctz(a.page);
+  // row / group = row * ceil(2^(31 + s) / group) >> (31 + s) with 2^s >= group: 2 row times that, its high word, >> s
+  const int sh = p.group == 1 ? 0 : 32 - __builtin_clz(p.group - 1);
+  const uint64_t mul = ((uint64_t(1) << (31 + sh)) + p.group - 1) / p.group;
+  p.group_mul = (unsigned)mul, p.group_shift = (unsigned)sh;
   if (in_chunks(a.tokens, a.seqs, p.group, a.max_len)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
   if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch_type<bf16, float>(p, s) : launch_type<bf16, bf16>(p, s);
   return a.out_type == TQ_F32 ? launch_type<f16, float>(p, s) : launch_type<f16, f16>(p, s);
