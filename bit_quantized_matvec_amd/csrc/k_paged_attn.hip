@@ -311,11 +311,12 @@ __device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts
   const int mine = tile * p.splits * step;
   const int joined = (p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
   const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
-  if (!last_of(counters + set, in_set, shared)) return;
-  join<C, O, ROWS, D, THREADS>(p, t, parts, mine + set * kFan * step, in_set, sets == 1 ? -1 : joined + set * step, lds);
-  if (sets == 1) return;
-  if (!last_of(counters + kFan, sets, shared)) return;
-  join<C, O, ROWS, D, THREADS>(p, t, parts, joined, sets, -1, lds);
+  int counter = set, src = mine + set * kFan * step, count = in_set, dst = sets == 1 ? -1 : joined + set * step;
+  while (last_of(counters + counter, count, shared)) {
+    join<C, O, ROWS, D, THREADS>(p, t, parts, src, count, dst, lds);
+    if (dst < 0) return;
+    counter = kFan, src = joined, count = sets, dst = -1;
+  }
 }
 
 // ---- few rows ------------------------------------------------------------------------------------------------------
@@ -368,12 +369,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   const int32_t* table = a.block_table + t.b * a.table_stride;
   auto look = [&](int block) {
     const int low = t.begin >> p.page_shift, high = (t.end - 1) >> p.page_shift;
-    int x[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) x[h] = table[min(max((block * kBlock + 16 * h) >> p.page_shift, low), high)];
-    if (min(x[0], x[1]) < 0 || max(x[0], x[1]) >= a.pages) raise_flag(a.bad_flag);
+    for (int h = 0; h < 2; ++h) ahead[h] = table[min(max((block * kBlock + 16 * h) >> p.page_shift, low), high)];
+  };
+  auto turn = [&]() {  // (not right after look(): a check there would wait for the entries and for everything asked for before)
+    if (min(ahead[0], ahead[1]) < 0 || max(ahead[0], ahead[1]) >= a.pages) raise_flag(a.bad_flag);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) ahead[h] = x[h] < 0 || x[h] >= a.pages ? -1 : x[h];
+    for (int h = 0; h < 2; ++h) pages[h] = ahead[h] < 0 || ahead[h] >= a.pages ? -1 : ahead[h];
   };
   auto load_k = [&](int block) {  // A row r of tile c is key 8 (r / 4) + 4 c + r % 4
     const int pg = max(r < 8 ? pages[0] : pages[1], 0);
@@ -400,7 +402,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   auto begin = [&]() {
     if (block < hi) {
       look(block);
-      pages[0] = ahead[0], pages[1] = ahead[1];
+      turn();
       load_k(block);
       load_v(block);
       look(block + kWaves);
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
       for (int kk = 0; kk < KK; ++kk) s[c] = H::mma(__builtin_bit_cast(Frag<C>, k[c][kk]), q[kk], s[c]);
     }
     if (next < hi) {
-      pages[0] = ahead[0], pages[1] = ahead[1];
+      turn();
       load_k(next);
       look(next + kWaves);  // a block ahead of its use
     }
