@@ -20,6 +20,9 @@ LIB = os.path.join(HERE, "libtq.so")
 # out of the product library
 PROBE_LIB = os.path.join(HERE, "libtq_probe.so")
 PROBE_SOURCES = ["hbm_probe.hip"]
+# argument checks of the ordinary call (binding.cpp): host code against torch's headers
+BINDING = os.path.join(HERE, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["tq_api.cpp", "k_workspace.hip", "scratch.hip", "k_quant.hip", "k_repack.hip", "k_gemv_pq2.hip", "k_gemm_pq2.hip", "k_gemv_ptq1.hip", "k_gemm_ptq1.hip",
@@ -47,14 +50,34 @@ def _compile(src: str, out: str, extra=()) -> None:
         sys.stderr.write(err + "\n")
 
 
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f for i in inc for f in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", LIB, f"-L{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for binding.cpp:\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory() as tmp:
         objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
         with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 4)) as ex:
             list(ex.map(lambda a: _compile(a[0], a[1], EXTRA.get(a[0], ())), zip(SOURCES, objs)))
         tmp_lib = LIB + ".tmp"
-        subprocess.check_call([HIPCC, "-shared", f"--offload-arch={ARCH}", *objs, "-o", tmp_lib])
+        subprocess.check_call([HIPCC, "-shared", f"--offload-arch={ARCH}", "-Wl,-soname,libtq.so", *objs, "-o", tmp_lib])
         os.replace(tmp_lib, LIB)
+        _build_binding()
         pobjs = [os.path.join(tmp, s + ".o") for s in PROBE_SOURCES]
         for src, obj in zip(PROBE_SOURCES, pobjs):
             _compile(src, obj)
@@ -62,7 +85,7 @@ def build(verbose: bool = False) -> str:
         subprocess.check_call([HIPCC, "-shared", f"--offload-arch={ARCH}", *pobjs, "-o", tmp_lib])
         os.replace(tmp_lib, PROBE_LIB)
     if verbose:
-        print("built", LIB, "and", PROBE_LIB)
+        print("built", LIB, BINDING, "and", PROBE_LIB)
     return LIB
 
 
