@@ -375,6 +375,7 @@ __device__ inline void in_order() { asm volatile("" ::: "memory"); }  // loads b
 template <typename IN, typename O, int DK>
 __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p) {
   constexpr int KS = DK / 32, HT = KS / 2, TK = terms_in<IN>(), OT = sizeof(O) == 4 ? 3 : 2;
+  constexpr int AHEAD = TK == 1 ? 1 : 0;  // reads of right operands ahead of their products: where the left ones leave registers
   // right operands: the state, R and X with the decays to the chunk's end; X itself, the 8 values of an operand's lane together
   __shared__ __attribute__((aligned(16))) frag sf[KS][2][3][64], rf[2][2][3][64], zf[2][2][3][64];
   __shared__ __attribute__((aligned(16))) float xs[2][2][64][8], sums[2][4][2][32], norms[2][4][4];
@@ -568,17 +569,17 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
           // K S: each operand is read while the one before it is multiplied
           f32x4 y[2] = {}, y2[2] = {};
           {
-            frag f[2][2][3];
+            frag f[AHEAD + 1][2][3];
             auto read = [&](int k) {
 #pragma unroll
               for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 3; ++e) f[k & 1][m][e] = sf[k][m][e][lane];
+                for (int e = 0; e < 3; ++e) f[k & AHEAD][m][e] = sf[k][m][e][lane];
             };
-            read(0);
+            if (AHEAD) read(0);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-              if (k + 1 < KS) read(k + 1);
+              if (k + AHEAD < KS) read(k + AHEAD);
               in_order();
 #pragma unroll
               for (int i = 0; i < TK; ++i)
@@ -586,7 +587,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
                 for (int e = 0; e < 3; ++e)
 #pragma unroll
                   for (int m = 0; m < 2; ++m)
-                    if (i + e < 3) (k & 1 ? y2 : y)[m] = mma(kf[k][i], f[k & 1][m][e], (k & 1 ? y2 : y)[m]);
+                    if (i + e < 3) (k & 1 ? y2 : y)[m] = mma(kf[k][i], f[k & AHEAD][m][e], (k & 1 ? y2 : y)[m]);
             }
           }
           // R = beta V - far_k (K S)
@@ -631,9 +632,10 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
 #pragma unroll
             for (int m = 0; m < 2; ++m) y[m] = f32x4{}, y2[m] = f32x4{};
             read(0);
-            if (s2) read(1);
+            if (s2 && AHEAD) read(1);
             in_order();
             product(0);
+            if (s2 && !AHEAD) read(1);
             if (s2) product(1);
           }
 #pragma unroll
@@ -653,16 +655,18 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
 #pragma unroll
             for (int m = 0; m < 2; ++m) s[t][m] *= decay;
           {
-            frag f[2][2][3];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
+            frag f[AHEAD + 1][2][3];
+            auto read = [&](int k) {
 #pragma unroll
               for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 3; ++e) f[k][m][e] = zf[k][m][e][lane];
-            in_order();
+                for (int e = 0; e < 3; ++e) f[k & AHEAD][m][e] = zf[k][m][e][lane];
+            };
+            if (AHEAD) read(0);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+              if (k + AHEAD < 2) read(k + AHEAD);
+              in_order();
 #pragma unroll
               for (int i = 0; i < TK; ++i)
 #pragma unroll
@@ -671,7 +675,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
                   for (int t = 0; t < HT; ++t)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
-                      if (i + e < 3) s[t][m] = mma(xf[t][k][i], f[k][m][e], s[t][m]);
+                      if (i + e < 3) s[t][m] = mma(xf[t][k][i], f[k & AHEAD][m][e], s[t][m]);
+            }
           }
           if (!odd) put_state();
           load_x();
