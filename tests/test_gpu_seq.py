@@ -542,3 +542,113 @@ def test_runs_on_the_current_stream(tq, n):
         block(tq, s)
     side.synchronize()
     assert all(torch.equal(s[k], want[k]) for k in NAMES)
+
+
+# ---- the two ways into a call ---------------------------------------------------------------------------------------
+
+def test_output_given_or_made(tq):
+    """A call with `out` is checked in C++, one without in Python: the same results."""
+    s = block_state(tq, 20, 7)
+    block(tq, s)
+    want = {k: s[k].clone() for k in NAMES}
+    q = tq.rope_append(s["q"], s["k"], s["v"], s["pos"], s["slots"], s["freq"], s["kc"], s["vc"])
+    o = tq.paged_attn(q, s["kc"], s["vc"], s["table"], s["len"], s["cu"], max_len=20, out_dtype=F32, ws=s["ws"])
+    go = tq.gdn(s["gq"], s["gk"], s["gv"], s["g"], s["beta"], s["state"], s["cu"], l2norm=True, max_len=20, state_out=s["after"], ws=s["gws"])
+    torch.cuda.synchronize()
+    for name, got in (("qo", q), ("o", o), ("go", go), ("kc", s["kc"]), ("vc", s["vc"]), ("after", s["after"])):
+        assert torch.equal(got, want[name]), name
+
+
+@pytest.mark.parametrize("over,error", [
+    (dict(q="double"), ValueError), (dict(k="bfloat16"), ValueError), (dict(k="cpu"), ValueError), (dict(pos="long"), ValueError),
+    (dict(slots="int"), ValueError), (dict(slots=None), ValueError), (dict(freq="float"), ValueError), (dict(kc="float"), ValueError),
+    (dict(vc="cpu"), ValueError), (dict(qo="float"), ValueError), (dict(q="shifted"), RuntimeError), (dict(eps=-1.0), RuntimeError),
+    (dict(layout="pairs"), ValueError), (dict(v="narrow"), RuntimeError),
+])
+def test_rope_append_refuses_with_output_given(tq, over, error):
+    s = {**block_state(tq, 5, 3), "eps": 1e-6, "layout": "half"}
+    for name, how in over.items():
+        if how == "shifted":  # rows that do not start at 16 bytes
+            s[name] = torch.zeros(s[name].numel() + 8, device="cuda")[1 : 1 + s[name].numel()].view(s[name].shape)
+        elif how == "narrow":
+            s[name] = s[name][..., :64].contiguous()
+        elif isinstance(how, str) and name != "layout":
+            s[name] = getattr(s[name], how)()
+        else:
+            s[name] = how
+    before = [s[x].clone() for x in ("qo", "kc", "vc")]
+    with pytest.raises(error):
+        tq.rope_append(s["q"], s["k"], s["v"], s["pos"], s["slots"], s["freq"], s["kc"], s["vc"], eps=s["eps"], layout=s["layout"], out=s["qo"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, s[y]) for x, y in zip(before, ("qo", "kc", "vc")))
+
+
+@pytest.mark.parametrize("over,error", [
+    (dict(qo="half"), RuntimeError), (dict(table="long"), ValueError), (dict(table="cpu"), ValueError), (dict(len="long"), ValueError),
+    (dict(cu="long"), ValueError), (dict(o="half"), RuntimeError), (dict(ws="float"), ValueError), (dict(window=-1), RuntimeError),
+    (dict(scale=math.inf), RuntimeError), (dict(n=-1), RuntimeError), (dict(vc="cpu"), ValueError),
+])
+def test_paged_attn_refuses_with_output_given(tq, over, error):
+    s = {**block_state(tq, 5, 3), "window": 0, "scale": None}
+    for name, how in over.items():
+        s[name] = getattr(s[name], how)() if isinstance(how, str) else how
+    before = s["o"].clone()
+    with pytest.raises(error):
+        tq.paged_attn(s["qo"], s["kc"], s["vc"], s["table"], s["len"], s["cu"], scale=s["scale"], window=s["window"], max_len=s["n"], out=s["o"], ws=s["ws"])
+    torch.cuda.synchronize()
+    assert torch.equal(before, s["o"])
+
+
+@pytest.mark.parametrize("over,error", [
+    (dict(gq="double"), ValueError), (dict(gk="half"), ValueError), (dict(g="cpu"), ValueError), (dict(beta="double"), ValueError),
+    (dict(state="half"), ValueError), (dict(cu="long"), ValueError), (dict(go="half"), RuntimeError), (dict(n=-1), RuntimeError),
+    (dict(scale=math.nan), RuntimeError), (dict(gws="float"), ValueError), (dict(after="cpu"), ValueError),
+])
+def test_gdn_refuses_with_output_given(tq, over, error):
+    s = {**block_state(tq, 150, 3), "scale": None}
+    for name, how in over.items():
+        s[name] = getattr(s[name], how)() if isinstance(how, str) else how
+    before = s["go"].clone()
+    with pytest.raises(error):
+        tq.gdn(s["gq"], s["gk"], s["gv"], s["g"], s["beta"], s["state"], s["cu"], scale=s["scale"], l2norm=True, max_len=s["n"], out=s["go"],
+               state_out=s["after"], ws=s["gws"])
+    torch.cuda.synchronize()
+    assert torch.equal(before, s["go"])
+
+
+# ---- long caches -----------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("new,keys,hq,hk,d,page,ct,ot,window", [
+    (1, 70_001, 6, 1, 256, 64, BF, F32, 0),     # joined in two levels
+    (1, 33_000, 16, 2, 128, 16, HF, HF, 0),
+    (1, 33_000, 17, 1, 64, 16, HF, F32, 30_000),
+    (33, 20_000, 4, 1, 128, 64, BF, BF, 0),     # two tiles of 128 rows, split
+    (70, 9_000, 2, 1, 256, 32, HF, F32, 5_000),
+    (300, 5_000, 8, 4, 64, 128, BF, F32, 0),
+])
+def test_paged_attn_long(tq, new, keys, hq, hk, d, page, ct, ot, window):
+    """Against float64 on the GPU: whole matrices, from the definition."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(keys)
+    pages = -(-keys // page)
+    table = torch.randperm(pages, generator=g, device="cuda")
+    q = torch.randn(new, hq, d, generator=g, device="cuda").to(ct)
+    kc, vc = torch.randn(pages, hk, page, d, generator=g, device="cuda").to(ct), torch.randn(pages, hk, d, page, generator=g, device="cuda").to(ct)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lse = torch.empty(new, hq, device="cuda")
+    got = tq.paged_attn(q, kc, vc, table.int()[None], ints([keys]), ints([0, new]), window=window, max_len=new, out_dtype=ot, lse=lse,
+                        ws=tq.attn_workspace(new, 1, hq, hk, d))
+    pos = torch.arange(keys - new, keys, device="cuda")[:, None]
+    key = torch.arange(keys, device="cuda")[None]
+    hide = (key > pos) | ((key <= pos - window) if window else False)
+    for h in range(hq):
+        k = kc[table, h // (hq // hk)].flatten(0, 1)[:keys].double()
+        v = vc[table, h // (hq // hk)].transpose(1, 2).flatten(0, 1)[:keys].double()
+        x = q[:, h].double()
+        s = (x @ k.t() * d**-0.5).masked_fill(hide, -math.inf)
+        size = (x.abs() @ k.abs().t() * d**-0.5).masked_fill(hide, 0).amax(-1)
+        p = torch.softmax(s, -1)
+        want, spread = p @ v, p @ v.abs()
+        near(got[:, h], want.cpu(), so.attention_bound(want.cpu(), spread.cpu(), size.cpu(), d, keys, ot, ct), f"head {h}")
+        wl = torch.logsumexp(s, -1).cpu()
+        near(lse[:, h], wl, ((d + 4) * size.cpu() + keys + 16 + wl.abs()) * so.U32, f"lse {h}")
