@@ -11,7 +11,10 @@
 // sums over rows are 8 lanes wide in a wave and then 4 waves wide through LDS,
 // which is double-buffered, so a token costs one barrier.
 //
-// Bound, one token: bytes of the state, read once and written once.
+// Bound, one token: bytes of the state, read once and written once: 64
+// sequences x 48 heads of 128 x 128, 403 MB, 78 us = 5.2 TB/s, what a large copy
+// reaches; one sequence 4.5 us, the launch.  Long sequences go in chunks
+// (k_gdn_chunk.hip); token after token 4096 of them take 6063 us.
 #include <algorithm>
 
 #include "seq.h"

@@ -37,6 +37,15 @@
 // every row of a matrix product.  A chunk with any in q, k, v, beta or with
 // g > 0 is walked token after token instead (as are sequences of less than
 // kStepLen tokens).
+//
+// Bound.  The walk: one chunk after another on 4 SIMDs per 32 columns, 2.4 us a
+// chunk at bf16, of which the matrix units take 0.7: splitting into terms, LDS
+// between the products and three barriers are the rest.  4096 bf16 tokens, 48
+// heads of 128 x 128: 188 us, 53 of them in the first kernel (166 MB written);
+// token after token 6063.  Five fp32 sequences of 77 to 701 tokens: 189 us (1290).
+// What else was measured at the first: one wave per 16 columns without LDS 1777
+// us (its loads wait one by one), eight waves of 16 columns that all do the same
+// 264, four waves that compute the outputs too 251.
 #include <algorithm>
 #include <cstddef>
 
@@ -47,7 +56,7 @@ namespace tq {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr int kStepLen = 24;
+constexpr int kStepLen = 16;  // tokens from which a chunk is worth its first kernel
 constexpr int kPrepThreads = 256;
 constexpr int64_t kBudget = int64_t(256) << 20;  // workspace: what the last-level cache holds
 constexpr int kFragBytes = 1024;
@@ -140,7 +149,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
   const int h = blockIdx.x % a.v_heads, group = a.v_heads / a.k_heads, kh = h / group;
   const int64_t slot = blockIdx.x / a.v_heads;
-  const int64_t b = p.whole ? find_seq(a.cu, a.seqs, 1, kChunk, slot, lane) : p.seq0 + slot / p.chunks;
+  const int64_t b = p.whole ? find_seq(a.cu, a.seqs, 1, kChunk, 1, slot, lane) : p.seq0 + slot / p.chunks;
   const SeqRange r = seq_range(a.cu, b, a.tokens, nullptr);
   const int64_t c = p.whole ? slot - (r.t0 / kChunk + b) : p.chunk0 + slot % p.chunks;
   if (r.n < kStepLen || c < 0 || c * kChunk >= r.n) return;

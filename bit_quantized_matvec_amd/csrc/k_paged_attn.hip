@@ -16,12 +16,15 @@
 // consecutive keys at a time.
 //
 // Rounding.  Q, K, V enter as they are; products are exact and summed in
-// fp32.  P enters the second product in the cache's type when the output has
-// that type, and as 2 (fp16) or 3 (bf16) terms whose sum holds 22 or 24 bits
-// when the output is fp32.  fp16 P is scaled by 2^11 (removed by the division
-// by l, which carries it too), so that small probabilities stay normal.  attn_chunk
-// moves a row's maximum, and so rescales O, only when a score passes it by more
-// than kSlack (base 2): P is at most 2^kSlack, 2^15 with the scaling in fp16.
+// fp32.  P enters the second product as 2 (fp16) or 3 (bf16) terms whose sum
+// holds 22 or 24 bits when the output is fp32.  When the output has the cache's
+// type, attn_rows, which waits for memory anyway, takes 2 terms (16 or 22 bits),
+// and attn_chunk, bound by the matrix units, one: half a step of that type per
+// probability, independent over the keys, beside the output's own half step.
+// fp16 P is scaled by 2^11 (removed by the division by l, which carries it
+// too), so that small probabilities stay normal.  attn_chunk moves a row's
+// maximum, and so rescales O, only when a score passes it by more than kSlack
+// (base 2): P is at most 2^kSlack, 2^15 with the scaling in fp16.
 //
 // Unseen keys.  Their scores become -inf; their V values are made zero where
 // no row of the workgroup sees them, as 0 * NaN would spoil a sum.  A value
@@ -36,14 +39,25 @@
 //   attn_rows    16 query rows per workgroup, 4 waves that each take every
 //                fourth block of 32 keys straight from memory to registers; no
 //                LDS before the waves are joined.  For few rows (single
-//                tokens): bound by the cache's bytes.
-//   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles
-//                staged in LDS, double-buffered, shared by the 4 waves.  Bound
-//                by the matrix units and the exponentials beside them.
+//                tokens): bound by the cache's bytes.  One stream over 131075
+//                keys, 2 x 256: 70 us, of which 38 stream the 268 MB (7 TB/s,
+//                partly from the last-level cache), 7 pass before the first
+//                keys arrive and 12 in two joins; 32 streams of 2 to 8 thousand
+//                keys, 4 x 128: 89 us, 4.2 TB/s.
+//   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles go
+//                straight from memory into LDS, double-buffered, shared by the
+//                waves.  Bound by the matrix units and the exponentials beside
+//                them: 2048 tokens over 8100 keys, 48 x 128: 415 us, 860
+//                TFLOP/s (a large library product reaches 1170); with the
+//                probabilities as two terms and 256 columns, 6 prompts in a
+//                window of 1024: 151 us.
 //
 // Few workgroups: the keys of a tile are split over several, whose partial
 // (m, l, O) go to the workspace.  The last to arrive of each 16 joins them, the
-// last of those joins the joined ones (a tree of two levels, up to 256 parts).
+// last of those joins the joined ones (a tree of two levels, up to 256 parts):
+// a join reads 16 x 12 KB through one compute unit, 5 us.  Splitting only the
+// tiles of attn_chunk's last round, so that it fills the card, changed nothing
+// at 128 columns and cost a quarter at 256.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -63,7 +77,8 @@ constexpr int kFan = 16;         // parts joined at once
 constexpr int kMaxSplits = kFan * kFan;
 constexpr int kMaxParts = 2048;  // parts of all tiles together
 constexpr int kMaxChunkParts = 512;
-constexpr int kLong = 16;
+constexpr int kLong = 32;
+constexpr int kLeastTiles = 8;  // of an attn_chunk part: joining parts of many rows costs what some tiles do
 constexpr int kCounters = kFan + 1;
 constexpr int64_t kHeader = (int64_t)kMaxParts * kCounters * 4;  // the counters, before the parts
 static_assert(kHeader % 256 == 0, "");
@@ -71,13 +86,20 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A wave holds 32 rows of Q and of O: at 256 columns those leave no room for a second wave on its SIMD, so two waves share
-// the rows, compute the scores both and take half of O's columns each.
+// the rows, compute the scores both and take half of O's columns each (6 windowed prompts: 172 -> 154 us).
 constexpr int chunk_threads(int dim) { return dim == 256 ? 512 : 256; }
 
 struct AttnParams {
   tq_paged_attn_args a;
   float scale2;  // scale * log2 e
-  int group, page_shift, splits, slots;
+  // Part 0 of every tile, then part 1, ...: the workgroups that find nothing to do come last.  (With a tile's parts together
+  // and a quarter of them live, the live ones all went to the same compute units: 8 streams x 4000 keys x 2 tokens, 256
+  // columns: 110 us.)
+  int tiles, splits;
+  // A tile's parts on different XCDs (workgroups go round the 8 of them): tiles differ in length.
+  __device__ int tile_of(int place, int part) const { return (int)((unsigned)(place + 3 * part) % (unsigned)tiles); }
+  int group, page_shift;
+  int slot_per, slot_add;  // a sequence's first tile among all: cu slot_per / rows + slot_add b
   int places_shift;  // log2 of the workgroups that the card holds at once
   int tiles_each;    // tiles per sequence of one token
   unsigned group_mul, group_shift;
@@ -136,9 +158,9 @@ __device__ inline Tile find_tile(const AttnParams& p, int tile, int lane) {
   Tile r;
   const int slot = tile / (unsigned)a.kv_heads;
   r.kvh = tile - slot * a.kv_heads;
-  r.b = a.cu ? find_seq(a.cu, a.seqs, p.group, ROWS, slot, lane) : p.tiles_each == 1 ? slot : slot / p.tiles_each;
+  r.b = a.cu ? find_seq(a.cu, a.seqs, p.slot_per, ROWS, p.slot_add, slot, lane) : p.tiles_each == 1 ? slot : slot / p.tiles_each;
   const SeqRange s = seq_range(a.cu, r.b, a.tokens, a.bad_flag);
-  const int64_t slot0 = a.cu ? first_slot(a.cu, r.b, p.group, ROWS) : r.b * p.tiles_each;
+  const int64_t slot0 = a.cu ? first_slot(a.cu, r.b, p.slot_per, ROWS, p.slot_add) : r.b * p.tiles_each;
   const int64_t row0 = (slot - slot0) * ROWS, all = (int64_t)s.n * p.group;
   r.t0 = s.t0;
   r.row0 = (int)row0;
@@ -309,7 +331,7 @@ __device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts
   unsigned* counters = static_cast<unsigned*>(p.a.workspace) + (int64_t)tile * kCounters;
   constexpr int step = part_floats<ROWS, D>();
   const int mine = tile * p.splits * step;
-  const int joined = (p.slots * p.a.kv_heads * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
+  const int joined = (p.tiles * p.splits + tile * ((p.splits + kFan - 1) / kFan)) * step;
   const int set = part / kFan, sets = (active + kFan - 1) / kFan, in_set = min(kFan, active - set * kFan);
   int counter = set, src = mine + set * kFan * step, count = in_set, dst = sets == 1 ? -1 : joined + set * step;
   while (last_of(counters + counter, count, shared)) {
@@ -324,21 +346,22 @@ __device__ void join_tree(const AttnParams& p, const Tile& t, const Parts& parts
 template <typename C, typename O, int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p) {
   constexpr int KK = D / 32, DT = D / 16;
-  constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 1;
+  constexpr int TERMS = sizeof(O) == 4 ? Half<C>::kTerms : 2;
   typedef Half<C> H;
   __shared__ __attribute__((aligned(16))) float stage[kWaves][kRowsTile][D + 4];
   __shared__ float stat[kWaves][2][kRowsTile];
   __shared__ int shared;
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / (unsigned)p.splits, part = blockIdx.x - tile * p.splits;
+  const int part = blockIdx.x / (unsigned)p.tiles, tile = p.tile_of(blockIdx.x - part * p.tiles, part);
   const Tile t = find_tile<kRowsTile>(p, tile, lane);
   if (t.rows <= 0) return;
   // blocks of 32 keys; every wave of a part has at least one
   const int first = t.begin / kBlock, blocks = t.end > 0 ? (t.end + kBlock - 1) / kBlock - first : 0;
   // Parts of equal length that fill the places once; of kLong blocks at most where sequences may differ in length, so that
-  // the longest does not hold up the end (32 streams of 2096 to 8192 keys, 128 columns: 144 us in one round, XX in parts of 16).
-  const int even = (int)(((int64_t)blocks * (p.slots * a.kv_heads) + (1 << p.places_shift) - 1) >> p.places_shift);
+  // the longest does not hold up the end (32 streams of 2 to 8 thousand keys, 128 columns: 144 us in one round, 91 in parts
+  // of 32 blocks, 95 of 16).
+  const int even = (int)(((int64_t)blocks * p.tiles + (1 << p.places_shift) - 1) >> p.places_shift);
   const unsigned unit = max(kWaves, a.seqs == 1 ? even : min(even, kLong));
   const unsigned active = max(1u, min((unsigned)p.splits, (blocks + unit - 1) / unit));
   if ((unsigned)part >= active) return;
@@ -741,11 +764,11 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
   const auto& a = p.a;
   const int lane = threadIdx.x & 63, waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = waves & 3, n = lane & 31, g = lane >> 5;
   const int d0 = waves / 4 * DT;  // this wave's first 32 columns
-  const int tile = blockIdx.x / (unsigned)p.splits, part = blockIdx.x - tile * p.splits;
+  const int part = blockIdx.x / (unsigned)p.tiles, tile = p.tile_of(blockIdx.x - part * p.tiles, part);
   const Tile t = find_tile<ROWS>(p, tile, lane);
   if (t.rows <= 0) return;
   const int first = t.begin / KT, blocks = t.end > 0 ? (t.end + KT - 1) / KT - first : 0;
-  const int active = max(1, min(p.splits, blocks));
+  const int active = max(1, min(p.splits, blocks / kLeastTiles));
   if (part >= active) return;
   const int each = (unsigned)blocks / (unsigned)active, more = blocks - each * active;  // the first `more` parts have one more
   const int lo = first + each * part + min(part, more), hi = lo + each + (part < more ? 1 : 0);
@@ -812,15 +835,23 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
 
 // ---- host ----------------------------------------------------------------------------------------------------------
 
-// Tiles of `rows` query rows over all sequences (an upper bound; what is left over finds no rows) and key heads.
-int64_t slots_of(int64_t tokens, int64_t seqs, int group, int rows, bool offsets) {
-  return offsets ? tokens * group / rows + seqs : seqs * ((group + rows - 1) / rows);
+// Registers and LDS allow two workgroups of four waves per compute unit, one of eight (or of four at 256 columns).
+int places_shift(int dim) { return dim == 256 ? 8 : 9; }
+
+// Tiles of the token axis, at most: as many per token as one token's rows take, or what all their rows take and one per
+// sequence; whichever is fewer.  What is left over finds no rows.
+int64_t tiles_of(int64_t tokens, int64_t seqs, int group, int rows) {
+  return std::min(tokens * ((group + rows - 1) / rows), tokens * group / rows + seqs);
 }
 
-// attn_chunk from 64 rows per sequence on.
-bool in_chunks(int64_t tokens, int64_t seqs, int group, int64_t max_len) {
-  const int64_t longest = max_len > 0 ? std::min(max_len, tokens) : (tokens + seqs - 1) / seqs;
-  return longest * group >= 64 && tokens > seqs;
+// attn_rows reads the cache once per 16 rows, attn_chunk once per 128, but computes tiles of 128 whatever their rows and
+// joins longer.  attn_chunk where attn_rows would have two tiles or more per sequence and an eighth as many as the card
+// holds: over 4000 keys, rows against chunk, in us: 1 stream x 16 tokens x 12 heads, 2 x 256: 30, 58 (24 tiles); 8 streams
+// x 2 tokens: 35, 34 (32 tiles), x 4: 62, 42, x 16: 170, 69; 4 x 128, 8 streams x 2: 30, 31 (64 tiles), x 4: 43, 36.
+bool in_chunks(const tq_paged_attn_args& a, int group) {
+  if (a.tokens <= a.seqs) return false;
+  const int64_t rows = (a.max_len > 0 ? std::min(a.max_len, a.tokens) : (a.tokens + a.seqs - 1) / a.seqs) * group;
+  return rows > kRowsTile && tiles_of(a.tokens, a.seqs, group, kRowsTile) * a.kv_heads >= (1 << places_shift(a.dim)) / 8;
 }
 // `parts` and what joins them: one per kFan of a tile's.
 int64_t parts_bytes(int64_t parts, int rows, int dim) { return (parts + parts / 2 + kFan) * rows * (dim + 2) * 4; }
@@ -828,13 +859,15 @@ int64_t parts_bytes(int64_t parts, int rows, int dim) { return (parts + parts / 
 template <typename C, typename O, int D>
 hipError_t launch_dim(AttnParams& p, hipStream_t s) {
   const auto& a = p.a;
-  const bool chunks = in_chunks(a.tokens, a.seqs, p.group, a.max_len);
-  p.slots = (int)slots_of(a.tokens, a.seqs, p.group, chunks ? kChunkTile : kRowsTile, a.cu != nullptr);
-  const int64_t tiles = (int64_t)p.slots * a.kv_heads, keys = a.table_width * a.page;
-  // Registers and LDS allow two workgroups of four waves per compute unit, one of eight (or of four at 256 columns).
-  p.places_shift = D == 256 ? 8 : 9;
+  const bool chunks = in_chunks(a, p.group);
+  p.places_shift = places_shift(D);
   const int rows = chunks ? kChunkTile : kRowsTile;
   p.tiles_each = (p.group + rows - 1) / rows;
+  const int64_t slots = tiles_of(a.tokens, a.seqs, p.group, rows);
+  const bool by_token = slots == a.tokens * p.tiles_each;
+  p.slot_per = by_token ? p.tiles_each * rows : p.group, p.slot_add = by_token ? 0 : 1;
+  const int64_t tiles = slots * a.kv_heads, keys = a.table_width * a.page;
+  p.tiles = (int)tiles;
   p.splits = 1;
   if (a.workspace) {
     const int64_t units = chunks ? (keys + chunk_keys(D) - 1) / chunk_keys(D) : (keys + kWaves * kBlock - 1) / (kWaves * kBlock);
@@ -860,8 +893,8 @@ hipError_t launch_type(AttnParams& p, hipStream_t s) {
 
 int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int kv_heads, int dim) {
   if (tokens == 0) return 0;
-  // whether attn_chunk runs depends on the lengths too: room for it where it may
-  const bool chunks = tokens > seqs && tokens * (heads / kv_heads) >= 64;
+  // whether attn_chunk runs depends on max_len too: room for it wherever it may
+  const bool chunks = tokens > seqs && tokens * (heads / kv_heads) > kRowsTile;
   return kHeader + std::max(parts_bytes(kMaxParts, kRowsTile, dim), chunks ? parts_bytes(kMaxChunkParts, kChunkTile, dim) : 0);
 }
 
@@ -875,7 +908,7 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   const int sh = p.group == 1 ? 0 : 32 - __builtin_clz(p.group - 1);
   const uint64_t mul = ((uint64_t(1) << (31 + sh)) + p.group - 1) / p.group;
   p.group_mul = (unsigned)mul, p.group_shift = (unsigned)sh;
-  if (in_chunks(a.tokens, a.seqs, p.group, a.max_len)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
+  if (in_chunks(a, p.group)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
   if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch_type<bf16, float>(p, s) : launch_type<bf16, bf16>(p, s);
   return a.out_type == TQ_F32 ? launch_type<f16, float>(p, s) : launch_type<f16, f16>(p, s);
 }

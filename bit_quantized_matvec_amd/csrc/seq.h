@@ -109,15 +109,14 @@ __device__ inline void split_terms(const float* p, VEC* out) {
   for (int t = 0; t < TERMS; ++t) out[t] = __builtin_bit_cast(VEC, w[t]);
 }
 
-// Tiles of `rows` rows over the sequences, `per` rows per token: sequence b's are the slots from cu[b] * per / rows + b on
-// (an upper bound for what the sequences before it need).  The largest b whose first slot is at most `slot`, 64 candidates
-// at a time.
-__device__ inline int64_t first_slot(const int32_t* cu, int64_t b, int per, int rows) { return (int64_t)cu[b] * per / rows + b; }
-__device__ inline int find_seq(const int32_t* cu, int64_t seqs, int per, int rows, int64_t slot, int lane) {
+// Tiles of `rows` rows over the sequences: sequence b's are the slots from cu[b] * per / rows + add * b on, an upper bound
+// for what the sequences before it need.  The largest b whose first slot is at most `slot`, 64 candidates at a time.
+__device__ inline int64_t first_slot(const int32_t* cu, int64_t b, int per, int rows, int add) { return (int64_t)cu[b] * per / rows + add * b; }
+__device__ inline int find_seq(const int32_t* cu, int64_t seqs, int per, int rows, int add, int64_t slot, int lane) {
   int64_t lo = 0, n = seqs;
   while (n > 1) {
     const int64_t step = (n + 63) / 64, i = lo + lane * step;
-    const bool ok = lane * step < n && first_slot(cu, i, per, rows) <= slot;
+    const bool ok = lane * step < n && first_slot(cu, i, per, rows, add) <= slot;
     const int64_t last = max(1, __popcll(__ballot(ok))) - 1;
     lo += last * step;
     n = min(step, n - last * step);

@@ -297,10 +297,11 @@ int tq_rope_append(const tq_rope_append_args *args, void *stream);
  * block_table[b][j / page] is the page of key j.  A page outside [0, pages)
  * counts as keys that nobody sees, with bad_flag; so does kv_len[b] beyond
  * the table.  Query head h reads key head h / (heads / kv_heads).
- * Products are exact, sums and statistics fp32.  out in the cache's type: the
- * probabilities are rounded to that type before the product with V, which is
- * what the output's own rounding amounts to; out fp32: they are split into
- * two (fp16) or three (bf16) terms that hold 22 or 24 bits.
+ * Products are exact, sums and statistics fp32.  Probabilities enter the
+ * product with V as two (fp16) or three (bf16) terms that hold 22 or 24 bits
+ * when out is fp32; as two terms when out has the cache's type and the rows are
+ * few; rounded to that type, which is what the output's own rounding amounts
+ * to, when they are many.
  * workspace (nullable): tq_paged_attn_workspace_bytes, zeroed before its first
  * use and left with its counters at zero by every call; without it no
  * sequence's keys are split over workgroups. */
@@ -333,10 +334,15 @@ int tq_paged_attn(const tq_paged_attn_args *args, void *stream);
  * its last state in state_out[slots[b]] (slots NULL: b).  slots[b] < 0 starts
  * from zeros and stores nothing; slots[b] >= states does that too, with
  * bad_flag.  Two sequences with one slot race.  state_out may be state.  An
- * empty sequence copies its state.  All arithmetic and the states are fp32,
- * running sums of g fp64.  dk 64 or 128, dv a multiple of 32 up to 256.
+ * empty sequence copies its state.  Arithmetic and states are fp32, running
+ * sums of g fp64.  dk 64 or 128, dv a multiple of 32 up to 256.
  * workspace: nullable; with tq_gdn_workspace_bytes of scratch (needs no
- * clearing), long sequences are computed in chunks on the matrix units. */
+ * clearing), sequences of 16 tokens and more are computed in chunks of 64 on
+ * the matrix units, operands split into bf16 terms that hold fp32's 24 bits
+ * (16 where they reach only an out of 16 bits).  What is not finite at a token
+ * reaches later ones only, in chunks too.  max_len, where it is known, keeps
+ * calls of more chunks than the workspace holds from looking for them past
+ * every sequence's end. */
 typedef struct {
     const void *q, *k, *v; /* [tokens][k_heads | k_heads | v_heads][dk | dk | dv], in_type */
     int64_t q_token, q_head, k_token, k_head, v_token, v_head;

@@ -211,6 +211,7 @@ CHUNK = [
     ([9, 4], [4, 0], 2, 1, 64, 16, BF, F32, 0),          # tokens before the first key see nothing
     ([150], [150], 24, 2, 256, 64, BF, F32, 0),
     ([210, 40], [260, 41], 12, 1, 128, 64, BF, F32, 64),
+    ([2, 2], [2300, 2100], 768, 64, 64, 64, BF, BF, 0),  # many key heads: few rows each, still split
 ]
 
 
