@@ -41,8 +41,8 @@
 // Bound.  The walk: one chunk after another on 4 SIMDs per 32 columns, 2.4 us a
 // chunk at bf16, of which the matrix units take 0.7: splitting into terms, LDS
 // between the products and three barriers are the rest.  4096 bf16 tokens, 48
-// heads of 128 x 128: 188 us, 53 of them in the first kernel (166 MB written);
-// token after token 6063.  Five fp32 sequences of 77 to 701 tokens: 189 us (1290).
+// heads of 128 x 128: 181 us, 44 of them in the first kernel (149 MB written);
+// token after token 6063.  Five fp32 sequences of 77 to 701 tokens: 177 us (1290).
 // What else was measured at the first: one wave per 16 columns without LDS 1777
 // us (its loads wait one by one), eight waves of 16 columns that all do the same
 // 264, four waves that compute the outputs too 251.
@@ -56,7 +56,10 @@ namespace tq {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr int kStepLen = 16;  // tokens from which a chunk is worth its first kernel
+// Tokens from which a chunk is worth its first kernel: 16 key and 48 value heads of 128 x 128, steps against chunks: one
+// sequence of 12 tokens 18 against 15 (bf16) and 22 us (fp32), of 16 23 against 15 and 22; eight of 12 48 against 48 and 66,
+// of 16 63 against 48 and 66, of 20 76 against 48 and 67.
+constexpr int kStepLen = 16;
 constexpr int kPrepThreads = 256;
 constexpr int64_t kBudget = int64_t(256) << 20;  // workspace: what the last-level cache holds
 constexpr int kFragBytes = 1024;
@@ -87,6 +90,7 @@ struct ChunkParams {
   int nseq, chunk0, chunks;  // this launch: chunks [chunk0, chunk0 + chunks) of sequences [seq0, seq0 + nseq)
   int whole;                 // one launch for everything: chunks laid out by cu
   int last;
+  int heads;  // value heads per workgroup of the first kernel
 };
 
 __device__ inline f32x4 mma(frag a, frag b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -147,8 +151,9 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   __shared__ float norms[kChunk];
   const auto& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
-  const int h = blockIdx.x % a.v_heads, group = a.v_heads / a.k_heads, kh = h / group;
-  const int64_t slot = blockIdx.x / a.v_heads;
+  // `heads` value heads of one key head: K Q^T and K K^T serve them all
+  const int sets = a.v_heads / p.heads, h0 = (int)(blockIdx.x % sets) * p.heads, group = a.v_heads / a.k_heads, kh = h0 / group;
+  const int64_t slot = blockIdx.x / sets;
   const int64_t b = p.whole ? find_seq(a.cu, a.seqs, 1, kChunk, 1, slot, lane) : p.seq0 + slot / p.chunks;
   const SeqRange r = seq_range(a.cu, b, a.tokens, nullptr);
   const int64_t c = p.whole ? slot - (r.t0 / kChunk + b) : p.chunk0 + slot % p.chunks;
@@ -158,10 +163,8 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
 
   uint8_t* unit = p.units + slot * p.unit_bytes;
   uint8_t* keys = unit + (int64_t)kh * (key_frags(DK, TK) * kFragBytes);
-  uint8_t* tri = unit + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
-  Scalars* sc = reinterpret_cast<Scalars*>(tri + tri_frags(3 + OT) * kFragBytes);
   auto put = [&](uint8_t* at, int index, frag f) { *reinterpret_cast<frag*>(at + index * kFragBytes + lane * 16) = f; };
-  const bool writes_keys = h % group == 0;
+  const bool writes_keys = h0 % group == 0;
 
   // this wave's 16 tokens, as right operands; column n is token i
   const int i = place(wave, n);
@@ -189,35 +192,15 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   }
   qq += __shfl_xor(qq, 16, 64), kk += __shfl_xor(kk, 16, 64);
   qq += __shfl_xor(qq, 32, 64), kk += __shfl_xor(kk, 32, 64);
-  float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f, beta = 0.f;
-  bool odd = false;
-  if (i < len) {
-    beta = a.beta[(t0 + i) * a.v_heads + h];
-    odd = !(qq < INFINITY) || !(kk < INFINITY) || !(fabsf(nq) < INFINITY) || !(nk < INFINITY) || !(fabsf(beta) < INFINITY);
-  } else {
-    nq = nk = 0.f;
-  }
+  float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f;
+  const bool odd_rows = i < len && (!(qq < INFINITY) || !(kk < INFINITY) || !(fabsf(nq) < INFINITY) || !(nk < INFINITY));
+  if (i >= len) nq = nk = 0.f;
   if (g == 0) norms[i] = nk;
-  {
-    const float x = lane < len ? a.g[(t0 + lane) * a.v_heads + h] : 0.f;
-    odd = odd || !(x <= 0.f);
-    if (wave == 0) {
-      double sum = fmaxf(x, kLeastG) * 1.4426950408889634074;  // in powers of two
+  __syncthreads();
+  f32x4 akk[2][2] = {}, aqk[2][2] = {};
 #pragma unroll
-      for (int o = 1; o < kChunk; o <<= 1) {
-        const double y = __shfl_up(sum, o, 64);
-        if (lane >= o) sum += y;
-      }
-      sums[lane] = sum;
-    }
-  }
-  odd = __syncthreads_or(odd);
-  if (odd && g == 0) sc->beta[i] = NAN;  // K, Q and K^T are still written: other heads may be odd in nothing
-  const double mine = sums[i];
-  const float nb = beta * nk;
-#pragma unroll 1
-  for (int s2 = 0; s2 <= wave >> 1; ++s2) {
-    f32x4 akk[2] = {}, aqk[2] = {};
+  for (int s2 = 0; s2 < 2; ++s2) {
+    if (s2 > wave >> 1) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -225,119 +208,143 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
         frag kt[TK];
 #pragma unroll
         for (int e = 0; e < TK; ++e) kt[e] = ks[2 * s2 + t][s][e][lane];
-        akk[t] = mma_terms<TK, TK>(kt, kf[s], akk[t]), aqk[t] = mma_terms<TK, TK>(kt, qf[s], aqk[t]);
+        akk[s2][t] = mma_terms<TK, TK>(kt, kf[s], akk[s2][t]), aqk[s2][t] = mma_terms<TK, TK>(kt, qf[s], aqk[s2][t]);
       }
-    float ra[8], rp[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int row = 32 * s2 + 8 * g + j;
-      const float e = exp2_(fminf((float)(mine - sums[row]), 0.f)) * norms[row];
-      const float q = nq * e * aqk[j >> 2][j & 3], k = nb * e * akk[j >> 2][j & 3];
-      rp[j] = row <= i ? q : 0.f;
-      ra[j] = row < i ? k : 0.f;
-    }
-    *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g]) = float4{ra[0], ra[1], ra[2], ra[3]};
-    *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g + 4]) = float4{ra[4], ra[5], ra[6], ra[7]};
-    frag pf[OT];
-    split_terms<OT>(rp, pf);
-#pragma unroll
-    for (int t = 0; t < OT; ++t) put(tri + tri_frags(3) * kFragBytes, tri_at(wave, s2) * OT + t, pf[t]);
-    if (writes_keys && s2 == wave >> 1) {
-      const int c2 = wave & 1;  // this wave transposes every second tile of the head's rows
-      frag one;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) one[j] = (bf16)(8 * g + j == place(c2, n) ? 1.f : 0.f);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int t = 0; t < TK; ++t) {
-          const f32x4 lo = mma(ks[2 * s2][s][t][lane], one, f32x4{}), hi = mma(ks[2 * s2 + 1][s][t][lane], one, f32x4{});
-          frag f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = (bf16)lo[j], f[4 + j] = (bf16)hi[j];
-          put(keys + 8 * KS * TK * kFragBytes, ((2 * s + c2) * 2 + s2) * TK + t, f);
-        }
-    }
   }
-  if (writes_keys)
+  if (writes_keys) {
+    const int s2 = wave >> 1, c2 = wave & 1;  // this wave transposes every second tile of the head's rows
+    frag one;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) one[j] = (bf16)(8 * g + j == place(c2, n) ? 1.f : 0.f);
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int t = 0; t < TK; ++t) {
+        const f32x4 lo = mma(ks[2 * s2][s][t][lane], one, f32x4{}), hi = mma(ks[2 * s2 + 1][s][t][lane], one, f32x4{});
+        frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = (bf16)lo[j], f[4 + j] = (bf16)hi[j];
+        put(keys + 8 * KS * TK * kFragBytes, ((2 * s + c2) * 2 + s2) * TK + t, f);
         put(keys, (wave * KS + s) * TK + t, kf[s][t]);
         put(keys + 4 * KS * TK * kFragBytes, (wave * KS + s) * TK + t, qf[s][t]);
       }
-  if (odd) return;
-  const double all = sums[kChunk - 1];
-  if (g == 0) {
-    const float far = exp2_((float)mine);
-    sc->beta[i] = beta;
-    sc->far_k[i] = beta * far * nk;
-    sc->far_q[i] = far * nq;
-    sc->last_k[i] = exp2_((float)(all - mine)) * nk;
-    sc->decay[i] = exp2_((float)all);
   }
-
-  // T: the diagonal blocks of 16 by substitution, one block in 16 lanes of the first wave: a lane holds row n of A and
-  // column n of T, and a step takes A's row k from lane k ...
-  __syncthreads();
-  if (wave == 0) {
-    float row[16], x[16];
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) *reinterpret_cast<f32x4*>(row + k) = *reinterpret_cast<const f32x4*>(&A[16 * g + n][16 * g + k]);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = k == n ? 1.f : 0.f;
-    steps<0>(row, x);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) T[16 * g + k][16 * g + n] = x[k];
-  } else if (wave < 3) {  // the blocks above the diagonal that operands of 32 columns reach
-#pragma unroll
-    for (int k = 0; k < 4; ++k) T[32 * (wave - 1) + 4 * g + k][32 * (wave - 1) + 16 + n] = 0.f;
-  }
-  __syncthreads();
-  // ... then T21 = -T22 (A21 T11), for blocks of 16 and of 32.  A step's 4 summed indices are 4g + s: what a result holds.
-  auto block = [&](const float(*l)[W], int li, int lj, f32x4 right, f32x4 sum, float sign) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) sum = mma4(sign * l[16 * li + n][16 * lj + 4 * g + s], right[s], sum);
-    return sum;
+  float beta = 0.f, gate = 0.f;
+  auto load_head = [&](int h) {
+    if (i < len) beta = a.beta[(t0 + i) * a.v_heads + h];
+    if (lane < len) gate = a.g[(t0 + lane) * a.v_heads + h];
   };
-  auto column = [&](int bi, int bj) {
-    f32x4 v;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = T[16 * bi + 4 * g + s][16 * bj + n];
-    return v;
-  };
-  auto store = [&](int bi, int bj, f32x4 v) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) T[16 * bi + 4 * g + s][16 * bj + n] = v[s];
-  };
-  if (wave < 2) {
-    const f32x4 m = block(A, 2 * wave + 1, 2 * wave, column(2 * wave, 2 * wave), f32x4{}, 1.f);
-    store(2 * wave + 1, 2 * wave, block(T, 2 * wave + 1, 2 * wave + 1, m, f32x4{}, -1.f));
-  }
-  __syncthreads();
-  if (wave < 2) {
-    f32x4 m[2] = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k < wave) continue;
-      const f32x4 v = column(k, wave);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) m[t] = block(A, 2 + t, k, v, m[t], 1.f);
-    }
-    store(2, wave, block(T, 2, 2, m[0], f32x4{}, -1.f));
-    store(3, wave, block(T, 3, 3, m[1], block(T, 3, 2, m[0], f32x4{}, -1.f), -1.f));
-  }
-  __syncthreads();
+  load_head(h0);
 #pragma unroll 1
-  for (int s2 = 0; s2 <= wave >> 1; ++s2) {
-    float x[8];
+  for (int h = h0; h < h0 + p.heads; ++h) {
+    uint8_t* tri = unit + (int64_t)a.k_heads * (key_frags(DK, TK) * kFragBytes) + (int64_t)h * (tri_frags(3 + OT) * kFragBytes + kScalarBytes);
+    Scalars* sc = reinterpret_cast<Scalars*>(tri + tri_frags(3 + OT) * kFragBytes);
+    if (wave == 0) {
+      double sum = fmaxf(gate, kLeastG) * 1.4426950408889634074;  // in powers of two
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = T[i][32 * s2 + 8 * g + j];
-    frag f[3];
-    split_terms<3>(x, f);
+      for (int o = 1; o < kChunk; o <<= 1) {
+        const double y = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += y;
+      }
+      sums[lane] = sum;
+    }
+    const bool odd = __syncthreads_or(odd_rows || !(fabsf(beta) < INFINITY) || !(gate <= 0.f));
+    const float be = beta, nb = beta * nk;
+    if (h + 1 < h0 + p.heads) load_head(h + 1);
+    if (odd) {
+      if (g == 0) sc->beta[i] = NAN;
+      continue;
+    }
+    const double mine = sums[i], all = sums[kChunk - 1];
 #pragma unroll
-    for (int t = 0; t < 3; ++t) put(tri, tri_at(wave, s2) * 3 + t, f[t]);
+    for (int s2 = 0; s2 < 2; ++s2) {
+      if (s2 > wave >> 1) continue;
+      float ra[8], rp[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = 32 * s2 + 8 * g + j;
+        const float e = exp2_(fminf((float)(mine - sums[row]), 0.f)) * norms[row];
+        const float q = nq * e * aqk[s2][j >> 2][j & 3], k = nb * e * akk[s2][j >> 2][j & 3];
+        rp[j] = row <= i ? q : 0.f;
+        ra[j] = row < i ? k : 0.f;
+      }
+      *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g]) = float4{ra[0], ra[1], ra[2], ra[3]};
+      *reinterpret_cast<float4*>(&A[i][32 * s2 + 8 * g + 4]) = float4{ra[4], ra[5], ra[6], ra[7]};
+      frag pf[OT];
+      split_terms<OT>(rp, pf);
+#pragma unroll
+      for (int t = 0; t < OT; ++t) put(tri + tri_frags(3) * kFragBytes, tri_at(wave, s2) * OT + t, pf[t]);
+    }
+    if (g == 0) {
+      const float far = exp2_((float)mine);
+      sc->beta[i] = be;
+      sc->far_k[i] = be * far * nk;
+      sc->far_q[i] = far * nq;
+      sc->last_k[i] = exp2_((float)(all - mine)) * nk;
+      sc->decay[i] = exp2_((float)all);
+    }
+
+    // T: the diagonal blocks of 16 by substitution, one block in 16 lanes of the first wave: a lane holds row n of A and
+    // column n of T, and a step takes A's row k from lane k ...
+    __syncthreads();
+    if (wave == 0) {
+      float row[16], x[16];
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) *reinterpret_cast<f32x4*>(row + k) = *reinterpret_cast<const f32x4*>(&A[16 * g + n][16 * g + k]);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = k == n ? 1.f : 0.f;
+      steps<0>(row, x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) T[16 * g + k][16 * g + n] = x[k];
+    } else if (wave < 3) {  // the blocks above the diagonal that operands of 32 columns reach
+#pragma unroll
+      for (int k = 0; k < 4; ++k) T[32 * (wave - 1) + 4 * g + k][32 * (wave - 1) + 16 + n] = 0.f;
+    }
+    __syncthreads();
+    // ... then T21 = -T22 (A21 T11), for blocks of 16 and of 32.  A step's 4 summed indices are 4g + s: what a result holds.
+    auto block = [&](const float(*l)[W], int li, int lj, f32x4 right, f32x4 sum, float sign) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) sum = mma4(sign * l[16 * li + n][16 * lj + 4 * g + s], right[s], sum);
+      return sum;
+    };
+    auto column = [&](int bi, int bj) {
+      f32x4 v;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[s] = T[16 * bi + 4 * g + s][16 * bj + n];
+      return v;
+    };
+    auto store = [&](int bi, int bj, f32x4 v) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) T[16 * bi + 4 * g + s][16 * bj + n] = v[s];
+    };
+    if (wave < 2) {
+      const f32x4 m = block(A, 2 * wave + 1, 2 * wave, column(2 * wave, 2 * wave), f32x4{}, 1.f);
+      store(2 * wave + 1, 2 * wave, block(T, 2 * wave + 1, 2 * wave + 1, m, f32x4{}, -1.f));
+    }
+    __syncthreads();
+    if (wave < 2) {
+      f32x4 m[2] = {};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k < wave) continue;
+        const f32x4 v = column(k, wave);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) m[t] = block(A, 2 + t, k, v, m[t], 1.f);
+      }
+      store(2, wave, block(T, 2, 2, m[0], f32x4{}, -1.f));
+      store(3, wave, block(T, 3, 3, m[1], block(T, 3, 2, m[0], f32x4{}, -1.f), -1.f));
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int s2 = 0; s2 <= wave >> 1; ++s2) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = T[i][32 * s2 + 8 * g + j];
+      frag f[3];
+      split_terms<3>(x, f);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) put(tri, tri_at(wave, s2) * 3 + t, f[t]);
+    }
   }
 }
 
@@ -825,7 +832,12 @@ hipError_t launch_all(const tq_gdn_args& a, hipStream_t s) {
   p.unit_bytes = unit_bytes(a.k_heads, a.v_heads, DK, terms_in<IN>(), OT);
   p.units = static_cast<uint8_t*>(a.workspace);
   auto run = [&]() {
-    hipLaunchKernelGGL((gdn_prepare_kernel<IN, DK, OT>), dim3((unsigned)(p.slots * a.v_heads)), dim3(kPrepThreads), 0, s, p);
+    const int group = a.v_heads / a.k_heads;
+    // A key head's value heads in one workgroup where those fill the card twice (16 key and 48 value heads, one sequence, bf16
+    // and fp32, one head each against three: 64 tokens 16.5, 23.2 against 22.0, 28.3 us; 1024 54.2, 85.3 against 55.7, 80.7;
+    // 4096 184, 382 against 179, 371)
+    p.heads = p.slots * a.k_heads >= 512 ? group : 1;
+    hipLaunchKernelGGL((gdn_prepare_kernel<IN, DK, OT>), dim3((unsigned)(p.slots * (a.v_heads / p.heads))), dim3(kPrepThreads), 0, s, p);
     launch_walk<IN, O, DK>(p, s);
     return hipGetLastError();
   };

@@ -904,6 +904,7 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   p.scale2 = a.scale * kLog2e;
   p.group = a.heads / a.kv_heads;
   p.page_shift = __builtin_ctz(a.page);
+  if (a.window >= a.table_width * a.page) p.a.window = 0;  // as wide as any sequence: no window (and no sums beyond 31 bits)
   // row / group = row * ceil(2^(31 + s) / group) >> (31 + s) with 2^s >= group: 2 row times that, its high word, >> s
   const int sh = p.group == 1 ? 0 : 32 - __builtin_clz(p.group - 1);
   const uint64_t mul = ((uint64_t(1) << (31 + sh)) + p.group - 1) / p.group;

@@ -68,7 +68,7 @@ int attn_status(const tq_paged_attn_args& a) {
   const int st = attn_sizes(a.tokens, a.seqs, a.heads, a.kv_heads, a.dim);
   if (st != TQ_OK) return st;
   if (a.pages < 1 || a.pages > kMaxPages || !page_ok(a.page) || a.table_width < 0 || a.table_width > kMaxTable || a.table_stride < a.table_width ||
-      a.table_stride > kMaxTable || a.table_width * a.page > (int64_t(1) << 31) - 4096 || a.max_len < 0 || a.window < 0 || !std::isfinite(a.scale))
+      a.table_stride > kMaxTable || a.table_width * a.page > (int64_t(1) << 31) - 2 * kMaxTokens || a.max_len < 0 || a.window < 0 || !std::isfinite(a.scale))
     return TQ_ERR_SHAPE;
   if (!a.cu && a.tokens != a.seqs) return TQ_ERR_SHAPE;
   if (a.tokens > 0 && a.seqs == 0) return TQ_ERR_SHAPE;

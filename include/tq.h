@@ -303,7 +303,8 @@ int tq_rope_append(const tq_rope_append_args *args, void *stream);
  * few; rounded to that type, which is what the output's own rounding amounts
  * to, when they are many.
  * workspace (nullable): tq_paged_attn_workspace_bytes, zeroed before its first
- * use and left with its counters at zero by every call; without it no
+ * use and left with its counters at zero by every call (calls that overlap need
+ * workspaces of their own, here and for tq_gdn); without it no
  * sequence's keys are split over workgroups. */
 typedef struct {
     const void *q; /* [tokens][heads][dim], cache_type */

@@ -209,6 +209,7 @@ CHUNK = [
     ([90, 50], [190, 400], 4, 1, 128, 16, BF, BF, 33),
     ([70, 1], [70, 1], 6, 2, 256, 16, HF, F32, 16),
     ([9, 4], [4, 0], 2, 1, 64, 16, BF, F32, 0),          # tokens before the first key see nothing
+    ([70, 60], [40, 100], 4, 1, 64, 16, BF, F32, 2**31 - 1),  # the widest window there is
     ([150], [150], 24, 2, 256, 64, BF, F32, 0),
     ([210, 40], [260, 41], 12, 1, 128, 64, BF, F32, 64),
     ([2, 2], [2300, 2100], 768, 64, 64, 64, BF, BF, 0),  # many key heads: few rows each, still split
@@ -467,6 +468,30 @@ def test_gdn_in_several_launches(tq, hint, slots):
     near(after[stored][:, some], states[stored], torch.full_like(states[stored], bound), "state")
     if slots:
         assert bool((after[[1, 4]] == 9.0).all())
+
+
+@pytest.mark.parametrize("it,ot", [(F32, F32), (BF, BF), (HF, F32)])
+def test_gdn_many_chunks_of_shared_heads(tq, it, ot):
+    """Enough chunks that a workgroup prepares all value heads of a key head; one of them has a token that is not finite."""
+    n, kh, vh, dk, dv, late = [1900, 300], 16, 48, 64, 32, 1000
+    q, k, v, g, beta, state, cu = gdn_inputs(n, kh, vh, dk, dv, it)
+    beta[late, 1] = math.nan
+    c = lambda x: x.cuda()  # noqa: E731
+    gs = state.cuda()
+    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=True, out_dtype=ot, max_len=max(n),
+                 ws=tq.gdn_workspace(sum(n), 2, vh, dk, dv, max_len=max(n))).cpu()
+    for key in (0, 7, 15):
+        heads = slice(3 * key, 3 * key + 3)
+        want, states, big = so.gdn(q[:, key : key + 1], k[:, key : key + 1], v[:, heads], g[:, heads], torch.nan_to_num(beta[:, heads]), state[:, heads], cu,
+                                   dk**-0.5, True, 1e-6)
+        bound = so.gdn_bound(max(n), dk, big)
+        limit = so.HALF_STEP[ot] * want.abs() + bound * dk**-0.5
+        have, after = got[:, heads].double(), gs[:, heads].cpu().double()
+        if key == 0:  # head 1 of the first sequence, from the late token on
+            assert not bool(torch.isfinite(have[late : n[0], 1]).any()) and not bool(torch.isfinite(after[0, 1]).any())
+            have[late : n[0], 1], after[0, 1] = want[late : n[0], 1], states[0, 1]
+        near(have, want, limit, f"out of key head {key}")
+        near(after, states, torch.full_like(states, bound), f"states of key head {key}")
 
 
 @pytest.mark.parametrize("cu", [[0, 150, 90, 200], [-64, 90, 900, 200], [70, 200, -200, 130], [200, 0, 200, 0]])
