@@ -40,17 +40,17 @@
 //                fourth block of 32 keys straight from memory to registers; no
 //                LDS before the waves are joined.  For few rows (single
 //                tokens): bound by the cache's bytes.  One stream over 131075
-//                keys, 2 x 256: 70 us, of which 38 stream the 268 MB (7 TB/s,
+//                keys, 2 x 256: 71 us, of which 38 stream the 268 MB (7 TB/s,
 //                partly from the last-level cache), 7 pass before the first
 //                keys arrive and 12 in two joins; 32 streams of 2 to 8 thousand
-//                keys, 4 x 128: 89 us, 4.2 TB/s.
+//                keys, 4 x 128: 91 us, 4.2 TB/s.
 //   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles go
 //                straight from memory into LDS, double-buffered, shared by the
 //                waves.  Bound by the matrix units and the exponentials beside
-//                them: 2048 tokens over 8100 keys, 48 x 128: 415 us, 860
-//                TFLOP/s (a large library product reaches 1170); with the
+//                them: 2048 tokens over 8100 keys, 48 x 128: 406 to 427 us,
+//                830 to 880 TFLOP/s (a large library product reaches 1170); with the
 //                probabilities as two terms and 256 columns, 6 prompts in a
-//                window of 1024: 151 us.
+//                window of 1024: 153 us.
 //
 // Few workgroups: the keys of a tile are split over several, whose partial
 // (m, l, O) go to the workspace.  The last to arrive of each 16 joins them, the
