@@ -47,8 +47,8 @@
 //   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles go
 //                straight from memory into LDS, double-buffered, shared by the
 //                waves.  Bound by the matrix units and the exponentials beside
-//                them: 2048 tokens over 8100 keys, 48 x 128: 406 to 427 us,
-//                830 to 880 TFLOP/s (a large library product reaches 1170); with the
+//                them: 2048 tokens over 8100 keys, 48 x 128: 395 us, 900
+//                TFLOP/s (a large library product reaches 1170); with the
 //                probabilities as two terms and 256 columns, 6 prompts in a
 //                window of 1024: 153 us.
 //
@@ -553,6 +553,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
 __device__ inline void to_lds(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) unsigned*)src, (__attribute__((address_space(3))) unsigned*)dst, 16, 0, 0);
 }
+__device__ inline void to_lds(__amdgpu_buffer_rsrc_t r, int own, int at, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, own, at, 0, 0);
+}
 __device__ inline float max_halves(float x) {  // over lanes i and i + 32
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -625,14 +628,28 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
     }
     return pg;
   };
+  // A page's K and V of this key head are one piece of memory each: its address goes through scalar registers, a lane's place
+  // in it is the same for every tile but for the rows' exchange (415 -> 395 us for 2048 tokens over 8100 keys, 48 x 128).
+  const int page_bytes = a.page * D * 2, k_off = lane / KC * D * 2, k_piece = lane % KC;
+  const int v_off = v_d0 * a.page * 2 + vchunk * 16;
   auto fetch = [&](int tile, int pg, int buf) {
-    const int64_t kpg = max(__builtin_amdgcn_readlane(pg, 2 * (wave * NI * KSTEP / 16)), 0), vpg = max(pg, 0);
-    const C* ks = kc + ((kpg * a.kv_heads + t.kvh) * a.page + ((tile * KT + k_row0) & (a.page - 1))) * (int64_t)D;
-    const C* vs = vc + ((vpg * a.kv_heads + t.kvh) * D + v_d0) * (int64_t)a.page + ((tile * KT + 8 * vchunk) & (a.page - 1));
+    const int64_t kpg = max(__builtin_amdgcn_readlane(pg, 2 * (wave * NI * KSTEP / 16)), 0);
+    const auto kr = __builtin_amdgcn_make_buffer_rsrc(const_cast<C*>(kc + (kpg * a.kv_heads + t.kvh) * (int64_t)a.page * D), 0, page_bytes, 0x00027000);
+    const int k_at = ((tile * KT + wave * NI * KSTEP) & (a.page - 1)) * D * 2;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      to_lds(ks + i * KSTEP * D + (lane % KC ^ k_swap<D>(k_row0 + i * KSTEP)) * 8, kbuf + buf * KT * D + (wave * NI + i) * 512);
-      to_lds(vs + (int64_t)i * VSTEP * a.page, vbuf + buf * v_values(D) + (wave * NI + i) * v_block(D));
+    for (int i = 0; i < NI; ++i)
+      to_lds(kr, k_off + (k_piece ^ k_swap<D>(k_row0 + i * KSTEP)) * 16, k_at + i * KSTEP * D * 2, kbuf + buf * KT * D + (wave * NI + i) * 512);
+    if (a.page >= KT) {  // the tile lies in one page
+      const int64_t vpg = max(__builtin_amdgcn_readlane(pg, 0), 0);
+      const auto vr = __builtin_amdgcn_make_buffer_rsrc(const_cast<C*>(vc + (vpg * a.kv_heads + t.kvh) * (int64_t)a.page * D), 0, page_bytes, 0x00027000);
+      const int v_at = (tile * KT & (a.page - 1)) * 2;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) to_lds(vr, v_off, v_at + i * VSTEP * a.page * 2, vbuf + buf * v_values(D) + (wave * NI + i) * v_block(D));
+    } else {
+      const int64_t vpg = max(pg, 0);
+      const C* vs = vc + ((vpg * a.kv_heads + t.kvh) * D + v_d0) * (int64_t)a.page + ((tile * KT + 8 * vchunk) & (a.page - 1));
+#pragma unroll
+      for (int i = 0; i < NI; ++i) to_lds(vs + (int64_t)i * VSTEP * a.page, vbuf + buf * v_values(D) + (wave * NI + i) * v_block(D));
     }
   };
 
