@@ -149,8 +149,13 @@ struct Tile {
   int row0, rows;   // first row and count in this tile (rows <= 0: none)
   int kvh;
   int first_pos;    // position of the sequence's first new token (may be negative)
-  int begin, end;   // keys seen by some row: [begin, end)
+  int last_pos;     // position of the last row's token
+  int begin, end;   // keys that the table has and some row sees: [begin, end), or 0, 0
 };
+
+// First key in the window of a token at this position.  (One before the first key sees nothing, and is taken as at it: no sum
+// leaves 31 bits, whatever the window.)
+__device__ inline int first_seen(int window, int pos) { return window > 0 ? max(0, max(pos, 0) - window + 1) : 0; }
 
 template <int ROWS>
 __device__ inline Tile find_tile(const AttnParams& p, int tile, int lane) {
@@ -165,12 +170,13 @@ __device__ inline Tile find_tile(const AttnParams& p, int tile, int lane) {
   r.t0 = s.t0;
   r.row0 = (int)row0;
   r.rows = row0 < 0 || row0 >= all ? 0 : (int)min((int64_t)ROWS, all - row0);
-  const int64_t want = a.kv_len[r.b], len = min(max(want, (int64_t)0), a.table_width << p.page_shift);
-  if (want != len) raise_flag(a.bad_flag);
-  r.first_pos = (int)(len - s.n);
-  const int lo = r.first_pos + p.token_of(r.row0), hi = r.first_pos + p.token_of(max(0, r.row0 + r.rows - 1));
-  r.begin = a.window > 0 ? max(0, lo - a.window + 1) : 0;
-  r.end = r.rows > 0 ? hi + 1 : 0;
+  const int64_t len = a.kv_len[r.b], keys = a.table_width << p.page_shift;
+  if (len < 0 || len > keys) raise_flag(a.bad_flag);
+  r.first_pos = (int)(max(len, (int64_t)0) - s.n);
+  r.last_pos = r.first_pos + p.token_of(max(0, r.row0 + r.rows - 1));
+  r.begin = first_seen(a.window, r.first_pos + p.token_of(r.row0));
+  r.end = r.rows > 0 ? (int)min((int64_t)r.last_pos + 1, keys) : 0;
+  if (r.begin >= r.end) r.begin = r.end = 0;
   return r;
 }
 
@@ -371,9 +377,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   const int r = lane & 15, g = lane >> 4;
   const bool row_ok = r < t.rows;
   const int row = t.row0 + (row_ok ? r : 0);
-  const int token = p.token_of(row), pos = t.first_pos + token;
-  const int least = a.window > 0 ? pos - a.window + 1 : 0;  // first key that this row sees
-  const int pos_lo = t.first_pos + p.token_of(t.row0), pos_hi = t.end - 1;
+  const int token = p.token_of(row);
+  const int least = first_seen(a.window, t.first_pos + token), pos = min(t.first_pos + token, t.end - 1);  // this row sees [least, pos]
+  const int pos_lo = min(t.first_pos + p.token_of(t.row0), t.end - 1), pos_hi = t.last_pos;  // every row sees (pos_hi - window, pos_lo]
 
   Frag<C> q[KK];
   {
@@ -587,7 +593,7 @@ __device__ inline int v_place(int row, int piece) {
   return row / ROWS * v_block(D) + row % ROWS * KT + (piece ^ v_swap<D>(row)) * 8;
 }
 
-// The rows and places that one wave works on.
+// The row that a lane works on: its Q, and the keys [least, pos] that it sees.
 template <typename C, int D>
 struct ChunkRows {
   Frag<C> q[D / 16];
@@ -656,7 +662,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
   int pg = look(lo), next_pg = -1;
   if (lo < hi) fetch(lo, pg, 0);
   next_pg = look(lo + 1);
-  const int pos_lo = t.first_pos + p.token_of(t.row0), pos_hi = t.end - 1;
+  const int pos_lo = min(t.first_pos + p.token_of(t.row0), t.end - 1), pos_hi = t.last_pos;  // every row sees (pos_hi - window, pos_lo]
 #pragma unroll 1
   for (int tile = lo, buf = 0; tile < hi; ++tile, buf ^= 1) {
     // the tile has arrived, and every wave has left the other buffer
@@ -796,8 +802,8 @@ __global__ __launch_bounds__(chunk_threads(D), 2) void attn_chunk_kernel(AttnPar
     const bool ok = in < t.rows;
     const int row = t.row0 + (ok ? in : 0);
     const int token = p.token_of(row);
-    rows.pos = t.first_pos + token;
-    rows.least = a.window > 0 ? rows.pos - a.window + 1 : 0;
+    rows.pos = min(t.first_pos + token, t.end - 1);
+    rows.least = first_seen(a.window, t.first_pos + token);
     const C* src = static_cast<const C*>(a.q) + (t.t0 + token) * a.q_token + (int64_t)(t.kvh * p.group + row - token * p.group) * a.q_head + 8 * g;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
@@ -921,7 +927,6 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   p.scale2 = a.scale * kLog2e;
   p.group = a.heads / a.kv_heads;
   p.page_shift = __builtin_ctz(a.page);
-  if (a.window >= a.table_width * a.page) p.a.window = 0;  // as wide as any sequence: no window (and no sums beyond 31 bits)
   // row / group = row * ceil(2^(31 + s) / group) >> (31 + s) with 2^s >= group: 2 row times that, its high word, >> s
   const int sh = p.group == 1 ? 0 : 32 - __builtin_clz(p.group - 1);
   const uint64_t mul = ((uint64_t(1) << (31 + sh)) + p.group - 1) / p.group;

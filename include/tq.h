@@ -295,8 +295,10 @@ int tq_rope_append(const tq_rope_append_args *args, void *stream);
  * the cache at keys that no token of the sequence sees is not used, whatever
  * it holds, and table entries of pages that no token sees are not read.
  * block_table[b][j / page] is the page of key j.  A page outside [0, pages)
- * counts as keys that nobody sees, with bad_flag; so does kv_len[b] beyond
- * the table.  Query head h reads key head h / (heads / kv_heads).
+ * counts as keys that nobody sees, with bad_flag; so do the keys that kv_len[b]
+ * has beyond the table (positions and windows are kv_len's).  kv_len[b] < 0
+ * counts as 0, with bad_flag.  Query head h reads key head h / (heads /
+ * kv_heads).
  * Products are exact, sums and statistics fp32.  Probabilities enter the
  * product with V as two (fp16) or three (bf16) terms that hold 22 or 24 bits
  * when out is fp32; as two terms when out has the cache's type and the rows are
