@@ -34,9 +34,12 @@
 // transposed in just that order.
 //
 // Values that are not finite reach only later tokens of the recurrence, but
-// every row of a matrix product.  A chunk with any in q, k, v, beta or with
-// g > 0 is walked token after token instead (as are sequences of less than
-// kStepLen tokens).
+// every row of a matrix product.  A chunk with any in q, k, beta or with g > 0
+// is walked token after token instead (as are sequences of less than kStepLen
+// tokens), and so is one in which a token writes what is not finite or above
+// 2^63: the second kernel looks at X and at X with its decays before either is
+// used, and keeps the state before the chunk until then.  (A state that is not
+// finite therefore has every chunk walked.)
 //
 // Bound.  The walk: one chunk after another on 4 SIMDs per 32 columns, 2.4 us a
 // chunk at bf16, of which the matrix units take 0.7: splitting into terms, LDS
@@ -607,14 +610,11 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
             }
           }
           // R = beta V - far_k (K S)
-          float spoil = 0.f;  // NaN if anything is not finite
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float vj = row + j < now ? Raw<IN>::number(v[m][j]) : 0.f;
-              spoil = fmaf(vj, 0.f, spoil);
-              if (m == 0) spoil = fmaf(be[j], 0.f, spoil);
               y[m][j] = fmaf(be[j], vj, -fk[j] * (y[m][j] + y2[m][j]));
             }
             half_frag f[3];
@@ -622,11 +622,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
 #pragma unroll
             for (int e = 0; e < 3; ++e) *half(rf[s2][m][e], c2) = f[e];
           }
-          const bool bad = __any(spoil != 0.f);
-          if (lane == 0) odds[wave] = bad;
           load_k(len);
           lds_barrier();
-          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
           // X = T R
           {
             frag f[2][2][3];
@@ -654,17 +651,26 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
             if (s2 && !AHEAD) read(1);
             if (s2) product(1);
           }
+          // Squares: infinite or NaN long before a term is, and T's ones bring what is not finite in R (beta, v, the state, or an
+          // overflow) to X.
+          float size = 0.f;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             y[m] += y2[m];
+            const f32x4 z = y[m] * lk;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) size = fmaf(y[m][j], y[m][j], fmaf(z[j], z[j], size));
             half_frag f[3];
-            split4<3>(y[m] * lk, f);
+            split4<3>(z, f);
 #pragma unroll
             for (int e = 0; e < 3; ++e) *half(zf[s2][m][e], c2) = f[e];
             *reinterpret_cast<f32x4*>(&xs[s2][m][lane][4 * c2]) = y[m];
           }
+          const bool bad = __any(!(size < INFINITY));
+          if (lane == 0) odds[wave] = bad;
           load_t();
           lds_barrier();
+          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
           // S = decay S + K^T Z
 #pragma unroll
           for (int t = 0; t < HT; ++t)
@@ -736,7 +742,6 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
           const int now = (int)min((int64_t)kChunk, stop - done);
           if (done + kChunk < stop) unit += p.unit_bytes;
           lds_barrier();
-          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
           // far_q (Q S)
           f32x4 o[2] = {};
           {
@@ -765,6 +770,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
           for (int m = 0; m < 2; ++m) o[m] *= fq;
           load_q();
           lds_barrier();
+          odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
           frag f[2][2][OT];
 #pragma unroll
           for (int k = 0; k < 2; ++k)

@@ -342,10 +342,11 @@ int tq_paged_attn(const tq_paged_attn_args *args, void *stream);
  * workspace: nullable; with tq_gdn_workspace_bytes of scratch (needs no
  * clearing), sequences of 16 tokens and more are computed in chunks of 64 on
  * the matrix units, operands split into bf16 terms that hold fp32's 24 bits
- * (16 where they reach only an out of 16 bits).  What is not finite at a token
- * reaches later ones only, in chunks too.  max_len, where it is known, keeps
- * calls of more chunks than the workspace holds from looking for them past
- * every sequence's end. */
+ * (16 where they reach only an out of 16 bits).  What is not finite at a token,
+ * or overflows there, reaches later ones only, in chunks too (between chunks, a
+ * state's values above 2^128 - 2^119, which bf16 rounds to infinity, count as
+ * infinite).  max_len, where it is known, keeps calls of more chunks than the
+ * workspace holds from looking for them past every sequence's end. */
 typedef struct {
     const void *q, *k, *v; /* [tokens][k_heads | k_heads | v_heads][dk | dk | dv], in_type */
     int64_t q_token, q_head, k_token, k_head, v_token, v_head;

@@ -1,11 +1,12 @@
-"""Where the operators between a block's projections meet the ends of their ranges: lengths beyond the block table."""
+"""Where the operators between a block's projections meet the ends of their ranges: lengths beyond the block table, and
+finite inputs whose products are not."""
 import math
 
 import pytest
 import torch
 
 import seq_oracle as so
-from test_gpu_seq import BF, F32, HF, attn_inputs, near, tq  # noqa: F401  (tq: the fixture)
+from test_gpu_seq import BF, F32, HF, attn_inputs, gdn_inputs, near, tq  # noqa: F401  (tq: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,75 @@ def test_paged_attn_lengths_beyond_the_table(tq, new, hq, hk, dim, ct, ot, page,
         empty = torch.isinf(wl)
         assert torch.equal(torch.isinf(lse.cpu()), empty) and bool((lse.cpu()[empty] < 0).all())
         near(lse.cpu()[~empty], wl[~empty], ((dim + 4) * size + keys + 16 + wl.abs())[~empty] * so.U32, "lse")
+
+
+# ---- finite inputs, products that are not -----------------------------------------------------------------------------
+
+def gdn_run(tq, q, k, v, g, beta, state, cu, l2norm):
+    c = lambda x: x.cuda()  # noqa: E731
+    n = max(b - a for a, b in zip(cu, cu[1:]))
+    gs = state.cuda()
+    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=l2norm, out_dtype=F32, max_len=n,
+                 ws=tq.gdn_workspace(v.shape[0], len(cu) - 1, v.shape[1], k.shape[2], v.shape[2], max_len=n))
+    torch.cuda.synchronize()
+    return got.cpu(), gs.cpu()
+
+
+@pytest.mark.parametrize("late", [0, 37, 64, 100, 169])
+@pytest.mark.parametrize("what,beta_late", [(3e38, 1.5), (3.4e38, 1.0), (-3.4028234e38, 2.0), (-3.4e38, 1.0)])
+def test_gdn_a_late_overflow_stays_late(tq, late, what, beta_late):
+    """A write beyond fp32's range, or so near its end that its first bf16 term is infinite, reaches no token before its own,
+    no other head and no other column."""
+    n, vh, dk, dv = 170, 2, 128, 64
+    q, k, v, g, beta, state, cu = gdn_inputs([n], vh, vh, dk, dv, F32)
+    clean = v.clone()
+    v[late, 0, 5], beta[late, 0] = what, beta_late
+    clean[late, 0, 5] = 0
+    got, after = gdn_run(tq, q, k, v, g, beta, state, cu, True)
+    want, states, big = so.gdn(q, k, clean, g, beta, state, cu, dk**-0.5, True, 1e-6)
+    bound = so.gdn_bound(n, dk, big)
+    limit = so.HALF_STEP[F32] * want.abs() + bound * dk**-0.5
+    rest = [x for x in range(dv) if x != 5]
+    near(got[:late], want[:late], limit[:late], "tokens before it")
+    near(got[:, 1], want[:, 1], limit[:, 1], "the other head")
+    near(got[:, 0][:, rest], want[:, 0][:, rest], limit[:, 0][:, rest], "other columns")
+    near(after[0, 0][:, rest], states[0, 0][:, rest], torch.full((dk, dv - 1), bound), "other columns' states")
+    near(after[0, 1], states[0, 1], torch.full((dk, dv), bound), "the other head's state")
+
+
+def test_gdn_large_writes_of_short_keys(tq):
+    """Keys much shorter than their norm's eps: what a token writes fits fp32, what it writes over the key's norm does not."""
+    n, late, dk, dv = 130, 90, 128, 64
+    q, k, v, g, beta, state, cu = gdn_inputs([n], 1, 1, dk, dv, F32)
+    g[:] = 0
+    k[late] *= 1e-5
+    v[late, 0, 5] = 1e37
+    beta[late] = 1.0
+    got, after = gdn_run(tq, q, k, v, g, beta, state, cu, True)
+    want, states, big = so.gdn(q, k, v, g, beta, state, cu, dk**-0.5, True, 1e-6)
+    assert bool(torch.isfinite(states).all()) and big < 1e38
+    bound = so.gdn_bound(n, dk, big)
+    near(got[late:], want[late:], so.HALF_STEP[F32] * want[late:].abs() + bound * dk**-0.5, "out")
+    near(after, states, torch.full_like(states, bound), "state")
+    v[late, 0, 5] = 0
+    small, _, big = so.gdn(q, k, v, g, beta, state, cu, dk**-0.5, True, 1e-6)
+    near(got[:late], small[:late], so.HALF_STEP[F32] * small[:late].abs() + so.gdn_bound(n, dk, big) * dk**-0.5, "tokens before it")
+
+
+@pytest.mark.parametrize("late", [20, 63, 100])
+def test_gdn_a_large_state_row_is_met_late(tq, late):
+    """A row of the state near fp32's end that only a late token's key reaches, and overflows."""
+    n, dk, dv = 120, 64, 32
+    q, k, v, g, beta, state, cu = gdn_inputs([n], 1, 1, dk, dv, F32)
+    k[..., 0] = q[..., 0] = 0
+    k, q = (x / x.norm(dim=-1, keepdim=True) for x in (k, q))
+    clean = state.clone()
+    clean[..., 0, :] = 0
+    state[..., 0, :] = 3e38
+    g[:] = 0
+    k[late] = 0
+    k[late, 0, 0] = 1.0
+    v[late], beta[late] = -3e38, 1.0
+    got, _ = gdn_run(tq, q, k, v, g, beta, state, cu, False)
+    want, _, big = so.gdn(q[:late], k[:late], v[:late], g[:late], beta[:late], clean, [0, late], dk**-0.5, False, 1e-6)
+    near(got[:late], want, so.HALF_STEP[F32] * want.abs() + so.gdn_bound(n, dk, big) * dk**-0.5, "tokens before it")
