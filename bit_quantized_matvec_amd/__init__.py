@@ -45,6 +45,7 @@ _SIGS = {
     # the argument structs of these are passed as packed bytes (seq.py)
     "tq_rope_append": ([ctypes.c_char_p, _p], _i32),
     "tq_paged_attn_workspace_bytes": ([_i64, _i64, _i32, _i32, _i32], _i64),
+    "tq_paged_attn_tile_rows": ([_i64, _i64, _i64, _i32, _i32, _i32], _i32),
     "tq_paged_attn": ([ctypes.c_char_p, _p], _i32),
     "tq_gdn_workspace_bytes": ([_i64, _i64, _i64, _i32, _i32, _i32], _i64),
     "tq_gdn": ([ctypes.c_char_p, _p], _i32),

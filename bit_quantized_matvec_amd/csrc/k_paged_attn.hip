@@ -871,18 +871,20 @@ int64_t tiles_of(int64_t tokens, int64_t seqs, int group, int rows) {
 // joins longer.  attn_chunk where attn_rows would have two tiles or more per sequence and an eighth as many as the card
 // holds: over 4000 keys, rows against chunk, in us: 1 stream x 16 tokens x 12 heads, 2 x 256: 30, 58 (24 tiles); 8 streams
 // x 2 tokens: 35, 34 (32 tiles), x 4: 62, 42, x 16: 170, 69; 4 x 128, 8 streams x 2: 30, 31 (64 tiles), x 4: 43, 36.
-bool in_chunks(const tq_paged_attn_args& a, int group) {
-  if (a.tokens <= a.seqs) return false;
-  const int64_t rows = (a.max_len > 0 ? std::min(a.max_len, a.tokens) : (a.tokens + a.seqs - 1) / a.seqs) * group;
-  return rows > kRowsTile && tiles_of(a.tokens, a.seqs, group, kRowsTile) * a.kv_heads >= (1 << places_shift(a.dim)) / 8;
+bool in_chunks(int64_t tokens, int64_t seqs, int64_t max_len, int heads, int kv_heads, int dim) {
+  if (tokens <= seqs) return false;
+  const int group = heads / kv_heads;
+  const int64_t rows = (max_len > 0 ? std::min(max_len, tokens) : (tokens + seqs - 1) / seqs) * group;
+  return rows > kRowsTile && tiles_of(tokens, seqs, group, kRowsTile) * kv_heads >= (1 << places_shift(dim)) / 8;
 }
+bool in_chunks(const tq_paged_attn_args& a) { return in_chunks(a.tokens, a.seqs, a.max_len, a.heads, a.kv_heads, a.dim); }
 // `parts` and what joins them: one per kFan of a tile's.
 int64_t parts_bytes(int64_t parts, int rows, int dim) { return (parts + parts / 2 + kFan) * rows * (dim + 2) * 4; }
 
 template <typename C, typename O, int D>
 hipError_t launch_dim(AttnParams& p, hipStream_t s) {
   const auto& a = p.a;
-  const bool chunks = in_chunks(a, p.group);
+  const bool chunks = in_chunks(a);
   p.places_shift = places_shift(D);
   const int rows = chunks ? kChunkTile : kRowsTile;
   p.tiles_each = (p.group + rows - 1) / rows;
@@ -921,6 +923,10 @@ int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int 
   return kHeader + std::max(parts_bytes(kMaxParts, kRowsTile, dim), chunks ? parts_bytes(kMaxChunkParts, kChunkTile, dim) : 0);
 }
 
+int paged_attn_tile_rows(int64_t tokens, int64_t seqs, int64_t max_len, int heads, int kv_heads, int dim) {
+  return tokens > 0 && in_chunks(tokens, seqs, max_len, heads, kv_heads, dim) ? kChunkTile : kRowsTile;
+}
+
 hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   AttnParams p{a};
   // attn_chunk takes a negative scale's sign into Q, and masks by -inf before the scaling: a scale of zero is the least
@@ -931,7 +937,7 @@ hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s) {
   const int sh = p.group == 1 ? 0 : 32 - __builtin_clz(p.group - 1);
   const uint64_t mul = ((uint64_t(1) << (31 + sh)) + p.group - 1) / p.group;
   p.group_mul = (unsigned)mul, p.group_shift = (unsigned)sh;
-  if (in_chunks(a, p.group)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
+  if (in_chunks(a)) p.scale2 = std::max(std::fabs(p.scale2), FLT_MIN);
   if (a.cache_type == TQ_BF16) return a.out_type == TQ_F32 ? launch_type<bf16, float>(p, s) : launch_type<bf16, bf16>(p, s);
   return a.out_type == TQ_F32 ? launch_type<f16, float>(p, s) : launch_type<f16, f16>(p, s);
 }

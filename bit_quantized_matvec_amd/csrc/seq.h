@@ -13,6 +13,7 @@ namespace tq {
 hipError_t launch_rope_append(const tq_rope_append_args& a, hipStream_t s);
 
 int64_t paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int heads, int kv_heads, int dim);
+int paged_attn_tile_rows(int64_t tokens, int64_t seqs, int64_t max_len, int heads, int kv_heads, int dim);
 hipError_t launch_paged_attn(const tq_paged_attn_args& a, hipStream_t s);
 
 int64_t gdn_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int v_heads, int dk, int dv);

@@ -126,6 +126,11 @@ int64_t tq_paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int32_t head
   return tq::paged_attn_workspace_bytes(tokens, seqs, heads, kv_heads, dim);
 }
 
+int tq_paged_attn_tile_rows(int64_t tokens, int64_t seqs, int64_t max_len, int32_t heads, int32_t kv_heads, int32_t dim) {
+  if (attn_sizes(tokens, seqs, heads, kv_heads, dim) != TQ_OK || max_len < 0 || (tokens > 0 && seqs == 0)) return 0;
+  return tq::paged_attn_tile_rows(tokens, seqs, max_len, heads, kv_heads, dim);
+}
+
 int tq_paged_attn(const tq_paged_attn_args* a, void* stream) {
   if (!a) return TQ_ERR_NULL;
   const int st = attn_status(*a);

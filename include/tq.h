@@ -327,6 +327,10 @@ typedef struct {
 /* Bytes for any window, table and lengths of this many tokens and sequences;
  * 0 for sizes that tq_paged_attn refuses. */
 int64_t tq_paged_attn_workspace_bytes(int64_t tokens, int64_t seqs, int32_t heads, int32_t kv_heads, int32_t dim);
+/* Query rows (tokens times the heads of one key head) that a workgroup of such
+ * a call takes, 16 or 128, which is to say which of two kernels serves it; 0
+ * for sizes that tq_paged_attn refuses.  For tests and measurements. */
+int tq_paged_attn_tile_rows(int64_t tokens, int64_t seqs, int64_t max_len, int32_t heads, int32_t kv_heads, int32_t dim);
 int tq_paged_attn(const tq_paged_attn_args *args, void *stream);
 
 /* The gated delta rule.  Per value head (key head = value head / (v_heads /
