@@ -714,15 +714,16 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
       };
       read_v(0);
       in_order();
+      auto seen = [&](int b, int i) {
+        const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
+        return (there >> (2 * (at >> 4)) & 1) && key <= rows.pos && key >= rows.least;
+      };
       if (!whole)
 #pragma unroll
         for (int b = 0; b < SB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = 32 * b + 16 * (i >> 3) + 8 * g + (i & 7), key = k0 + at;
-            const bool ok = there >> (2 * (at >> 4)) & 1;
-              if (!(ok && key <= rows.pos && key >= rows.least)) s[b][i] = -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i)
+            if (!seen(b, i)) s[b][i] = -INFINITY;
       Frag<C> pf[SB][2][TERMS], sf[SB][2];
       {
         float mx = s[0][0];
@@ -753,7 +754,7 @@ __device__ __forceinline__ void chunk_pass(const AttnParams& p, const Tile& t, i
             split_terms<TERMS>(e + 8 * h, pf[b][h]);
             if constexpr (CAREFUL)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) sf[b][h][j] = (C)(s[b][8 * h + j] == -INFINITY ? 0.f : 1.f);
+              for (int j = 0; j < 8; ++j) sf[b][h][j] = (C)(seen(b, 8 * h + j) ? 1.f : 0.f);
           }
         }
       }

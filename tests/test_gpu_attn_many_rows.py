@@ -89,6 +89,32 @@ def test_paged_attn_a_late_value_stays_late(tq, ct, bad, new, hq, hk, rows, page
         assert bool(torch.isnan(hit).all() if math.isnan(bad) else (hit == bad).all())
 
 
+@pytest.mark.parametrize("new,hq,hk,rows", [(40, 32, 16, 128), (60, 2, 1, 16)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ct", [BF, HF])
+def test_paged_attn_a_seen_value_counts_whatever_its_score(tq, new, hq, hk, rows, dim, ct):
+    """A key with a score of minus infinity is seen all the same: an infinite value there is not passed over."""
+    keys, page, late = 100, 16, 70
+    serves(tq, [new], hq, hk, dim, rows)
+    q, kc, vc, table, cu = attn_inputs([new], [keys], hq, hk, dim, page, ct)
+    q[..., 0] = 1.0
+    kc[table[0, late // page], :, late % page, 0] = -math.inf
+    vc[table[0, late // page], :, 5, late % page] = math.inf
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = tq.paged_attn(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), ints([keys]), ints(cu), out_dtype=F32, max_len=new).cpu()
+    first = late - (keys - new)
+    assert not bool(torch.isfinite(got[first:, :, 5]).any())
+    kc[table[0, late // page], :, late % page, 0] = -60000.0  # a weight of nothing
+    vc[table[0, late // page], :, 5, late % page] = 0
+    want, _, spread, _ = so.attention(q, kc, vc, table, [keys], cu, dim**-0.5, 0)
+    kc[table[0, late // page], :, late % page, 0] = 0
+    size = so.attention(q, kc, vc, table, [keys], cu, dim**-0.5, 0)[3]  # of the scores that have weight
+    bound = so.attention_bound(want, spread, size, dim, keys, F32, ct)
+    rest = [x for x in range(dim) if x != 5]
+    near(got[:first], want[:first], bound[:first], "tokens before it")
+    near(got[first:][..., rest], want[first:][..., rest], bound[first:][..., rest], "other columns")
+
+
 @pytest.mark.parametrize("hq,hk,d,page,ct,ot", [(16, 16, 64, 16, HF, F32), (32, 16, 128, 16, BF, BF), (16, 16, 128, 64, HF, HF), (24, 8, 256, 16, BF, F32),
                                                 (8, 8, 256, 64, HF, HF)])
 def test_paged_attn_many_rows_bad_tables(tq, hq, hk, d, page, ct, ot):
