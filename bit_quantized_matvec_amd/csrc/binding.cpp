@@ -4,6 +4,7 @@
 // Python then say what is wrong, or serve what is rare (an output to be made, tensor subclasses).
 #include <Python.h>
 #include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -116,6 +117,7 @@ PyObject* finish(const Args& a, int (*call)(const ARGS*, void*), const ARGS& arg
   void* s = PyLong_AsVoidPtr(stream);
   Py_DECREF(stream);
   if (PyErr_Occurred()) return nullptr;
+  const c10::DeviceGuard guard(a.dev);  // the tensors' device, whatever the current one is
   const int status = call(&args, s);
   if (status != TQ_OK) return PyLong_FromLong(status);
   Py_INCREF(out);

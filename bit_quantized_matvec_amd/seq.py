@@ -11,6 +11,7 @@ Argument checks and marshalling only, as in the package; the arguments go to the
 """
 from __future__ import annotations
 
+import contextlib
 import math
 import struct
 
@@ -28,6 +29,14 @@ _ATTN = struct.Struct("@P2q2P3P3P1P7q7if0q")
 _GDN = struct.Struct("@3P6q2P2P2P2P1P5q7i2f0q")
 
 _stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _call(f, args: bytes, device, where: str) -> None:
+    """A call of the library on the tensors' device and that device's current stream."""
+    other = device.index is not None and device.index != _current_device()
+    with torch.cuda.device(device) if other else contextlib.nullcontext():
+        _check(f(args, _stream(device.index)), where)
 
 
 def _bad(name: str, t, want: str):
@@ -194,10 +203,10 @@ def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q_norm
         o = out.data_ptr()
     else:
         o = _full(out, cdt, (tokens, heads, dim), dev, "out")
-    _check(_lib.tq_rope_append(
-        _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, pos, slot, freq, wq, wk, o, kp, vp, _flag(bad_flag, dev),
-                   tokens, pages, heads, kv_heads, dim, rot, page, code, ccode, _LAYOUTS[layout], eps, rope_scale),
-        _stream(dev.index)), "tq_rope_append")
+    _call(_lib.tq_rope_append,
+          _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, pos, slot, freq, wq, wk, o, kp, vp, _flag(bad_flag, dev),
+                     tokens, pages, heads, kv_heads, dim, rot, page, code, ccode, _LAYOUTS[layout], eps, rope_scale),
+          dev, "tq_rope_append")
     return out
 
 
@@ -240,10 +249,10 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_len, cu=None, *, scale=None,
     out, o, ocode = _result(out, out_dtype, cdt, (tokens, heads, dim), dev)
     lp = _some(lse, torch.float32, (tokens, heads), dev, "lse")
     wp, wn = _ws(ws, 0 if ws is None else attn_workspace_bytes(tokens, seqs, heads, kv_heads, dim), dev)
-    _check(_lib.tq_paged_attn(
-        _ATTN.pack(q.data_ptr(), q0, q1, kp, vp, block_table.data_ptr(), lens, cup, o, lp, wp, _flag(bad_flag, dev), width, stride, tokens, seqs,
-                   pages, max_len, wn, heads, kv_heads, dim, page, ccode, ocode, window, dim**-0.5 if scale is None else scale),
-        _stream(dev.index)), "tq_paged_attn")
+    _call(_lib.tq_paged_attn,
+          _ATTN.pack(q.data_ptr(), q0, q1, kp, vp, block_table.data_ptr(), lens, cup, o, lp, wp, _flag(bad_flag, dev), width, stride, tokens, seqs,
+                     pages, max_len, wn, heads, kv_heads, dim, page, ccode, ocode, window, dim**-0.5 if scale is None else scale),
+          dev, "tq_paged_attn")
     return out
 
 
@@ -296,9 +305,9 @@ def gdn(q, k, v, g, beta, state, cu=None, *, slots=None, scale=None, l2norm: boo
     gp, bp = _full(g, torch.float32, row, dev, "g"), _full(beta, torch.float32, row, dev, "beta")
     out, o, ocode = _result(out, out_dtype, dt, (tokens, v_heads, dv), dev)
     wp, wn = _ws(ws, 0 if ws is None else gdn_workspace_bytes(tokens, seqs, v_heads, dk, dv, max_len), dev)
-    _check(_lib.tq_gdn(
-        _GDN.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, gp, bp, sp, so, slot, cup, o, wp, _flag(bad_flag, dev),
-                  tokens, seqs, states, max_len, wn, k_heads, v_heads, dk, dv, code, ocode, 1 if l2norm else 0,
-                  dk**-0.5 if scale is None else scale, eps),
-        _stream(dev.index)), "tq_gdn")
+    _call(_lib.tq_gdn,
+          _GDN.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, gp, bp, sp, so, slot, cup, o, wp, _flag(bad_flag, dev),
+                    tokens, seqs, states, max_len, wn, k_heads, v_heads, dk, dv, code, ocode, 1 if l2norm else 0,
+                    dk**-0.5 if scale is None else scale, eps),
+          dev, "tq_gdn")
     return out

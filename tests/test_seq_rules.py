@@ -1,5 +1,6 @@
 """Which kernel a call of the operators between a block's projections takes, by its sizes.  No kernel is launched."""
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -26,3 +27,46 @@ def test_paged_attn_rows_of_a_workgroup(rows):
                                   (1, 0, 1, 24, 2, 256), (1 << 21, 1, 1, 24, 2, 256)])
 def test_paged_attn_rows_of_refused_sizes(rows, args):
     assert rows(*args) == 0
+
+
+class OnSecondDevice(torch.Tensor):
+    """Host memory that claims to be on a second GPU."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+    @property
+    def device(self):
+        return torch.device("cuda", 1)
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """The tensors' device is made current around a call (none has anything to do here), and its stream is taken."""
+    import bit_quantized_matvec_amd as tq
+
+    current, calls = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(tq.seq, "_current_device", lambda: current[0])
+    monkeypatch.setattr(tq.seq, "_stream", lambda index: calls.append((index, current[0])))
+
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnSecondDevice)
+
+    i32, bf = torch.int32, torch.bfloat16
+    kc, vc = t(2, 1, 16, 64, dtype=bf), t(2, 1, 64, 16, dtype=bf)
+    tq.rope_append(t(0, 1, 64), t(0, 1, 64), t(0, 1, 64), None, t(0, dtype=torch.int64), None, kc, vc, out=t(0, 1, 64, dtype=bf))
+    tq.paged_attn(t(0, 1, 64, dtype=bf), kc, vc, t(1, 2, dtype=i32), t(1, dtype=i32), t(2, dtype=i32), out=t(0, 1, 64, dtype=bf))
+    tq.gdn(t(0, 1, 64), t(0, 1, 64), t(0, 1, 32), t(0, 1), t(0, 1), t(1, 1, 64, 32), t(1, dtype=i32), out=t(0, 1, 32))
+    assert calls == [(1, 1)] * 3 and current == [0]
