@@ -8,6 +8,7 @@ without fast-math (the q8_K quantizer relies on IEEE division and rounding).
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import tempfile
@@ -20,7 +21,8 @@ LIB = os.path.join(HERE, "libtq.so")
 # out of the product library
 PROBE_LIB = os.path.join(HERE, "libtq_probe.so")
 PROBE_SOURCES = ["hbm_probe.hip"]
-# argument checks of the ordinary call (binding.cpp): host code against torch's headers
+# argument checks of the ordinary call (binding.cpp): host code against torch's headers.  The package works without it, so
+# a machine without a C++ compiler or Python's headers still builds the rest.
 BINDING = os.path.join(HERE, "_binding.so")
 CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
@@ -57,9 +59,16 @@ def _build_binding() -> None:
 
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    missing = [x for x, there in ((CXX, shutil.which(CXX)), ("Python.h", os.path.exists(os.path.join(inc[2], "Python.h"))),
+                                  ("torch's headers", os.path.exists(os.path.join(inc[0], "ATen", "core", "Tensor.h")))) if not there]
+    if missing:
+        if os.path.exists(BINDING):  # (of other sources)
+            os.remove(BINDING)
+        sys.stderr.write(f"{os.path.basename(BINDING)} is not built: no {', no '.join(missing)}; the operators' calls take the host some 6 us more\n")
+        return
     lib = os.path.join(root, "lib")
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *[f for i in inc for f in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", LIB, f"-L{lib}",
+           f'-DTQ_TORCH_VERSION="{torch.__version__}"', *[f for i in inc for f in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", LIB, f"-L{lib}",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -85,7 +94,7 @@ def build(verbose: bool = False) -> str:
         subprocess.check_call([HIPCC, "-shared", f"--offload-arch={ARCH}", *pobjs, "-o", tmp_lib])
         os.replace(tmp_lib, PROBE_LIB)
     if verbose:
-        print("built", LIB, BINDING, "and", PROBE_LIB)
+        print("built", ", ".join(x for x in (LIB, BINDING, PROBE_LIB) if os.path.exists(x)))
     return LIB
 
 

@@ -257,5 +257,7 @@ PyMODINIT_FUNC PyInit__binding() {
   if (!c) return nullptr;
   g_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream");
   Py_DECREF(c);
-  return g_stream ? PyModule_Create(&g_module) : nullptr;
+  PyObject* m = g_stream ? PyModule_Create(&g_module) : nullptr;
+  if (m && PyModule_AddStringConstant(m, "torch_version", TQ_TORCH_VERSION) != 0) Py_CLEAR(m);  // whose headers this was built with
+  return m;
 }

@@ -14,11 +14,30 @@ from __future__ import annotations
 import contextlib
 import math
 import struct
+import warnings
 
 import torch
 
 from . import ERR_SHAPE, TQError, _check, _lib
-from . import _binding  # the ordinary call, checked in C++; None where these checks have to say what is wrong or serve what is rare
+
+
+def _load_binding():
+    """The checks of the ordinary call in C++: where these checks have to say what is wrong or serve what is rare, its calls
+    return None.  Where it is not there, or was built for another torch (whose classes it reads), these checks serve every call."""
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        why = str(e)
+    else:
+        built = getattr(b, "torch_version", None)
+        if built == torch.__version__:
+            return b
+        why = f"it was built for torch {built}"
+    warnings.warn(f"_binding.so is not used ({why}): each of these operators' calls takes the host some 6 us more; build.py builds it", stacklevel=3)
+    return None
+
+
+_binding = _load_binding()
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
@@ -172,7 +191,7 @@ def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q_norm
     q [tokens, heads, dim], k and v [tokens, kv_heads, dim]: fp32, bf16 or fp16, any token and head strides (views of
     a fused projection's rows).  positions int32 [tokens]; slots int64 [tokens] (page * page size + place, negative:
     not stored); inv_freq float64 [rot / 2] or None; q_norm and k_norm fp32 [dim] or None."""
-    if out is not None and layout in _LAYOUTS:
+    if _binding and out is not None and layout in _LAYOUTS:
         r = _binding.rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, q_norm, k_norm, eps, _LAYOUTS[layout], rope_scale, out, bad_flag)
         if r is out:
             return out
@@ -227,7 +246,7 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_len, cu=None, *, scale=None,
     included; cu int32 [seqs + 1] or None (one token each); scale defaults to dim^-1/2; window 0 = all earlier keys;
     max_len: the longest sequence's new tokens, if known.  out in the cache's type or fp32; lse: fp32 [tokens, heads]
     to be filled, or None; ws: see ``attn_workspace``."""
-    if out is not None and out_dtype is None:
+    if _binding and out is not None and out_dtype is None:
         r = _binding.paged_attn(q, k_cache, v_cache, block_table, kv_len, cu, scale, window, max_len, out, lse, ws, bad_flag)
         if r is out:
             return out
@@ -275,7 +294,7 @@ def gdn(q, k, v, g, beta, state, cu=None, *, slots=None, scale=None, l2norm: boo
     (one token each); slots int32 [seqs] into the states, or None (sequence b has state b); scale defaults to
     dk^-1/2; l2norm: q and k are normalised per head first; ws: see ``gdn_workspace``.  Returns out [tokens, v_heads,
     dv] in the inputs' type or fp32."""
-    if out is not None and out_dtype is None:
+    if _binding and out is not None and out_dtype is None:
         r = _binding.gdn(q, k, v, g, beta, state, cu, slots, scale, 1 if l2norm else 0, eps, max_len, out, state_out, ws, bad_flag)
         if r is out:
             return out
