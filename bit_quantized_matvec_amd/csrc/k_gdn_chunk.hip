@@ -19,9 +19,12 @@
 // norms and decays multiply rows of results.  Where out has 16 bits, what goes
 // only into it (S in S^T q, P, X in P X) takes 2 terms: 2^-17 of the values'
 // size beside the 2^-9 or 2^-12 of the output's own rounding.
-// T is built in fp32 on the fp32 matrix instructions.  Every entry that the
-// block recursion forms is one of T's own, and those are bounded by the
-// recurrence's transitions, so nothing grows on the way.
+// T is built in fp32 on the fp32 matrix instructions.  T maps R to X, as the
+// recurrence does: with beta |k|^2 <= 2, which l2norm and beta <= 2 ensure, its
+// transitions shrink the state and T's entries stay small.  The recursion over
+// blocks forms T's own entries and, between them, A21 T11: sums of at most 32
+// products of A (at most beta each) and T.  Keys that are longer and not
+// normalised let T grow as the recurrence itself grows.
 //
 // Layout.  A matrix-instruction result leaves lane (n, g) with rows 4g .. 4g+3
 // of column n, and an operand wants 8g .. 8g+7 of the summed index.  Rows of
@@ -44,8 +47,8 @@
 // Bound.  The walk: one chunk after another on 4 SIMDs per 32 columns, 2.4 us a
 // chunk at bf16, of which the matrix units take 0.7: splitting into terms, LDS
 // between the products and three barriers are the rest.  4096 bf16 tokens, 48
-// heads of 128 x 128: 181 us, 44 of them in the first kernel (149 MB written);
-// token after token 6063.  Five fp32 sequences of 77 to 701 tokens: 177 us (1290).
+// heads of 128 x 128: 179 us, 44 of them in the first kernel (149 MB written);
+// token after token 6063.  Five fp32 sequences of 77 to 701 tokens: 175 us (1290).
 // What else was measured at the first: one wave per 16 columns without LDS 1777
 // us (its loads wait one by one), eight waves of 16 columns that all do the same
 // 264, four waves that compute the outputs too 251.

@@ -47,8 +47,8 @@
 //   attn_chunk   128 query rows per workgroup, 32 per wave; K and V tiles go
 //                straight from memory into LDS, double-buffered, shared by the
 //                waves.  Bound by the matrix units and the exponentials beside
-//                them: 2048 tokens over 8100 keys, 48 x 128: 395 us, 900
-//                TFLOP/s (a large library product reaches 1170); with the
+//                them: 2048 tokens over 8100 keys, 48 x 128: 393 to 409 us, 870
+//                to 905 TFLOP/s (a large library product reaches 1170); with the
 //                probabilities as two terms and 256 columns, 6 prompts in a
 //                window of 1024: 153 us.
 //
@@ -362,7 +362,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_rows_kernel(A
   const int part = blockIdx.x / (unsigned)p.tiles, tile = p.tile_of(blockIdx.x - part * p.tiles, part);
   const Tile t = find_tile<kRowsTile>(p, tile, lane);
   if (t.rows <= 0) return;
-  // blocks of 32 keys; every wave of a part has at least one
+  // Blocks of 32 keys, every fourth of a part for each wave.  A wave that has none (less than 97 keys, or parts of 3 blocks)
+  // leaves m = -inf, l = 0, and the joins pass over it.
   const int first = t.begin / kBlock, blocks = t.end > 0 ? (t.end + kBlock - 1) / kBlock - first : 0;
   // Parts of equal length that fill the places once; of kLong blocks at most where sequences may differ in length, so that
   // the longest does not hold up the end (32 streams of 2 to 8 thousand keys, 128 columns: 144 us in one round, 91 in parts

@@ -22,8 +22,9 @@
 // Bound: bytes (every value read and written once); launch latency for a few
 // tokens.  4099 fp32 tokens of 28 heads of 256: 176 MB in 52 us = 3.4 TB/s (the
 // V workgroups cost 4.5 of them, forming the angles 7; two workgroups per token
-// 59 us, rows asked for two to five passes ahead 53 to 56); 64 bf16 tokens 6.0
-// us; one token 4.4 us, the launch.
+// 59 us, rows asked for two to five passes ahead 53 to 56), or 39 us on the
+// tensors of the call before, which the last-level cache holds in part; 64 bf16
+// tokens 6.0 us; one token 4.4 us, the launch.
 #include <algorithm>
 
 #include "seq.h"

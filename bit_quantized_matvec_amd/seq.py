@@ -245,7 +245,8 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_len, cu=None, *, scale=None,
     q [tokens, heads, dim] in the cache's type; block_table int32 [seqs, width]; kv_len int32 [seqs], new tokens
     included; cu int32 [seqs + 1] or None (one token each); scale defaults to dim^-1/2; window 0 = all earlier keys;
     max_len: the longest sequence's new tokens, if known.  out in the cache's type or fp32; lse: fp32 [tokens, heads]
-    to be filled, or None; ws: see ``attn_workspace``."""
+    to be filled, or None.  ws: see ``attn_workspace``; without one no sequence's keys are split over workgroups
+    (one stream over 131075 keys 3.5 ms instead of 0.07, over 1000 keys 40 us instead of 18)."""
     if _binding and out is not None and out_dtype is None:
         r = _binding.paged_attn(q, k_cache, v_cache, block_table, kv_len, cu, scale, window, max_len, out, lse, ws, bad_flag)
         if r is out:
@@ -292,8 +293,10 @@ def gdn(q, k, v, g, beta, state, cu=None, *, slots=None, scale=None, l2norm: boo
     q and k [tokens, k_heads, dk], v [tokens, v_heads, dv]: fp32, bf16 or fp16, any token and head strides; g (log
     decay, <= 0) and beta fp32 [tokens, v_heads]; state fp32 [states, v_heads, dk, dv]; cu int32 [seqs + 1] or None
     (one token each); slots int32 [seqs] into the states, or None (sequence b has state b); scale defaults to
-    dk^-1/2; l2norm: q and k are normalised per head first; ws: see ``gdn_workspace``.  Returns out [tokens, v_heads,
-    dv] in the inputs' type or fp32."""
+    dk^-1/2; l2norm: q and k are normalised per head first.  ws: see ``gdn_workspace``; without one long sequences go
+    token after token (4096 tokens in 5.6 ms instead of 0.19).  max_len: the longest sequence's tokens; without it the
+    call is taken for one long sequence, which several short ones pay for (8 of 4 tokens 59 us instead of 23).  Returns
+    out [tokens, v_heads, dv] in the inputs' type or fp32."""
     if _binding and out is not None and out_dtype is None:
         r = _binding.gdn(q, k, v, g, beta, state, cu, slots, scale, 1 if l2norm else 0, eps, max_len, out, state_out, ws, bad_flag)
         if r is out:
