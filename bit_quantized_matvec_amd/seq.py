@@ -51,6 +51,13 @@ _stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
+def _pack(form: struct.Struct, where: str, *fields) -> bytes:
+    try:
+        return form.pack(*fields)
+    except (struct.error, OverflowError) as e:  # what no field holds
+        raise ValueError(f"{where}: an argument that is no number, or out of its type's range ({e})") from None
+
+
 def _call(f, args: bytes, device, where: str) -> None:
     """A call of the library on the tensors' device and that device's current stream."""
     other = device.index is not None and device.index != _current_device()
@@ -208,6 +215,8 @@ def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q_norm
         raise TQError(ERR_SHAPE, f"rope_append: q {tuple(q.shape)}, k {tuple(kn)}, v {tuple(vn)} and k_cache {tuple(k_cache.shape)} do not fit")
     rot = 0
     if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor):
+            _bad("inv_freq", inv_freq, "a float64 CUDA tensor [rot / 2], or None")
         rot = 2 * inv_freq.numel()
     if layout not in _LAYOUTS:
         raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
@@ -223,8 +232,8 @@ def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q_norm
     else:
         o = _full(out, cdt, (tokens, heads, dim), dev, "out")
     _call(_lib.tq_rope_append,
-          _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, pos, slot, freq, wq, wk, o, kp, vp, _flag(bad_flag, dev),
-                     tokens, pages, heads, kv_heads, dim, rot, page, code, ccode, _LAYOUTS[layout], eps, rope_scale),
+          _pack(_ROPE, "rope_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, pos, slot, freq, wq, wk, o, kp, vp,
+                _flag(bad_flag, dev), tokens, pages, heads, kv_heads, dim, rot, page, code, ccode, _LAYOUTS[layout], eps, rope_scale),
           dev, "tq_rope_append")
     return out
 
@@ -270,8 +279,8 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_len, cu=None, *, scale=None,
     lp = _some(lse, torch.float32, (tokens, heads), dev, "lse")
     wp, wn = _ws(ws, 0 if ws is None else attn_workspace_bytes(tokens, seqs, heads, kv_heads, dim), dev)
     _call(_lib.tq_paged_attn,
-          _ATTN.pack(q.data_ptr(), q0, q1, kp, vp, block_table.data_ptr(), lens, cup, o, lp, wp, _flag(bad_flag, dev), width, stride, tokens, seqs,
-                     pages, max_len, wn, heads, kv_heads, dim, page, ccode, ocode, window, dim**-0.5 if scale is None else scale),
+          _pack(_ATTN, "paged_attn", q.data_ptr(), q0, q1, kp, vp, block_table.data_ptr(), lens, cup, o, lp, wp, _flag(bad_flag, dev), width, stride,
+                tokens, seqs, pages, max_len, wn, heads, kv_heads, dim, page, ccode, ocode, window, dim**-0.5 if scale is None else scale),
           dev, "tq_paged_attn")
     return out
 
@@ -328,8 +337,8 @@ def gdn(q, k, v, g, beta, state, cu=None, *, slots=None, scale=None, l2norm: boo
     out, o, ocode = _result(out, out_dtype, dt, (tokens, v_heads, dv), dev)
     wp, wn = _ws(ws, 0 if ws is None else gdn_workspace_bytes(tokens, seqs, v_heads, dk, dv, max_len), dev)
     _call(_lib.tq_gdn,
-          _GDN.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, gp, bp, sp, so, slot, cup, o, wp, _flag(bad_flag, dev),
-                    tokens, seqs, states, max_len, wn, k_heads, v_heads, dk, dv, code, ocode, 1 if l2norm else 0,
-                    dk**-0.5 if scale is None else scale, eps),
+          _pack(_GDN, "gdn", q.data_ptr(), k.data_ptr(), v.data_ptr(), q0, q1, k0, k1, v0, v1, gp, bp, sp, so, slot, cup, o, wp,
+                _flag(bad_flag, dev), tokens, seqs, states, max_len, wn, k_heads, v_heads, dk, dv, code, ocode, 1 if l2norm else 0,
+                dk**-0.5 if scale is None else scale, eps),
           dev, "tq_gdn")
     return out

@@ -70,3 +70,28 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     tq.paged_attn(t(0, 1, 64, dtype=bf), kc, vc, t(1, 2, dtype=i32), t(1, dtype=i32), t(2, dtype=i32), out=t(0, 1, 64, dtype=bf))
     tq.gdn(t(0, 1, 64), t(0, 1, 64), t(0, 1, 32), t(0, 1), t(0, 1), t(1, 1, 64, 32), t(1, dtype=i32), out=t(0, 1, 32))
     assert calls == [(1, 1)] * 3 and current == [0]
+
+
+@pytest.mark.parametrize("call,over", [
+    ("rope", dict(inv_freq=[1.0] * 32)), ("rope", dict(eps="small")), ("rope", dict(rope_scale=None)),
+    ("attn", dict(window=2**31)), ("attn", dict(window=1.5)), ("attn", dict(max_len=None)), ("attn", dict(max_len=2**63)), ("attn", dict(scale="1")),
+    ("gdn", dict(max_len=2**64)), ("gdn", dict(eps=None)),
+])
+def test_arguments_that_no_field_holds(call, over):
+    import bit_quantized_matvec_amd as tq
+
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnSecondDevice)
+
+    i32, bf = torch.int32, torch.bfloat16
+    kc, vc = t(2, 1, 16, 64, dtype=bf), t(2, 1, 64, 16, dtype=bf)
+    if call == "rope":
+        f, a = tq.rope_append, dict(q=t(0, 1, 64), k=t(0, 1, 64), v=t(0, 1, 64), positions=t(0, dtype=i32), slots=t(0, dtype=torch.int64),
+                                    inv_freq=t(32, dtype=torch.float64), k_cache=kc, v_cache=vc, out=t(0, 1, 64, dtype=bf))
+    elif call == "attn":
+        f, a = tq.paged_attn, dict(q=t(0, 1, 64, dtype=bf), k_cache=kc, v_cache=vc, block_table=t(1, 2, dtype=i32), kv_len=t(1, dtype=i32),
+                                   cu=t(2, dtype=i32), out=t(0, 1, 64, dtype=bf))
+    else:
+        f, a = tq.gdn, dict(q=t(0, 1, 64), k=t(0, 1, 64), v=t(0, 1, 32), g=t(0, 1), beta=t(0, 1), state=t(1, 1, 64, 32), cu=t(1, dtype=i32), out=t(0, 1, 32))
+    with pytest.raises(ValueError):
+        f(**{**a, **over})
