@@ -37,12 +37,13 @@
 // transposed in just that order.
 //
 // Values that are not finite reach only later tokens of the recurrence, but
-// every row of a matrix product.  A chunk with any in q, k, beta or with g > 0
-// is walked token after token instead (as are sequences of less than kStepLen
-// tokens), and so is one in which a token writes what is not finite or above
-// 2^63: the second kernel looks at X and at X with its decays before either is
-// used, and keeps the state before the chunk until then.  (A state that is not
-// finite therefore has every chunk walked.)
+// every row of a matrix product.  A chunk with any in q, k, beta, with g > 0 or
+// a 1 / |k| above kMostNorm is walked token after token instead (as are
+// sequences of less than kStepLen tokens), and so is one in which a token writes
+// what is not finite or above 2^63: the second kernel looks at X before it is
+// used, and keeps the state before the chunk until then.  A column whose state is
+// not finite stays so, and all its outputs with it, either way: after the first
+// chunk that it has walked it is not looked at any more.
 //
 // Bound.  The walk: one chunk after another on 4 SIMDs per 32 columns, 2.4 us a
 // chunk at bf16, of which the matrix units take 0.7: splitting into terms, LDS
@@ -71,6 +72,7 @@ constexpr int64_t kBudget = int64_t(256) << 20;  // workspace: what the last-lev
 constexpr int kFragBytes = 1024;
 constexpr int kScalarBytes = 2048;
 constexpr float kLeastG = -1024.f;  // e^g is 0 in fp32 far above
+constexpr float kMostNorm = 0x1p60f;  // of 1 / |k|: what a token writes, below 2^64, stays finite times it
 
 typedef bf16 frag __attribute__((ext_vector_type(8)));
 
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void gdn_prepare_kernel(ChunkParam
   qq += __shfl_xor(qq, 16, 64), kk += __shfl_xor(kk, 16, 64);
   qq += __shfl_xor(qq, 32, 64), kk += __shfl_xor(kk, 32, 64);
   float nq = (a.l2norm ? 1.f / sqrtf(qq + a.eps) : 1.f) * a.scale, nk = a.l2norm ? 1.f / sqrtf(kk + a.eps) : 1.f;
-  const bool odd_rows = i < len && (!(qq < INFINITY) || !(kk < INFINITY) || !(fabsf(nq) < INFINITY) || !(nk < INFINITY));
+  const bool odd_rows = i < len && (!(qq < INFINITY) || !(kk < INFINITY) || !(fabsf(nq) < INFINITY) || !(nk < kMostNorm));
   if (i >= len) nq = nk = 0.f;
   if (g == 0) norms[i] = nk;
   __syncthreads();
@@ -506,6 +508,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
       }
   };
 
+  uint64_t seen[2] = {~uint64_t(0), ~uint64_t(0)};  // the lanes whose column's state may be finite
   int64_t done = r.n < kStepLen ? 0 : from;
   const int64_t stop = r.n < kStepLen ? 0 : min((int64_t)r.n, from + (int64_t)p.chunks * kChunk);
   while (true) {
@@ -654,24 +657,23 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
             if (s2 && !AHEAD) read(1);
             if (s2) product(1);
           }
-          // Squares: infinite or NaN long before a term is, and T's ones bring what is not finite in R (beta, v, the state, or an
-          // overflow) to X.
-          float size = 0.f;
+          // Squares: infinite or NaN long before a term is (lk is below kMostNorm), and T's ones bring what is not finite in R
+          // (beta, v, the state, or an overflow) to X.
+          float size[2] = {};
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             y[m] += y2[m];
-            const f32x4 z = y[m] * lk;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) size = fmaf(y[m][j], y[m][j], fmaf(z[j], z[j], size));
+            for (int j = 0; j < 4; ++j) size[m] = fmaf(y[m][j], y[m][j], size[m]);
             half_frag f[3];
-            split4<3>(z, f);
+            split4<3>(y[m] * lk, f);
 #pragma unroll
             for (int e = 0; e < 3; ++e) *half(zf[s2][m][e], c2) = f[e];
             *reinterpret_cast<f32x4*>(&xs[s2][m][lane][4 * c2]) = y[m];
           }
-          const bool bad = __any(!(size < INFINITY));
-          if (lane == 0) odds[wave] = bad;
           load_t();
+          const uint64_t bad = (__ballot(!(size[0] < INFINITY)) & seen[0]) | (__ballot(!(size[1] < INFINITY)) & seen[1]);
+          if (lane == 0) odds[wave] = bad != 0;
           lds_barrier();
           odd = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) != 0;
           // S = decay S + K^T Z
@@ -807,6 +809,26 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_walk_kernel(ChunkParams p
     }
     if (walk_to > done) walk(r.t0 + done, r.t0 + walk_to), done = walk_to;
     if (!odd) break;
+    if (carries) {
+      unsigned mine = 0;  // bit 16 m + n: column n of m, as far as this wave's rows go
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < HT; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) any = any || !(fabsf(s[e][m][j]) < INFINITY);
+        const uint64_t b = __ballot(any);
+        mine |= ((unsigned)(b | b >> 16 | b >> 32 | b >> 48) & 0xFFFFu) << 16 * m;
+      }
+      if (lane == 0) odds[wave] = mine;
+    }
+    lds_barrier();
+    if (carries) {
+      const unsigned lost = __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) seen[m] = ~(uint64_t(0x0001000100010001) * (lost >> 16 * m & 0xFFFFu));
+    }
   }
 
   if (!carries || (ends && (!kept || (r.n == 0 && a.state_out == a.state)))) return;

@@ -65,11 +65,11 @@ def test_paged_attn_lengths_beyond_the_table(tq, new, hq, hk, dim, ct, ot, page,
 
 # ---- finite inputs, products that are not -----------------------------------------------------------------------------
 
-def gdn_run(tq, q, k, v, g, beta, state, cu, l2norm):
+def gdn_run(tq, q, k, v, g, beta, state, cu, l2norm, eps=1e-6):
     c = lambda x: x.cuda()  # noqa: E731
     n = max(b - a for a, b in zip(cu, cu[1:]))
     gs = state.cuda()
-    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=l2norm, out_dtype=F32, max_len=n,
+    got = tq.gdn(c(q), c(k), c(v), c(g), c(beta), gs, torch.tensor(cu, dtype=torch.int32, device="cuda"), l2norm=l2norm, eps=eps, out_dtype=F32, max_len=n,
                  ws=tq.gdn_workspace(v.shape[0], len(cu) - 1, v.shape[1], k.shape[2], v.shape[2], max_len=n))
     torch.cuda.synchronize()
     return got.cpu(), gs.cpu()
@@ -133,3 +133,45 @@ def test_gdn_a_large_state_row_is_met_late(tq, late):
     got, _ = gdn_run(tq, q, k, v, g, beta, state, cu, False)
     want, _, big = so.gdn(q[:late], k[:late], v[:late], g[:late], beta[:late], clean, [0, late], dk**-0.5, False, 1e-6)
     near(got[:late], want, so.HALF_STEP[F32] * want.abs() + so.gdn_bound(n, dk, big) * dk**-0.5, "tokens before it")
+
+
+@pytest.mark.parametrize("it", [F32, BF])
+def test_gdn_columns_that_are_lost_leave_the_others(tq, it):
+    """A column whose state is not finite: all its outputs are not from there on, and the others go on as ever, a later
+    overflow's column, too, up to its own token."""
+    n, vh, dk, dv = 700, 2, 128, 64
+    q, k, v, g, beta, state, cu = gdn_inputs([n], vh, vh, dk, dv, it)
+    clean, start = v.clone(), state.clone()
+    state[0, 0, 3, 7] = math.inf                 # from the first token on
+    v[70, 0, 5] = math.nan                       # from token 70 on
+    v[300, 0, 40], beta[300, 0] = 3e38, 1.75     # from token 300 on: the write overflows
+    v[555, 0, 41] = -math.inf
+    clean[300, 0, 40] = 0
+    got, after = gdn_run(tq, q, k, v, g, beta, state, cu, True)
+    want, states, big = so.gdn(q, k, clean, g, beta, start, cu, dk**-0.5, True, 1e-6)
+    bound = so.gdn_bound(n, dk, big)
+    limit = so.HALF_STEP[F32] * want.abs() + bound * dk**-0.5
+    near(got[:, 1], want[:, 1], limit[:, 1], "the other head")
+    near(after[0, 1], states[0, 1], torch.full((dk, dv), bound), "the other head's state")
+    for col in range(dv):
+        first = {7: 0, 5: 70, 40: 300, 41: 555}.get(col, n)
+        near(got[:first, 0, col], want[:first, 0, col], limit[:first, 0, col], f"column {col}")
+        assert not bool(torch.isfinite(got[first:, 0, col]).any()), col
+        if first == n:
+            near(after[0, 0, :, col], states[0, 0, :, col], torch.full((dk,), bound), f"state of column {col}")
+        else:
+            assert not bool(torch.isfinite(after[0, 0, :, col]).any()), col
+
+
+@pytest.mark.parametrize("power", [-30, -61])
+def test_gdn_keys_of_next_to_no_length(tq, power):
+    """With eps = 0 a key's norm is one however short the key is."""
+    n, dk, dv = 150, 128, 64
+    q, k, v, g, beta, state, cu = gdn_inputs([n], 1, 1, dk, dv, F32)
+    k = k / k.norm(dim=-1, keepdim=True)
+    k[70:80] *= 2.0**power
+    got, after = gdn_run(tq, q, k, v, g, beta, state, cu, True, eps=0.0)
+    want, states, big = so.gdn(q, k, v, g, beta, state, cu, dk**-0.5, True, 0.0)
+    bound = so.gdn_bound(n, dk, big)
+    near(got, want, so.HALF_STEP[F32] * want.abs() + bound * dk**-0.5, "out")
+    near(after, states, torch.full_like(states, bound), "state")
