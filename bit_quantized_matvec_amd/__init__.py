@@ -49,6 +49,14 @@ _SIGS = {
     "tq_paged_attn": ([ctypes.c_char_p, _p], _i32),
     "tq_gdn_workspace_bytes": ([_i64, _i64, _i64, _i32, _i32, _i32], _i64),
     "tq_gdn": ([ctypes.c_char_p, _p], _i32),
+    # and of these too (batch.py)
+    "tq_route": ([ctypes.c_char_p, _p], _i32),
+    "tq_expert_lists": ([_p, _i64, _i32, _p, _p, _p], _i32),
+    "tq_gemm_experts": ([ctypes.c_char_p, _p], _i32),
+    "tq_adapter_workspace_bytes": ([_i64, _i32, _i32, _i64], _i64),
+    "tq_adapter_add": ([ctypes.c_char_p, _p], _i32),
+    "tq_sample_workspace_bytes": ([_i64, _i64], _i64),
+    "tq_sample": ([ctypes.c_char_p, _p], _i32),
     "tq_status_str": ([_i32], ctypes.c_char_p),
     "tq_last_hip_error": ([], _i32),
     "tq_version": ([], _i32),
@@ -351,3 +359,5 @@ class TernaryMatrix:
 
 from .seq import (attn_workspace, attn_workspace_bytes, gdn, gdn_workspace, gdn_workspace_bytes, kv_cache,  # noqa: E402
                   paged_attn, rope_append, rope_frequencies)
+from .batch import (adapter_add, adapter_workspace, adapter_workspace_bytes, expert_lists, gemm_experts, route, sample,  # noqa: E402
+                    sample_workspace, sample_workspace_bytes)

@@ -28,7 +28,8 @@ CXX = os.environ.get("CXX", "g++")
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["tq_api.cpp", "k_workspace.hip", "scratch.hip", "k_quant.hip", "k_repack.hip", "k_gemv_pq2.hip", "k_gemm_pq2.hip", "k_gemv_ptq1.hip", "k_gemm_ptq1.hip",
-           "seq_api.cpp", "k_rope_append.hip", "k_paged_attn.hip", "k_gdn.hip", "k_gdn_chunk.hip"]
+           "seq_api.cpp", "k_rope_append.hip", "k_paged_attn.hip", "k_gdn.hip", "k_gdn_chunk.hip",
+           "batch_api.cpp", "k_route.hip", "k_experts_pq2.hip", "k_adapter.hip", "k_sample.hip"]
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -38,7 +39,8 @@ FLAGS = [
 # Per-source extras: the MFMA kernels keep their accumulators in ordinary
 # VGPRs, so the epilogues read them without v_accvgpr_read copies.
 EXTRA = {"k_gemm_pq2.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "k_gemm_ptq1.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "k_gemm_ptq1.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "k_experts_pq2.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str, out: str, extra=()) -> None:

@@ -1,4 +1,4 @@
-// binding.cpp -- the argument checks of seq.py for the ordinary call, in C++: a decode call takes the GPU 5 us, and reading
+// binding.cpp -- the argument checks of seq.py and batch.py for the ordinary call, in C++: a decode call takes the GPU 5 us, and reading
 // some twelve tensors' types, shapes, strides and devices from Python 7 more.  Each function either does the whole call
 // (returns out, or the status that the C ABI refused it with), or returns None and has touched nothing: the caller's checks in
 // Python then say what is wrong, or serve what is rare (an output to be made, tensor subclasses).
@@ -226,6 +226,141 @@ PyObject* gdn(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return finish(a, tq_gdn, r, argv[12]);
 }
 
+// [rows, columns] with contiguous rows
+const void* matrix(Args& a, int i, at::IntArrayRef* shape, int64_t* stride, int* type) {
+  const at::Tensor* t = a.tensor(i);
+  if (!t || t->dim() != 2 || t->device() != a.dev) return a.fail(), nullptr;
+  *type = type_code(t->scalar_type());
+  *shape = t->sizes();
+  if (*type < 0 || (t->stride(1) != 1 && (*shape)[1] > 1)) return a.fail(), nullptr;
+  *stride = (*shape)[0] > 1 ? t->stride(0) : 0;
+  return t->data_ptr();
+}
+
+// The two tensors of a pair of outputs, in place of the pair.
+bool pair(const Args& a, int i, PyObject** first, PyObject** second) {
+  if (!PyTuple_CheckExact(a.v[i]) || PyTuple_GET_SIZE(a.v[i]) != 2) return false;
+  *first = PyTuple_GET_ITEM(a.v[i], 0), *second = PyTuple_GET_ITEM(a.v[i], 1);
+  return true;
+}
+
+// logits, k, score, bias, groups, top_groups, group_best, renorm, scale, out
+PyObject* route(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  Args a{argv, n};
+  if (n != 10 || !leader(a, 0)) Py_RETURN_NONE;
+  PyObject* outs[2];
+  if (!pair(a, 9, &outs[0], &outs[1])) Py_RETURN_NONE;
+  tq_route_args r{};
+  at::IntArrayRef s;
+  r.logits = matrix(a, 0, &s, &r.logit_stride, &r.in_type);
+  if (!a.ok) Py_RETURN_NONE;
+  r.tokens = s[0], r.experts = dim32(s[1]);
+  r.bias = static_cast<const float*>(a.some(3, at::kFloat, {s[1]}));
+  r.k = a.integer32(1), r.score = a.integer32(2), r.groups = a.integer32(4), r.top_groups = a.integer32(5), r.group_best = a.integer32(6);
+  r.renorm = a.integer32(7), r.scale = a.real(8);
+  Args o{outs, 2, a.dev};
+  r.weights = static_cast<float*>(o.full(0, at::kFloat, {s[0], r.k}));
+  r.ids = static_cast<int32_t*>(o.full(1, at::kInt, {s[0], r.k}));
+  if (!a.ok || !o.ok) Py_RETURN_NONE;
+  return finish(a, tq_route, r, argv[9]);
+}
+
+struct Lists {
+  const int32_t* ids;
+  int64_t pairs;
+  int32_t experts;
+  int32_t *order, *offsets;
+};
+int call_lists(const Lists* l, void* stream) { return tq_expert_lists(l->ids, l->pairs, l->experts, l->order, l->offsets, stream); }
+
+// experts, n, out
+PyObject* expert_lists(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  Args a{argv, n};
+  const at::Tensor* t = n == 3 ? a.tensor(0) : nullptr;
+  if (!t || !t->is_cuda() || t->scalar_type() != at::kInt || !t->is_contiguous()) Py_RETURN_NONE;
+  a.dev = t->device();
+  PyObject* outs[2];
+  if (!pair(a, 2, &outs[0], &outs[1])) Py_RETURN_NONE;
+  Lists l{static_cast<const int32_t*>(t->data_ptr()), t->numel(), a.integer32(1), nullptr, nullptr};
+  Args o{outs, 2, a.dev};
+  l.order = static_cast<int32_t*>(o.full(0, at::kInt, {l.pairs}));
+  l.offsets = static_cast<int32_t*>(o.full(1, at::kInt, {(int64_t)l.experts + 1}));
+  if (!a.ok || !o.ok) Py_RETURN_NONE;
+  return finish(a, call_lists, l, argv[2]);
+}
+
+// fmt, w, rows, cols, q, d, order, offsets, out, bad_flag
+PyObject* gemm_experts(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  Args a{argv, n};
+  const at::Tensor* w = n == 10 ? a.tensor(1) : nullptr;
+  if (!w || !w->is_cuda() || w->scalar_type() != at::kByte || w->dim() != 2 || !w->is_contiguous()) Py_RETURN_NONE;
+  a.dev = w->device();
+  tq_gemm_experts_args r{};
+  r.fmt = a.integer32(0), r.rows = a.integer(2), r.cols = a.integer(3);
+  const at::Tensor *q = a.tensor(4), *order = a.tensor(6);
+  if (!a.ok || q->dim() != 2 || order->dim() != 1 || w->size(0) > INT32_MAX - 1) Py_RETURN_NONE;
+  const int64_t bytes = tq_repacked_bytes(r.fmt, r.rows, r.cols);
+  if (bytes <= 0 || w->size(1) != bytes) Py_RETURN_NONE;
+  r.experts = (int32_t)w->size(0), r.inputs = q->size(0), r.pairs = order->size(0);
+  r.w = w->data_ptr();
+  r.q = static_cast<const int8_t*>(a.full(4, at::kChar, {r.inputs, r.cols}));
+  r.d = static_cast<const float*>(a.full(5, at::kFloat, {r.inputs, r.cols / 256}));
+  r.order = static_cast<const int32_t*>(a.full(6, at::kInt, {r.pairs}));
+  r.offsets = static_cast<const int32_t*>(a.full(7, at::kInt, {(int64_t)r.experts + 1}));
+  r.y = static_cast<float*>(a.full(8, at::kFloat, {r.pairs, r.rows}));
+  r.bad_flag = static_cast<int32_t*>(a.some(9, at::kInt, {1}));
+  if (!a.ok) Py_RETURN_NONE;
+  return finish(a, tq_gemm_experts, r, argv[8]);
+}
+
+// y, x, a, b, index, ranks, scale, out, ws, bad_flag
+PyObject* adapter_add(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  Args a{argv, n};
+  if (n != 10 || !leader(a, 0)) Py_RETURN_NONE;
+  tq_adapter_add_args r{};
+  at::IntArrayRef ys, xs, os;
+  int out_type = -1;
+  r.y = matrix(a, 0, &ys, &r.y_stride, &r.y_type);
+  if (a.ok) r.x = matrix(a, 1, &xs, &r.x_stride, &r.x_type);
+  if (a.ok) r.out = const_cast<void*>(matrix(a, 7, &os, &r.out_stride, &out_type));
+  const at::Tensor* w = a.ok ? a.tensor(2) : nullptr;
+  if (!w || w->dim() != 3 || os != ys || out_type != r.y_type || xs[0] != ys[0] || xs[1] != w->size(2) || (r.out_stride == 0 && ys[0] > 1)) Py_RETURN_NONE;
+  const auto type = w->scalar_type();
+  r.w_type = type_code(type);
+  r.tokens = ys[0], r.rows = ys[1], r.cols = xs[1], r.adapters = dim32(w->size(0)), r.rank = dim32(w->size(1));
+  r.a = a.full(2, type, {w->size(0), w->size(1), w->size(2)});
+  r.b = a.full(3, type, {w->size(0), r.rows, w->size(1)});
+  r.index = static_cast<const int32_t*>(a.full(4, at::kInt, {r.tokens}));
+  r.ranks = static_cast<const int32_t*>(a.some(5, at::kInt, {w->size(0)}));
+  r.scale = static_cast<const float*>(a.some(6, at::kFloat, {w->size(0)}));
+  r.workspace = a.workspace(8, tq_adapter_workspace_bytes(r.tokens, r.adapters, r.rank, r.cols), &r.workspace_bytes);
+  r.bad_flag = static_cast<int32_t*>(a.some(9, at::kInt, {1}));
+  if (!a.ok || r.w_type <= TQ_F32) Py_RETURN_NONE;
+  return finish(a, tq_adapter_add, r, argv[7]);
+}
+
+// logits, u, temperature, top_k, top_p, min_p, out, logprob, ws
+PyObject* sample(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  Args a{argv, n};
+  if (n != 9 || !leader(a, 0)) Py_RETURN_NONE;
+  tq_sample_args r{};
+  at::IntArrayRef s;
+  r.logits = matrix(a, 0, &s, &r.logit_stride, &r.in_type);
+  if (!a.ok) Py_RETURN_NONE;
+  r.rows = s[0], r.vocab = s[1];
+  const int64_t one[1] = {s[0]};
+  r.u = static_cast<const float*>(a.full(1, at::kFloat, one));
+  r.temperature = static_cast<const float*>(a.some(2, at::kFloat, one));
+  r.top_k = static_cast<const int32_t*>(a.some(3, at::kInt, one));
+  r.top_p = static_cast<const float*>(a.some(4, at::kFloat, one));
+  r.min_p = static_cast<const float*>(a.some(5, at::kFloat, one));
+  r.tokens = static_cast<int32_t*>(a.full(6, at::kInt, one));
+  r.logprob = static_cast<float*>(a.some(7, at::kFloat, one));
+  r.workspace = a.workspace(8, tq_sample_workspace_bytes(r.rows, r.vocab), &r.workspace_bytes);
+  if (!a.ok) Py_RETURN_NONE;
+  return finish(a, tq_sample, r, argv[6]);
+}
+
 // A C++ exception must not pass through the interpreter.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* argv, Py_ssize_t n) {
@@ -247,6 +382,11 @@ constexpr PyCFunction method() {
 PyMethodDef g_methods[] = {{"rope_append", method<rope_append>(), METH_FASTCALL, nullptr},
                            {"paged_attn", method<paged_attn>(), METH_FASTCALL, nullptr},
                            {"gdn", method<gdn>(), METH_FASTCALL, nullptr},
+                           {"route", method<route>(), METH_FASTCALL, nullptr},
+                           {"expert_lists", method<expert_lists>(), METH_FASTCALL, nullptr},
+                           {"gemm_experts", method<gemm_experts>(), METH_FASTCALL, nullptr},
+                           {"adapter_add", method<adapter_add>(), METH_FASTCALL, nullptr},
+                           {"sample", method<sample>(), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};
 

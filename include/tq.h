@@ -375,6 +375,142 @@ typedef struct {
 int64_t tq_gdn_workspace_bytes(int64_t tokens, int64_t seqs, int64_t max_len, int32_t v_heads, int32_t dk, int32_t dv);
 int tq_gdn(const tq_gdn_args *args, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What differs from row to row in a batch that shares its weights: each
+ * token's experts (tq_route, tq_expert_lists, tq_gemm_experts), each request's
+ * low-rank adapter (tq_adapter_add) and each request's sampling (tq_sample).
+ * Conventions as above: values of index tensors are checked where they are
+ * read, tokens (pairs, rows) may be zero, nullable fields say so.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { TQ_SOFTMAX = 0, TQ_SIGMOID = 1 } tq_score;
+
+/* Choice of k experts for each token.
+ *   s = softmax(x) or 1 / (1 + exp(-x)) over the token's logits x
+ *   c = s + bias             (bias chooses and does not weigh; nullable)
+ *   groups > 1: the experts lie in `groups` groups of consecutive ones; a group
+ *     is worth the sum of its group_best (1 or 2) largest c, and the top_groups
+ *     groups worth most stay
+ *   of the experts that stay, the k of largest c are chosen, in that order
+ *   weight = scale s, or scale s / (sum of the chosen s) with renorm
+ * Equal ones: the lowest index first, for groups too.  An expert whose logit
+ * or c is -inf or NaN is absent: it counts as s = 0, c = -inf and is never
+ * chosen; where fewer than k are left the places behind them get id -1 and
+ * weight 0.  Of a softmax with logits of +inf these share equally.
+ * Scores, sums and comparisons are fp64, weights are rounded once.
+ * experts 1 to 1024; k 1 to 32, at most the experts that stay; groups divides
+ * experts, up to 64. */
+typedef struct {
+  const void *logits; /* [tokens][experts], in_type, rows logit_stride elements apart */
+  const float *bias;  /* [experts], nullable */
+  float *weights;     /* [tokens][k] contiguous */
+  int32_t *ids;       /* [tokens][k] contiguous */
+  int64_t logit_stride, tokens;
+  int32_t experts, k, groups, top_groups, group_best, score, renorm, in_type;
+  float scale;
+} tq_route_args;
+
+int tq_route(const tq_route_args *args, void *stream);
+
+/* The pairs (token, place) of a choice sorted by expert.  ids int32 [pairs];
+ * order int32 [pairs]: pair numbers by expert, those of one expert in their own
+ * order; offsets int32 [experts + 1]: expert e has order[offsets[e]] ..
+ * order[offsets[e + 1] - 1].  Pairs whose id is not in [0, experts) come last,
+ * from offsets[experts] on.  experts 1 to 65536, pairs up to 2^25.  Adapters
+ * and their tokens are sorted the same way. */
+int tq_expert_lists(const int32_t *ids, int64_t pairs, int32_t experts, int32_t *order, int32_t *offsets, void *stream);
+
+/* Ternary products whose matrix is chosen per pair: y[p] = W_e x[p / (pairs /
+ * inputs)] for every pair p of expert e (order and offsets as tq_expert_lists
+ * leaves them).  inputs == tokens shares a token's activations between its
+ * experts (gate, up); inputs == pairs gives every pair its own (down).  Each
+ * pair's row is bit-identical to tq_gemv without a workspace.  Pairs without an
+ * expert get zeros.  pq2_0 only (others TQ_ERR_UNSUPPORTED).  A number in
+ * `order` outside [0, pairs), or offsets that decrease or leave [0, pairs],
+ * are skipped or clamped, with bad_flag (their rows of y then hold anything);
+ * a pair that `order` names twice is written twice. */
+typedef struct {
+  const void *w;      /* [experts][tq_repacked_bytes(fmt, rows, cols)] */
+  const int8_t *q;    /* [inputs][cols], q8_K */
+  const float *d;     /* [inputs][cols / 256] */
+  const int32_t *order, *offsets;
+  float *y;           /* [pairs][rows] */
+  int32_t *bad_flag;  /* nullable */
+  int64_t rows, cols, pairs, inputs;
+  int32_t experts, fmt;
+} tq_gemm_experts_args;
+
+int tq_gemm_experts(const tq_gemm_experts_args *args, void *stream);
+
+/* Low-rank adapters beside a shared projection: out[t] = y[t] + scale_i B_i
+ * (A_i x[t]) with i = index[t]; index[t] < 0: out[t] = y[t] (and with bad_flag
+ * for index[t] >= adapters).  Adapter i uses the first ranks[i] rows of A_i and
+ * columns of B_i (ranks NULL: all; clamped to [0, rank]); what lies behind them
+ * is not used, whatever it holds.  scale NULL: 1.  out may be y itself (same
+ * stride), and may not overlap it otherwise.
+ * x_type fp32 or w_type; w_type bf16 or fp16; out has y's type.  Products are
+ * exact to 24 bits of both factors, sums and A x fp32, one rounding at the end.
+ * cols and rank multiples of 8 (rank up to 256); x, a and b 16-byte aligned and
+ * x_stride a multiple of 16 bytes; rows, y_stride and out_stride are free.
+ * workspace: tq_adapter_workspace_bytes, needs no clearing; not nullable. */
+typedef struct {
+  const void *x;        /* [tokens][cols], x_type, rows x_stride elements apart */
+  const void *y;        /* [tokens][rows], y_type */
+  const void *a;        /* [adapters][rank][cols], w_type */
+  const void *b;        /* [adapters][rows][rank], w_type */
+  void *out;            /* [tokens][rows], y_type */
+  const int32_t *index; /* [tokens] */
+  const int32_t *ranks; /* [adapters], nullable */
+  const float *scale;   /* [adapters], nullable */
+  void *workspace;
+  int32_t *bad_flag;    /* nullable */
+  int64_t x_stride, y_stride, out_stride, tokens, cols, rows, workspace_bytes;
+  int32_t adapters, rank, x_type, w_type, y_type;
+} tq_adapter_add_args;
+
+/* Bytes for these sizes, 0 for sizes that tq_adapter_add refuses. */
+int64_t tq_adapter_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank, int64_t cols);
+int tq_adapter_add(const tq_adapter_add_args *args, void *stream);
+
+/* One token for each row of logits x, from a given random number u:
+ *   z_i = (x_i - max x) / temperature, e_i = exp z_i
+ *   order: x descending, equal ones by index
+ *   top_k > 0: the first top_k of the order stay
+ *   top_p < 1: of these, the shortest beginning whose sum of e is at least
+ *     top_p times the sum of all of these stays (always the first one)
+ *   min_p > 0: of these, those with e_i >= min_p stay
+ *   token = the first index i that stays and whose running sum of e over the
+ *     indices that stay exceeds u times their whole sum
+ * temperature 0 (or less, or NaN): the index of the largest logit, the lowest
+ * of equal ones.  logprob = log(e_token / sum of all e_i), before any filter
+ * (temperature counts as 1 for greedy rows).  NaN parameters other than the
+ * temperature switch their filter off (u: 0); u outside [0, 1) takes the first
+ * or the last token that stays; top_p <= 0 keeps the first; min_p > 1 the
+ * largest logits.  NULL parameters: temperature 1, filters off.
+ * Logits of -inf and NaN are never drawn; a row without others gives token -1
+ * and logprob -inf.  Logits of +inf share equally.  e is fp64, rounded to a
+ * multiple of 2^-43 so that sums are whole numbers and do not depend on their
+ * order: tokens below 2^-44 of the largest weigh nothing.
+ * workspace: tq_sample_workspace_bytes, zeroed before its first use and left
+ * ready by every call; calls that overlap need workspaces of their own.  Not
+ * nullable.  vocab 1 to 2^20. */
+typedef struct {
+  const void *logits;       /* [rows][vocab], in_type, rows logit_stride elements apart */
+  const float *u;           /* [rows] */
+  const float *temperature; /* [rows], nullable */
+  const int32_t *top_k;     /* [rows], nullable */
+  const float *top_p, *min_p; /* [rows], nullable */
+  int32_t *tokens;          /* [rows] */
+  float *logprob;           /* [rows], nullable */
+  void *workspace;
+  int64_t logit_stride, rows, vocab, workspace_bytes;
+  int32_t in_type;
+} tq_sample_args;
+
+/* Bytes for these sizes, 0 for sizes that tq_sample refuses. */
+int64_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab);
+int tq_sample(const tq_sample_args *args, void *stream);
+
 /* Static description of a status code. */
 const char *tq_status_str(int status);
 
