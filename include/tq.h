@@ -393,7 +393,8 @@ typedef enum { TQ_SOFTMAX = 0, TQ_SIGMOID = 1 } tq_score;
  *     groups worth most stay
  *   of the experts that stay, the k of largest c are chosen, in that order
  *   weight = scale s, or scale s / (sum of the chosen s) with renorm
- * Equal ones: the lowest index first, for groups too.  An expert whose logit
+ * Equal ones: the lowest index first, for groups too; without a bias and
+ * without sums of two the logits are compared, whose order is that of c.  An expert whose logit
  * or c is -inf or NaN is absent: it counts as s = 0, c = -inf and is never
  * chosen; where fewer than k are left the places behind them get id -1 and
  * weight 0.  Of a softmax with logits of +inf these share equally.
