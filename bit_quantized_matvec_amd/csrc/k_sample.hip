@@ -3,30 +3,46 @@
 //
 // The filters each keep a beginning of one order (logits descending, equal
 // ones by index), so what stays after top-k and top-p is "keys above K, and
-// the first j of those equal to K", found without sorting: a radix descent
-// over the 32-bit keys of the logits (11 + 11 + 10 bits), counting tokens and
-// adding up their weights per digit, stops at the digit where the count (or
-// the weight) is reached.  min_p is a test of each token by itself.
+// the first j of those equal to K", found without sorting.  min_p is a test of
+// each token by itself.
 //
-// A weight is exp(z) in fp64, rounded to a multiple of 2^-43, as a whole
-// number: sums are exact and the same in any order, so atomics in LDS change
-// nothing, and 2^20 tokens of weight 1 still fit 64 bits.  fp32 would draw
+// A weight is exp(z) in fp64; within a slice of a row it is a whole number of
+// 2^-43 of the slice's largest, so that the sums of LDS atomics do not depend
+// on their order; slices are added up as fp64 in one order.  fp32 would draw
 // another token wherever u falls within some 2^-20 of a border.
 //
-// One workgroup per row; the row is read once for its maximum, once per digit
-// and search, and for the draw (a sum per wave's share of the row, the same
-// over the share that holds the drawn place, then 64 tokens at a time).
+// Two launches, a workgroup per slice of a row in both:
+//   bins_kernel: the slice, held in registers, gives its largest logit and a
+//     histogram (tokens, weight) over bins of 1/8 in z, 32 down from it.  Bins
+//     are floor(8 x / T), the same numbers in every slice, so the histograms
+//     of a row add up.  The row's last workgroup does that, and names the bins
+//     in which the cuts of top-k, top-p and min-p lie.  Tokens further down
+//     than 32 weigh less than 2^-44 of the largest: nothing.
+//   pick_kernel: the tokens of those bins go to a list.  The row's last
+//     workgroup finds K and j in it (by 1024 digits of the keys' range at a
+//     time), adds up what stays per slice, and draws: the slice, then the token
+//     in it.
+// Where the list is too short for the bins (a flat row), the last workgroup
+// searches the whole row instead (search_row: a radix descent over the keys).
+//
+// Rows that need no search (greedy ones) end with the first launch.
 #include <algorithm>
 
 #include "batch.h"
+#include "kernels.h"
 #include "seq.h"
 
 namespace tq {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 2048;
+constexpr int kMaxWaves = 16;
+constexpr int kPer = 16;     // logits of a thread
+constexpr int kBins = 256;   // of 1 / kPerUnit
+constexpr int kPerUnit = 8;
+constexpr int kMost = 1 << 14;  // places of a row's list
+constexpr int kMaxSlices = 65;
+constexpr int kNear = 1024;  // places of the list that are kept in LDS
+constexpr int kDigits = 1024;
 constexpr uint64_t kOne = uint64_t(1) << 43;  // the weight of the largest logit
 
 __device__ inline uint32_t key_of(float x) {  // 0: never drawn
@@ -36,17 +52,44 @@ __device__ inline uint32_t key_of(float x) {  // 0: never drawn
 }
 __device__ inline float value_of(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
 
+// exp(z) for z in [-50, 0]: z = (64 k + j) ln2 / 64 + r, |r| <= ln2 / 128, exp(z) = 2^k 2^(j/64) exp(r), the last by its series
+// to r^6 / 720 < 2^-54.  k ln2 / 64 is taken off in two parts, the first of 24 bits, so that its product is exact.
+constexpr int kRoots = 64;
+__device__ inline void fill_roots(double* roots) {
+  if (threadIdx.x < kRoots) roots[threadIdx.x] = exp2((double)threadIdx.x / kRoots);
+}
+__device__ inline double exp_of(double z, const double* roots) {
+  constexpr double kStep = 0.6931471805599453094 / kRoots, kHigh = (double)(float)kStep;
+  constexpr double kLow = (kStep - kHigh) + 2.3190468138462996e-17 / kRoots;  // (the double nearest ln2 is that much short)
+  const double n = __builtin_rint(z * (1.0 / kStep));
+  const double r = __builtin_fma(n, -kLow, __builtin_fma(n, -kHigh, z));
+  double p = __builtin_fma(r, 1.0 / 120, 1.0 / 24);
+  p = __builtin_fma(r, p, 1.0 / 6);
+  p = __builtin_fma(r, p, 0.5);
+  p = __builtin_fma(r, p, 1.0);
+  p = __builtin_fma(r, p, 1.0);
+  const int i = (int)n;
+  return __builtin_ldexp(roots[i & (kRoots - 1)] * p, i >> 6);
+}
+
 struct Scale {
   float most;
   double inv_t;
+  const double* roots;
   // z of a logit above -inf
   __device__ double z(float x) const { return x == most ? 0.0 : ((double)x - (double)most) * inv_t; }
   __device__ double e(float x) const {
     const double v = z(x);
-    return v > -50.0 ? exp(v) : 0.0;  // (also where +inf makes z no number)
+    return v > -50.0 ? exp_of(v, roots) : 0.0;  // (also where +inf makes z no number)
   }
-  __device__ uint64_t weight(float x) const { return (uint64_t)__builtin_rint(e(x) * (double)kOne); }
+  __device__ uint64_t weight(float x) const { return units(e(x)); }
+  // A number up to 1 as a whole number of 2^-43: the low bits of its sum with 2^52
+  __device__ static uint64_t units(double e) { return __builtin_bit_cast(uint64_t, __builtin_fma(e, (double)kOne, 0x1p52)) & ((uint64_t(1) << 52) - 1); }
 };
+
+// The bin of a logit: the same for every slice, increasing with x.  (Beyond kFar logits that are 7 apart in z share one.)
+constexpr double kFar = 1e9;
+__device__ inline int bin_of(float x, double per) { return (int)__builtin_floor(fmax(-kFar, fmin((double)x * per, kFar))); }
 
 __device__ inline uint64_t shfl_up64(uint64_t v, int d) {
   const uint32_t lo = __shfl_up((uint32_t)v, d, 64), hi = __shfl_up((uint32_t)(v >> 32), d, 64);
@@ -60,6 +103,14 @@ __device__ inline uint64_t wave_scan(uint64_t v, int lane) {
   }
   return v;
 }
+__device__ inline double wave_scan(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 __device__ inline uint64_t wave_total(uint64_t v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -69,270 +120,721 @@ __device__ inline uint64_t wave_total(uint64_t v) {
   return v;
 }
 
+// ---- the workspace ----
+
+struct Slice {  // a slice's largest logit and its first place
+  float most;
+  int at;
+};
+// What bins_kernel's last workgroup of a row leaves for pick_kernel.  Bins count down from that of the row's largest logit.
+struct Row {
+  float most;
+  int top_bin;
+  int search;       // 0: the token is there already
+  int k_bin;        // the cut of top-k lies in this bin (kBins: no top-k)
+  int p0, p1;       // that of top-p in one of these (p0 > p1: no top-p)
+  int m0, m1;       // tokens above m0 pass min_p, below m1 none (m0 = kBins: no min-p)
+  uint32_t k_count; // tokens above k_bin
+  double k_mass;    // weight above k_bin; without top-k of the row
+  double p_mass;    // weight above p0
+  double total;     // weight of the row
+};
+struct Layout {
+  int slices, threads;
+  int64_t per;  // logits of a slice
+  int64_t rows, parts, mass, count, list, bytes;
+};
+// The counters of a launch's rows lie in front, at the same places for every size, so that one workspace serves any call that it
+// is large enough for; a launch takes at most kRows rows.
+constexpr int64_t kRows = 4096;
+constexpr int64_t kCounterBytes = kRows * 16;
+Layout layout(int64_t rows, int64_t vocab) {
+  Layout l;
+  rows = std::min(rows, kRows);
+  // Slices of 4096 logits while they are few, of 16384 where there is work enough (or the slices are many).
+  l.threads = 256;
+  while (l.threads < 1024 && (rows * vocab / (l.threads * kPer) > 1024 || vocab + 7 > (int64_t)l.threads * kPer * kMaxSlices)) l.threads *= 2;
+  l.per = l.threads * kPer;
+  l.slices = (int)((vocab + 7 + l.per - 1) / l.per);  // (the first logit may be place 7)
+  const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  l.rows = kCounterBytes;
+  l.parts = l.rows + up(rows * (int64_t)sizeof(Row));
+  l.mass = l.parts + up(rows * l.slices * (int64_t)sizeof(Slice));
+  l.count = l.mass + up(rows * l.slices * kBins * 8);
+  l.list = l.count + up(rows * l.slices * kBins * 4);
+  l.bytes = l.list + up(rows * std::min<int64_t>(kMost, vocab) * 8);
+  return l;
+}
+struct Space {
+  unsigned* counters;  // [rows][4]: arrivals of both launches, places of the list; zero between calls
+  Row* rows;
+  unsigned long long* parts;  // [rows][slices] of Slice
+  unsigned long long* mass;   // [rows][slices][kBins], sums from the slice's first bin on
+  unsigned* count;            // [rows][slices][kBins], likewise
+  unsigned long long* list;   // [rows][most]: key, place
+  int slices, most;
+};
+
+// Data handed from one workgroup of a launch to another goes through agent-scope stores and loads; a workgroup's arrival is
+// counted once its stores are acknowledged (the order of the split products).
+template <typename T>
+__device__ inline void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ inline T get(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Whether this workgroup is the last of `n` (uniform); the counter is back at zero then.
+__device__ inline bool last_of(unsigned* counter, unsigned n, int* shared) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *shared = before == n - 1;
+    if (before == n - 1) put(counter, 0u);
+  }
+  __syncthreads();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  return *shared;
+}
+
+// Places of a row are counted from the 16-byte block that its first logit lies in, so that blocks of 16 bytes are read whole
+// whatever the row's alignment: logit i is place i + lead.
+template <typename T>
+__device__ inline int lead_of(const T* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
+}
+// kPer logits of a thread: groups of 16 bytes from logit `at` on, `stride` logits apart.  What lies outside [0, n) or is NaN is
+// -inf.
+template <typename T>
+__device__ inline void load_logits(const T* row, int64_t at, int64_t stride, int64_t n, float* x) {
+  constexpr int kV = 16 / sizeof(T);
+  typedef Vec<T, kV> V;
+#pragma unroll
+  for (int g = 0; g < kPer / kV; ++g, at += stride) {
+    if (at >= 0 && at + kV <= n) {
+      const V v = *reinterpret_cast<const V*>(row + at);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) x[kV * g + j] = (float)v.v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) x[kV * g + j] = at + j >= 0 && at + j < n ? (float)row[at + j] : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = x[i] == x[i] ? x[i] : -INFINITY;
+}
+// A slice's logits spread over the workgroup, neighbours in neighbouring threads; and the logit that x[i] is.
+template <typename T>
+__device__ inline int64_t load_slice(const T* row, int slice, int64_t n, float* x) {
+  constexpr int kV = 16 / sizeof(T);
+  const int64_t at = (int64_t)slice * blockDim.x * kPer + (int)threadIdx.x * kV - lead_of(row);
+  load_logits(row, at, (int64_t)blockDim.x * kV, n, x);
+  return at;
+}
+template <typename T>
+__device__ inline int64_t logit_of(int64_t at, int i) {
+  constexpr int kV = 16 / sizeof(T);
+  return at + (int64_t)(i / kV) * blockDim.x * kV + i % kV;
+}
+
+struct Request {
+  double inv_t, top_p, min_p;
+  double per;  // bins of a unit of x
+  int64_t top_k;
+  bool greedy, use_k, use_p, sums;
+};
+__device__ inline Request request(const tq_sample_args& a, int64_t r) {
+  Request q;
+  const float t = a.temperature ? a.temperature[r] : 1.0f;
+  q.greedy = !(t > 0.0f);
+  q.inv_t = q.greedy ? 1.0 : 1.0 / (double)t;
+  q.per = kPerUnit * q.inv_t;
+  q.top_k = a.top_k ? a.top_k[r] : 0;
+  q.top_p = a.top_p ? (double)a.top_p[r] : 1.0;
+  const double m = a.min_p && !q.greedy ? (double)a.min_p[r] : 0.0;
+  q.min_p = m > 0.0 ? fmin(m, 1.0) : 0.0;
+  q.use_k = !q.greedy && q.top_k > 0 && q.top_k < a.vocab;
+  q.use_p = !q.greedy && q.top_p < 1.0;
+  q.sums = !q.greedy || a.logprob;
+  return q;
+}
+
+__device__ inline void finish(const tq_sample_args& a, int64_t r, int token, double z, double total) {
+  a.tokens[r] = token;
+  if (a.logprob) a.logprob[r] = token < 0 ? -INFINITY : (float)(z - log(total));
+}
+
+// ---- the first launch ----
+
+struct BinsShared {
+  unsigned long long mass[kBins];
+  unsigned count[kBins];
+  float best[kMaxWaves];
+  int best_at[kMaxWaves];
+  unsigned long long sum[kBins / 64];
+  unsigned tokens[kBins / 64];
+  double roots[kRoots];
+  double cum_mass[kBins];
+  unsigned cum_count[kBins];
+  double scale[kMaxSlices];
+  int shift[kMaxSlices];
+  int flag;
+};
+
+// The largest of a workgroup's logits and its first place, in all threads.
+__device__ inline void block_best(float* best, int* at, float* lds_best, int* lds_at) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float ox = __shfl_xor(*best, o, 64);
+    const int oa = __shfl_xor(*at, o, 64);
+    if (ox > *best || (ox == *best && oa < *at)) *best = ox, *at = oa;
+  }
+  const int waves = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) lds_best[threadIdx.x >> 6] = *best, lds_at[threadIdx.x >> 6] = *at;
+  __syncthreads();
+  *best = lds_best[0], *at = lds_at[0];
+  for (int w = 1; w < waves; ++w)
+    if (lds_best[w] > *best || (lds_best[w] == *best && lds_at[w] < *at)) *best = lds_best[w], *at = lds_at[w];
+  __syncthreads();
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) {
+  __shared__ BinsShared sh;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int slice = blockIdx.x % ws.slices;
+  const int64_t r = blockIdx.x / ws.slices;
+  const Request q = request(a, r);
+  for (int b = tid; b < kBins; b += blockDim.x) sh.mass[b] = 0, sh.count[b] = 0;
+  fill_roots(sh.roots);
+
+  float x[kPer];
+  const int64_t at0 = load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
+  float best = -INFINITY;
+  int at = 0x7FFFFFFF;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (x[i] > best) best = x[i], at = (int)logit_of<T>(at0, i);
+  block_best(&best, &at, sh.best, sh.best_at);
+  if (q.sums && best > -INFINITY) {  // uniform
+    const Scale sc{best, q.inv_t, sh.roots};
+    const int top = bin_of(best, q.per);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (!(x[i] > -INFINITY)) continue;
+      const int b = top - bin_of(x[i], q.per);
+      if (b >= kBins) continue;
+      atomicAdd(&sh.mass[b], (unsigned long long)sc.weight(x[i]));
+      if (q.use_k) atomicAdd(&sh.count[b], 1u);
+    }
+  }
+  __syncthreads();
+  const int64_t part = r * ws.slices + slice;
+  if (q.sums) {  // sums from the first bin on: every sum that is asked for later is one number
+    uint64_t m = 0, c = 0;
+    if (tid < kBins) {
+      m = wave_scan((uint64_t)sh.mass[tid], lane);
+      if (q.use_k) c = wave_scan((uint64_t)sh.count[tid], lane);
+      if (lane == 63) sh.sum[tid >> 6] = m, sh.tokens[tid >> 6] = (unsigned)c;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+      for (int w = 0; w < tid >> 6; ++w) m += sh.sum[w], c += sh.tokens[w];
+      put(&ws.mass[part * kBins + tid], (unsigned long long)m);
+      if (q.use_k) put(&ws.count[part * kBins + tid], (unsigned)c);
+    }
+  }
+  if (tid == 0) put(&ws.parts[part], __builtin_bit_cast(unsigned long long, (Slice{best, at})));
+  if (!last_of(&ws.counters[4 * r], ws.slices, &sh.flag)) return;
+
+  // the row
+  best = -INFINITY, at = 0x7FFFFFFF;
+  Slice mine{-INFINITY, 0x7FFFFFFF};
+  if (tid < ws.slices) {
+    mine = __builtin_bit_cast(Slice, get(&ws.parts[r * ws.slices + tid]));
+    best = mine.most, at = mine.at;
+  }
+  block_best(&best, &at, sh.best, sh.best_at);
+  if (!(best > -INFINITY)) {  // nothing to draw from
+    if (tid == 0) {
+      finish(a, r, -1, 0.0, 1.0);
+      ws.rows[r].search = 0;
+    }
+    return;
+  }
+  const Scale sc{best, q.inv_t, sh.roots};
+  const int top = bin_of(best, q.per);
+  if (tid < ws.slices) {
+    const bool some = mine.most > -INFINITY;
+    sh.scale[tid] = some ? sc.e(mine.most) / (double)kOne : 0.0;
+    sh.shift[tid] = some ? min(top - bin_of(mine.most, q.per), kBins) : kBins;
+  }
+  __syncthreads();
+  if (tid < kBins) {
+    double m = 0;
+    unsigned c = 0;
+    if (q.sums) {
+#pragma unroll 8
+      for (int s = 0; s < ws.slices; ++s) {
+        const int b = tid - sh.shift[s];
+        const int64_t i = (r * ws.slices + s) * kBins + max(b, 0);
+        const double v = (double)get(&ws.mass[i]);
+        m = b >= 0 ? __builtin_fma(v, sh.scale[s], m) : m;
+        if (q.use_k) {
+          const unsigned n = get(&ws.count[i]);
+          c += b >= 0 ? n : 0;
+        }
+      }
+    }
+    sh.cum_mass[tid] = m, sh.cum_count[tid] = c;
+  }
+  __syncthreads();
+  if (tid >= 64) return;
+  // wave 0: first bins that reach a number
+  const auto first_bin = [&](auto reached) {
+    int f = kBins;
+    for (int i = kBins / 64 - 1; i >= 0; --i) {
+      const uint64_t ok = __ballot(reached(64 * i + lane));
+      if (ok) f = 64 * i + __builtin_ctzll(ok);
+    }
+    return f;
+  };
+  const double total = sh.cum_mass[kBins - 1];
+  if (q.greedy) {
+    if (lane == 0) {
+      finish(a, r, at, 0.0, total);
+      ws.rows[r].search = 0;
+    }
+    return;
+  }
+  Row row;
+  row.most = best, row.top_bin = top, row.search = 1, row.total = total;
+  row.k_bin = kBins, row.k_count = 0, row.k_mass = total;
+  row.p0 = 1, row.p1 = 0, row.p_mass = 0, row.m0 = row.m1 = kBins;
+  double hi = total;
+  if (q.use_k) {
+    row.k_bin = first_bin([&](int b) { return sh.cum_count[b] >= (uint64_t)q.top_k; });
+    if (row.k_bin < kBins) {  // (otherwise all that weigh anything stay)
+      row.k_count = row.k_bin ? sh.cum_count[row.k_bin - 1] : 0;
+      row.k_mass = row.k_bin ? sh.cum_mass[row.k_bin - 1] : 0.0;
+      hi = sh.cum_mass[row.k_bin];
+    }
+  }
+  if (q.use_p) {
+    // what stays after top-k weighs between k_mass and hi; sums of the parts in another order differ in the last bits
+    const double p = fmax(q.top_p, 0.0), g0 = p * row.k_mass * (1 - 1e-12), g1 = p * hi * (1 + 1e-12);
+    row.p0 = min(first_bin([&](int b) { return sh.cum_mass[b] >= g0; }), kBins - 1);
+    row.p1 = min(first_bin([&](int b) { return sh.cum_mass[b] >= g1; }), min(row.k_bin, kBins - 1));
+    row.p0 = min(row.p0, row.p1);
+    row.p_mass = row.p0 ? sh.cum_mass[row.p0 - 1] : 0.0;
+  }
+  if (q.min_p > 0.0) {
+    // z = log(min_p): bins of two logits differ from their difference's by one, and by one more for roundings
+    const int b = (int)fmin(-log(q.min_p) * kPerUnit, 1e6);
+    row.m0 = max(0, b - 2), row.m1 = b + 2;
+    if (fabs((double)best * q.per) >= kFar) row.m0 = 0, row.m1 = kBins;
+  }
+  if (lane == 0) ws.rows[r] = row;
+}
+
+// ---- the search of a whole row, by one workgroup ----
+
 // What stays: keys above `key`, and the first `ties` (by index) of those equal to it, if their e is at least min_p.
 struct Cut {
   uint32_t key;
   uint64_t ties;
-  uint64_t above;  // weight of the keys above
+  double sum;    // weight of what stays (as if every e were at least min_p)
 };
 
-struct Shared {
-  uint32_t count[kBins];
-  unsigned long long mass[kBins];
-  unsigned long long part[kWaves], part2[kWaves];
-  float best[kWaves];
-  int best_at[kWaves];
-  uint32_t digit;
-  uint32_t before_count;
-  unsigned long long before_mass, digit_mass;
-  uint32_t digit_count;
-  int pick;
-  unsigned long long pick_mass, pick_ties;
+struct PickShared {
+  unsigned long long mass[kDigits];
+  uint32_t count[kDigits];
+  unsigned long long part[kMaxWaves], part2[kMaxWaves];
+  uint32_t kmin;
+  int digit;
+  unsigned long long before_count, before_mass, digit_count, digit_mass;
+  unsigned long long slice_mass[kMaxSlices], slice_ties[kMaxSlices];
+  double slice_sum[kMaxSlices];
+  int flag, pick;
+  int token;
+  double run;
+  unsigned long long tied;
+  double roots[kRoots];
+  unsigned long long near[kNear];  // the first of the list
 };
 
-// The beginning of the order that has `tokens` tokens (by_count), or whose weight reaches `goal`.  The caller knows that the
-// row has that many, or that much.
-template <typename T>
-__device__ Cut find_cut(const T* row, int n, const Scale& sc, bool by_count, uint64_t tokens, double goal, Shared& sh) {
+// The beginning of the order, among the keys in [lo, hi] that `each` goes through, that reaches `tokens` tokens (by_count) or
+// the weight `goal` (a fraction of 1), `above` of it already there: by 1024 digits of the keys' range at a time.
+template <typename EACH>
+__device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bool by_count, uint64_t tokens, double goal, double above, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  uint32_t prefix = 0;
-  uint64_t above_count = 0, above_mass = 0;
-  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
-  uint32_t equal = 0;
-#pragma unroll 1
-  for (int level = 0; level < 3; ++level) {
-    const int shift = kShift[level], bins = 1 << kBits[level];
-    for (int b = tid; b < bins; b += kThreads) sh.count[b] = 0, sh.mass[b] = 0;
+  uint64_t before_count = 0, before_mass = 0, equal = 0;
+  while (true) {
+    int shift = 0;
+    while ((hi - lo) >> shift >= kDigits) ++shift;
+    for (int b = tid; b < kDigits; b += blockDim.x) sh.count[b] = 0, sh.mass[b] = 0;
+    if (tid == 0) sh.digit = -1;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = (float)row[i];
-      const uint32_t key = key_of(x);
-      if (key == 0 || (level > 0 && key >> (shift + kBits[level]) != prefix)) continue;
-      const uint32_t b = (key >> shift) & (bins - 1);
+    each([&](uint32_t key, int) {
+      if (key < lo || key > hi) return;
+      const uint32_t b = (key - lo) >> shift;
       atomicAdd(&sh.count[b], 1u);
-      atomicAdd(&sh.mass[b], (unsigned long long)sc.weight(x));
-    }
+      atomicAdd(&sh.mass[b], (unsigned long long)sc.weight(value_of(key)));
+    });
     __syncthreads();
-    // thread i has the digits bins - 1 - 2i and the one below it (one digit each on the last level)
-    const int per = bins / kThreads;
-    uint64_t c[2] = {0, 0}, m[2] = {0, 0};
+    // thread i has the digits from kDigits - 1 - per * i downwards
+    const int per = kDigits / (int)blockDim.x;
+    uint64_t c = 0, m = 0;
     for (int j = 0; j < per; ++j) {
-      const int b = bins - 1 - (per * tid + j);
-      c[j] = sh.count[b], m[j] = sh.mass[b];
+      const int b = kDigits - 1 - (per * tid + j);
+      c += sh.count[b], m += sh.mass[b];
     }
-    const uint64_t c_in = wave_scan(c[0] + c[1], lane), m_in = wave_scan(m[0] + m[1], lane);
+    const uint64_t c_in = wave_scan(c, lane), m_in = wave_scan(m, lane);
     if (lane == 63) sh.part[wave] = c_in, sh.part2[wave] = m_in;
-    if (tid == 0) sh.digit = 0xFFFFFFFFu;
     __syncthreads();
-    uint64_t cb = above_count + c_in - c[0] - c[1], mb = above_mass + m_in - m[0] - m[1];
+    uint64_t cb = before_count + c_in - c, mb = before_mass + m_in - m;
     for (int w = 0; w < wave; ++w) cb += sh.part[w], mb += sh.part2[w];
     for (int j = 0; j < per; ++j) {
-      const uint64_t ca = cb + c[j], ma = mb + m[j];
-      const bool was = by_count ? cb >= tokens : cb > 0 && (double)mb >= goal;
-      const bool is = by_count ? ca >= tokens : ca > 0 && (double)ma >= goal;
-      if (is && !was) {  // one digit of one thread
-        sh.digit = bins - 1 - (per * tid + j);
-        sh.before_count = (uint32_t)cb, sh.before_mass = mb, sh.digit_count = (uint32_t)c[j];
+      const int b = kDigits - 1 - (per * tid + j);
+      const uint64_t ca = cb + sh.count[b], ma = mb + sh.mass[b];
+      const auto reached = [&](uint64_t n, uint64_t v) { return by_count ? n >= tokens : n > 0 && above + (double)v / (double)kOne >= goal; };
+      if (reached(ca, ma) && !reached(cb, mb)) {  // one digit of one thread
+        sh.digit = b;
+        sh.before_count = cb, sh.before_mass = mb, sh.digit_count = sh.count[b], sh.digit_mass = sh.mass[b];
       }
       cb = ca, mb = ma;
     }
     __syncthreads();
-    if (sh.digit == 0xFFFFFFFFu) return {0, 0, 0};  // not reached: all of them (uniform)
-    prefix = prefix << kBits[level] | sh.digit;
-    above_count = sh.before_count, above_mass = sh.before_mass;
-    equal = sh.digit_count;
+    const int digit = sh.digit;
+    if (digit < 0) return {0, 0, 0};  // not reached: all of them stay (uniform)
+    before_count = sh.before_count, before_mass = sh.before_mass, equal = sh.digit_count;
+    const uint64_t digit_mass = sh.digit_mass;
     __syncthreads();
+    hi = (uint32_t)min((uint64_t)hi, lo + ((uint64_t)(digit + 1) << shift) - 1);
+    lo += (uint32_t)digit << shift;
+    // one token in the digit: all from its lowest key on stay
+    if (equal == 1) return {lo, 1, above + (double)(before_mass + digit_mass) / (double)kOne};
+    if (shift == 0) break;
   }
-  Cut cut{prefix, 1, above_mass};
+  const double sum = above + (double)before_mass / (double)kOne, w = (double)sc.weight(value_of(lo)) / (double)kOne;
+  uint64_t ties = 1;
   if (by_count) {
-    cut.ties = tokens - above_count;
+    ties = tokens - before_count;
   } else {
-    const uint64_t w = sc.weight(value_of(prefix));
-    const double need = goal - (double)above_mass;
-    if (w > 0 && need > 0) cut.ties = (uint64_t)fmax(1.0, __builtin_ceil(need / (double)w));
+    const double need = goal - sum;
+    if (w > 0 && need > 0) ties = (uint64_t)fmin(fmax(1.0, __builtin_ceil(need / w)), 1e9);
   }
-  cut.ties = min(cut.ties, (uint64_t)equal);
-  return cut;
+  ties = min(ties, equal);
+  return {lo, ties, sum + (double)ties * w};
 }
 
-// Weight of the tokens above the cut and number of those equal to it, of [first, last), by one wave.
-template <typename T>
-__device__ void share_sums(const T* row, int first, int last, const Scale& sc, const Cut& cut, double min_p, uint64_t* mass, uint64_t* ties) {
-  const int lane = threadIdx.x & 63;
-  uint64_t m = 0, t = 0;
-  for (int i = first + lane; i < last; i += 64) {
-    const float x = (float)row[i];
-    const uint32_t key = key_of(x);
-    if (key == 0 || key < cut.key) continue;
-    const double e = sc.e(x);
-    if (!(e >= min_p)) continue;
-    if (key == cut.key)
-      ++t;
-    else
-      m += (uint64_t)__builtin_rint(e * (double)kOne);
+// Whether a logit stays; ties are for the caller to count.
+struct Kept {
+  Scale sc;
+  Cut cut;
+  double min_p;
+  // 0: goes, 1: stays, 2: equal to the cut's key
+  __device__ int test(uint32_t key, float x, double* e) const {
+    if (key == 0 || key < cut.key) return 0;
+    *e = sc.e(x);
+    if (!(*e >= min_p)) return 0;
+    return key == cut.key ? 2 : 1;
   }
-  *mass = wave_total(m), *ties = wave_total(t);
-}
+};
 
+// The token of [first, last) at which the running weight passes `goal` (in units of 2^-43 of the row's largest), `ties` of the
+// equal ones still to come; the last one that weighs anything where it never does.  One workgroup, at most kPer logits a thread.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_kernel(tq_sample_args a) {
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t r = blockIdx.x;
-  const T* row = static_cast<const T*>(a.logits) + r * a.logit_stride;
-  const int n = (int)a.vocab;
-
-  // largest logit and its first place
-  float best = -INFINITY;
-  int at = 0x7FFFFFFF;
-  for (int i = tid; i < n; i += kThreads) {
-    const float x = (float)row[i];
-    if (x > best) best = x, at = i;
-  }
+__device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, uint64_t ties, double goal, PickShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t at0 = first + (int64_t)tid * kPer;
+  float x[kPer];
+  load_logits(row, at0, 16 / sizeof(T), last, x);
+  uint64_t w[kPer], sum = 0, equal = 0;
+  unsigned tied = 0;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float ox = __shfl_xor(best, o, 64);
-    const int oa = __shfl_xor(at, o, 64);
-    if (ox > best || (ox == best && oa < at)) best = ox, at = oa;
+  for (int i = 0; i < kPer; ++i) {
+    double e = 0;
+    const int t = k.test(key_of(x[i]), x[i], &e);
+    w[i] = t ? Scale::units(e) : 0;
+    if (t == 2) tied |= 1u << i, ++equal;
   }
-  if (lane == 0) sh.best[wave] = best, sh.best_at[wave] = at;
+  const uint64_t eq_in = wave_scan(equal, lane);
+  if (lane == 63) sh.part[wave] = eq_in;
   __syncthreads();
-  best = sh.best[0], at = sh.best_at[0];
-  for (int w = 1; w < kWaves; ++w)
-    if (sh.best[w] > best || (sh.best[w] == best && sh.best_at[w] < at)) best = sh.best[w], at = sh.best_at[w];
+  uint64_t before = eq_in - equal;
+  for (int v = 0; v < wave; ++v) before += sh.part[v];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (tied >> i & 1) {
+      if (before >= ties) w[i] = 0;
+      ++before;
+    }
+    sum += w[i];
+  }
   __syncthreads();
-  if (!(best > -INFINITY)) {  // nothing to draw from
-    if (tid == 0) {
-      a.tokens[r] = -1;
-      if (a.logprob) a.logprob[r] = -INFINITY;
+  const uint64_t in = wave_scan(sum, lane);
+  if (lane == 63) sh.part[wave] = in;
+  if (tid == 0) sh.token = -1, sh.pick = 0x7FFFFFFF;
+  __syncthreads();
+  uint64_t run = in - sum;
+  for (int v = 0; v < wave; ++v) run += sh.part[v];
+  int found = 0x7FFFFFFF, final = -1;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    run += w[i];
+    if (w[i]) {
+      final = (int)(at0 - first) + i;
+      if ((double)run > goal) found = min(found, final);
     }
-    return;
   }
+  atomicMin(&sh.pick, found);
+  atomicMax(&sh.token, final);
+  __syncthreads();
+  const int p = sh.pick != 0x7FFFFFFF ? sh.pick : sh.token;
+  __syncthreads();
+  return p < 0 ? -1 : (int)first + p;
+}
 
-  const float temperature = a.temperature ? a.temperature[r] : 1.0f;
-  const bool greedy = !(temperature > 0.0f);
-  const Scale sc{best, greedy ? 1.0 : 1.0 / (double)temperature};
-  uint64_t all = 0;  // weight of the whole row
-  const int64_t top_k = a.top_k ? a.top_k[r] : 0;
-  const double top_p = a.top_p ? (double)a.top_p[r] : 1.0;
-  const bool use_k = !greedy && top_k > 0 && top_k < n, use_p = !greedy && top_p < 1.0;
-  if (a.logprob || (use_p && !use_k)) {
-    uint64_t m = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = (float)row[i];
-      if (x > -INFINITY) m += sc.weight(x);
+// The goal of a draw from what weighs `sum`.
+__device__ inline double goal_of(float u, double sum) { return !(u > 0.0f) ? 0.0 : u >= 1.0f ? INFINITY : (double)u * sum; }
+
+// Per slice: the weight of what stays (units of 2^-43 of the row's largest) and the number equal to the cut's key.
+template <typename T>
+__device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q, const Scale& sc, int slices, Kept* kept, PickShared& sh) {
+  const T* row = static_cast<const T*>(a.logits) + r * a.logit_stride;
+  const int n = (int)a.vocab, per = (int)blockDim.x * kPer, lead = lead_of(row);
+  const auto each = [&](auto f) {
+    for (int s = 0; s < slices; ++s) {
+      float x[kPer];
+      const int64_t at = load_slice(row, s, n, x);
+#pragma unroll 1
+      for (int i = 0; i < kPer; ++i)
+        if (const uint32_t key = key_of(x[i])) f(key, (int)logit_of<T>(at, i));
     }
-    m = wave_total(m);
-    if (lane == 0) sh.part[wave] = m;
-    __syncthreads();
-    for (int w = 0; w < kWaves; ++w) all += sh.part[w];
-    __syncthreads();
+  };
+  Cut cut{0, 0, 0};
+  const uint32_t top = key_of(sc.most);
+  double stays = -1;
+  if (q.use_k) {
+    cut = find_cut(each, 1u, top, sc, true, (uint64_t)q.top_k, 0.0, 0.0, sh);
+    if (cut.key) stays = cut.sum;
   }
+  if (q.use_p) {
+    if (stays < 0) {
+      uint64_t m = 0;
+      each([&](uint32_t key, int) { m += sc.weight(value_of(key)); });
+      m = wave_total(m);
+      if ((threadIdx.x & 63) == 0) sh.part[threadIdx.x >> 6] = m;
+      __syncthreads();
+      m = 0;
+      for (int w = 0; w < (int)(blockDim.x >> 6); ++w) m += sh.part[w];
+      __syncthreads();
+      stays = (double)m / (double)kOne;
+    }
+    cut = find_cut(each, 1u, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, 0.0, sh);
+  }
+  *kept = Kept{sc, cut, q.min_p};
+  each([&](uint32_t key, int at) {
+    double e = 0;
+    const int t = kept->test(key, value_of(key), &e);
+    if (t == 1) atomicAdd(&sh.slice_mass[(at + lead) / per], (unsigned long long)Scale::units(e));
+    if (t == 2) atomicAdd(&sh.slice_ties[(at + lead) / per], 1ull);
+  });
+  __syncthreads();
+}
 
-  int token = at;
-  if (!greedy) {
-    double min_p = a.min_p ? (double)a.min_p[r] : 0.0;
-    min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
-    Cut cut{0, 0, 0};
-    uint64_t kept = all;
+// ---- the second launch ----
+
+template <typename T>
+__global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) {
+  __shared__ PickShared sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int slice = blockIdx.x % ws.slices;
+  const int64_t r = blockIdx.x / ws.slices;
+  const Row row = ws.rows[r];
+  if (!row.search) return;  // uniform over the row
+  const Request q = request(a, r);
+  fill_roots(sh.roots);
+  const Scale sc{row.most, q.inv_t, sh.roots};
+  const T* logits = static_cast<const T*>(a.logits) + r * a.logit_stride;
+  unsigned* places = &ws.counters[4 * r + 2];
+  const bool use_k = row.k_bin < kBins, use_p = row.p0 <= row.p1, use_m = row.m0 < kBins;
+  const auto listed = [&](int b) { return (use_k && b == row.k_bin) || (b >= row.p0 && b <= row.p1) || (b >= row.m0 && b <= row.m1); };
+
+  // this slice's tokens of the listed bins
+  if (use_k || use_p || use_m) {
+    float x[kPer];
+    const int64_t at0 = load_slice(logits, slice, a.vocab, x);
+    unsigned in = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (x[i] > -INFINITY && listed(row.top_bin - bin_of(x[i], q.per))) in |= 1u << i;
+    const unsigned n = __popc(in);
+    const unsigned upto = (unsigned)wave_scan((uint64_t)n, lane);
+    if (lane == 63) sh.part[wave] = upto;
+    __syncthreads();
+    unsigned before = upto - n, all = 0;
+    for (int w = 0; w < waves; ++w) {
+      if (w < wave) before += (unsigned)sh.part[w];
+      all += (unsigned)sh.part[w];
+    }
+    if (tid == 0) sh.pick = all ? (int)__hip_atomic_fetch_add(places, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    __syncthreads();
+    int64_t to = (int64_t)(unsigned)sh.pick + before;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (in >> i & 1) {
+        if (to < ws.most) put(&ws.list[r * ws.most + to], (unsigned long long)key_of(x[i]) << 32 | (unsigned)logit_of<T>(at0, i));
+        ++to;
+      }
+  }
+  if (!last_of(&ws.counters[4 * r + 1], ws.slices, &sh.flag)) return;
+
+  const unsigned n = get(places);
+  for (unsigned i = tid; i < min(n, (unsigned)kNear); i += blockDim.x) sh.near[i] = get(&ws.list[r * ws.most + i]);
+  const int per = (int)blockDim.x * kPer, lead = lead_of(logits);
+  for (int s = tid; s < ws.slices; s += blockDim.x) sh.slice_mass[s] = 0, sh.slice_ties[s] = 0;
+  __syncthreads();
+  if (tid == 0) put(places, 0u);
+  Kept kept{sc, {0, 0, 0}, q.min_p};
+  int sure = kBins;  // tokens of the bins above it stay, and are not in question
+  if (n > (unsigned)ws.most) {
+    search_row<T>(a, r, q, sc, ws.slices, &kept, sh);
+    sure = 0;
+  } else {
+    const unsigned long long* list = ws.list + r * ws.most;
+    // the listed tokens of the bins [b0, b1]
+    const auto each_of = [&](int b0, int b1) {
+      return [&, b0, b1](auto f) {
+        for (unsigned i = tid; i < n; i += blockDim.x) {
+          const unsigned long long v = i < kNear ? sh.near[i] : get(&list[i]);
+          const uint32_t key = (uint32_t)(v >> 32);
+          const int b = row.top_bin - bin_of(value_of(key), q.per);
+          if (b >= b0 && b <= b1) f(key, (int)(uint32_t)v);
+        }
+      };
+    };
+    const auto lowest = [&](int b0, int b1) {  // key
+      if (tid == 0) sh.kmin = 0xFFFFFFFFu;
+      __syncthreads();
+      each_of(b0, b1)([&](uint32_t key, int) { atomicMin(&sh.kmin, key); });
+      __syncthreads();
+      return sh.kmin;
+    };
+    const uint32_t top = key_of(sc.most);
+    int cut_bin = kBins;
+    double stays = row.k_mass;
     if (use_k) {
-      cut = find_cut(row, n, sc, true, (uint64_t)top_k, 0.0, sh);
-      if (use_p && cut.key == 0) {  // fewer tokens than top_k: all of them
-        uint64_t m = 0;
-        for (int i = tid; i < n; i += kThreads) {
-          const float x = (float)row[i];
-          if (x > -INFINITY) m += sc.weight(x);
-        }
-        m = wave_total(m);
-        if (lane == 0) sh.part[wave] = m;
-        __syncthreads();
-        kept = 0;
-        for (int w = 0; w < kWaves; ++w) kept += sh.part[w];
-        __syncthreads();
-      } else {
-        kept = cut.key ? cut.above + cut.ties * sc.weight(value_of(cut.key)) : 0;
-      }
+      kept.cut = find_cut(each_of(row.k_bin, row.k_bin), lowest(row.k_bin, row.k_bin), top, sc, true, (uint64_t)q.top_k - row.k_count, 0.0, row.k_mass, sh);
+      stays = kept.cut.sum;
+      cut_bin = row.k_bin;
     }
-    if (use_p) cut = find_cut(row, n, sc, false, 0, fmax(top_p, 0.0) * (double)kept, sh);
+    if (use_p) {
+      // the bins from p0 on are in the list up to p1, where the cut is reached
+      const uint32_t low = lowest(row.p0, row.p1);
+      kept.cut = find_cut(each_of(row.p0, row.p1), low, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, row.p_mass, sh);
+      if (kept.cut.key == 0) kept.cut = {low, uint64_t(1) << 32, 0};  // by roundings not reached: all of these
+      cut_bin = row.top_bin - bin_of(value_of(kept.cut.key), q.per);
+    }
+    sure = min(cut_bin, row.m0);
+    for (int s = tid; s < ws.slices && sure > 0; s += blockDim.x) {
+      const Slice part = __builtin_bit_cast(Slice, ws.parts[r * ws.slices + s]);
+      double m = 0;
+      if (part.most > -INFINITY) {
+        const int b = min(sure, kBins) - 1 - (row.top_bin - bin_of(part.most, q.per));
+        if (b >= 0) m = (double)ws.mass[(r * ws.slices + s) * kBins + b] * sc.e(part.most);
+      }
+      sh.slice_sum[s] = m;
+    }
+    // what is in question: the cut's bin, and those of min_p above it
+    each_of(sure, min(cut_bin, row.m1))([&](uint32_t key, int at) {
+      double e = 0;
+      const int t = kept.test(key, value_of(key), &e);
+      if (t == 1) atomicAdd(&sh.slice_mass[(at + lead) / per], (unsigned long long)Scale::units(e));
+      if (t == 2) atomicAdd(&sh.slice_ties[(at + lead) / per], 1ull);
+    });
+    __syncthreads();
+  }
 
-    // the draw: the share of the row that holds the place, its share, and the token
-    const uint64_t tie_weight = cut.key ? sc.weight(value_of(cut.key)) : 0;
-    int first = 0, last = n;
-    uint64_t before = 0, ties_left = cut.ties, goal = 0;
-    for (int level = 0; level < 2; ++level) {
-      const int share = ((last - first + kWaves - 1) / kWaves + 63) / 64 * 64;
-      const int lo = (int)min((int64_t)last, (int64_t)first + (int64_t)wave * share), hi = (int)min((int64_t)last, (int64_t)lo + share);
-      uint64_t m, t;
-      share_sums(row, lo, hi, sc, cut, min_p, &m, &t);
-      if (lane == 0) sh.part[wave] = m, sh.part2[wave] = t;
-      __syncthreads();
-      uint64_t left = ties_left, sum = before;
-      if (level == 0) {
-        for (int w = 0; w < kWaves; ++w) {
-          const uint64_t k = min(left, (uint64_t)sh.part2[w]);
-          sum += sh.part[w] + k * tie_weight;
-          left -= k;
-        }
-        const float u = a.u[r];
-        goal = !(u > 0.0f) ? 0 : u >= 1.0f ? sum - 1 : (uint64_t)((double)u * (double)sum);
-        goal = min(goal, sum - 1);
-        left = ties_left, sum = before;
-      }
-      int pick = 0;
-      for (int w = 0; w < kWaves; ++w) {
-        const uint64_t k = min(left, (uint64_t)sh.part2[w]);
-        const uint64_t after = sum + sh.part[w] + k * tie_weight;
-        pick = w;
-        if (after > goal) break;
-        sum = after, left -= k;
-      }
-      before = sum, ties_left = left;
-      const int nf = (int)min((int64_t)last, (int64_t)first + (int64_t)pick * share);
-      last = (int)min((int64_t)last, (int64_t)nf + share), first = nf;
-      __syncthreads();
+  // the draw: the slice, and the token in it.  Wave 0 has slices 2 lane and 2 lane + 1.
+  if (wave == 0) {
+    const double tie = kept.cut.key ? (double)sc.weight(value_of(kept.cut.key)) : 0.0;
+    uint64_t t[2] = {0, 0};
+    double m[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int s = 2 * lane + j;
+      if (s >= ws.slices) continue;
+      t[j] = sh.slice_ties[s];
+      m[j] = (sure > 0 ? sh.slice_sum[s] : 0.0) + (double)sh.slice_mass[s];
     }
-    if (wave == 0) {
-      for (int i = first; i < last; i += 64) {
-        const int p = i + lane;
-        const float x = p < last ? (float)row[p] : -INFINITY;
-        const uint32_t key = key_of(x);
-        const double e = key ? sc.e(x) : 0.0;
-        const bool stays = key != 0 && e >= min_p;
-        const uint64_t equal = __ballot(stays && key == cut.key && cut.key != 0);
-        const bool tie = equal >> lane & 1 && (uint64_t)__popcll(equal & ((uint64_t(1) << lane) - 1)) < ties_left;
-        uint64_t w = 0;
-        if (stays && (key > cut.key || tie)) w = (uint64_t)__builtin_rint(e * (double)kOne);
-        const uint64_t sum = before + wave_scan(w, lane);
-        const uint64_t over = __ballot(w > 0 && sum > goal);
-        if (over) {
-          token = i + __builtin_ctzll(over);
-          break;
-        }
-        before = (uint64_t)__builtin_amdgcn_readlane((int)sum, 63) & 0xFFFFFFFFu;
-        before |= (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(sum >> 32), 63) << 32;
-        ties_left -= min(ties_left, (uint64_t)__popcll(equal));
-      }
+    const uint64_t t_in = wave_scan(t[0] + t[1], lane);
+    uint64_t left[2];  // ties that are still to come where a slice begins
+    left[0] = kept.cut.ties - min(kept.cut.ties, t_in - t[0] - t[1]);
+    left[1] = left[0] - min(left[0], t[0]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) m[j] += (double)min(left[j], t[j]) * tie;
+    const double in = wave_scan(m[0] + m[1], lane);
+    const double goal = goal_of(a.u[r], __shfl(in, 63, 64));
+    // the first slice that weighs something and whose sum passes the goal, or the last that weighs something
+    const double begin[2] = {in - m[0] - m[1], in - m[1]};
+    const bool some[2] = {m[0] > 0, m[1] > 0}, over[2] = {some[0] && begin[1] > goal, some[1] && in > goal};
+    const uint64_t overs = __ballot(over[0] || over[1]), somes = __ballot(some[0] || some[1]);
+    const int who = overs ? __builtin_ctzll(overs) : somes ? 63 - __builtin_clzll(somes) : -1;
+    if (lane == max(who, 0)) {
+      const int j = overs ? !over[0] : some[1];
+      sh.pick = who < 0 ? -1 : 2 * lane + j;
+      sh.run = goal - begin[j], sh.tied = left[j];
     }
   }
-  if (tid == 0) {
-    a.tokens[r] = token;
-    if (a.logprob) a.logprob[r] = (float)(sc.z((float)row[token]) - log((double)all / (double)kOne));
+  __syncthreads();
+  const int pick = sh.pick;
+  const double goal = sh.run;
+  const uint64_t tied = sh.tied;
+  __syncthreads();
+  int token = -1;
+  if (pick >= 0)
+    token = draw(logits, (int64_t)pick * per - lead, min((int64_t)a.vocab, (int64_t)(pick + 1) * per - lead), kept, tied, goal, sh);
+  if (tid == 0) finish(a, r, token, token < 0 ? 0.0 : sc.z((float)logits[token]), row.total);
+}
+
+template <typename T>
+hipError_t launch_t(tq_sample_args a, hipStream_t s) {
+  const Layout l = layout(a.rows, a.vocab);
+  char* p = static_cast<char*>(a.workspace);
+  const Space ws{reinterpret_cast<unsigned*>(p), reinterpret_cast<Row*>(p + l.rows), reinterpret_cast<unsigned long long*>(p + l.parts),
+                 reinterpret_cast<unsigned long long*>(p + l.mass), reinterpret_cast<unsigned*>(p + l.count),
+                 reinterpret_cast<unsigned long long*>(p + l.list), l.slices, (int)std::min<int64_t>(kMost, a.vocab)};
+  const int64_t all = a.rows;
+  const auto from = [](auto*& q, int64_t n) {
+    if (q) q += n;
+  };
+  for (int64_t done = 0; done < all; done += kRows) {
+    a.rows = std::min(kRows, all - done);
+    const dim3 grid((unsigned)(a.rows * l.slices)), block(l.threads);
+    hipLaunchKernelGGL((bins_kernel<T>), grid, block, 0, s, a, ws);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((pick_kernel<T>), grid, block, 0, s, a, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.logits = static_cast<const T*>(a.logits) + kRows * a.logit_stride;
+    from(a.u, kRows), from(a.temperature, kRows), from(a.top_k, kRows), from(a.top_p, kRows), from(a.min_p, kRows), from(a.tokens, kRows);
+    from(a.logprob, kRows);
   }
+  return hipSuccess;
 }
 
 }  // namespace
 
-int64_t sample_workspace_bytes(int64_t rows, int64_t vocab) { return 16; }
+int64_t sample_workspace_bytes(int64_t rows, int64_t vocab) { return layout(rows, vocab).bytes; }
 
 hipError_t launch_sample(const tq_sample_args& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.rows), block(kThreads);
-  if (a.in_type == TQ_F32)
-    hipLaunchKernelGGL((sample_kernel<float>), grid, block, 0, s, a);
-  else if (a.in_type == TQ_BF16)
-    hipLaunchKernelGGL((sample_kernel<bf16>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((sample_kernel<f16>), grid, block, 0, s, a);
-  return hipGetLastError();
+  return a.in_type == TQ_F32 ? launch_t<float>(a, s) : a.in_type == TQ_BF16 ? launch_t<bf16>(a, s) : launch_t<f16>(a, s);
 }
 
 }  // namespace tq

@@ -489,9 +489,9 @@ int tq_adapter_add(const tq_adapter_add_args *args, void *stream);
  * or the last token that stays; top_p <= 0 keeps the first; min_p > 1 the
  * largest logits.  NULL parameters: temperature 1, filters off.
  * Logits of -inf and NaN are never drawn; a row without others gives token -1
- * and logprob -inf.  Logits of +inf share equally.  e is fp64, rounded to a
- * multiple of 2^-43 so that sums are whole numbers and do not depend on their
- * order: tokens below 2^-44 of the largest weigh nothing.
+ * and logprob -inf.  Logits of +inf share equally.  e is fp64; sums are good
+ * to some 2^-43 of the largest e and do not depend on timing; tokens below
+ * 2^-44 of the largest weigh nothing.
  * workspace: tq_sample_workspace_bytes, zeroed before its first use and left
  * ready by every call; calls that overlap need workspaces of their own.  Not
  * nullable.  vocab 1 to 2^20. */
