@@ -187,8 +187,8 @@ def sample_workspace_bytes(rows: int, vocab: int) -> int:
 
 
 def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
-    """A zeroed workspace for ``sample`` calls of these sizes; every call leaves it ready for the next."""
-    return torch.zeros(max(16, sample_workspace_bytes(rows, vocab)), dtype=torch.uint8, device=device)
+    """Scratch for ``sample`` calls of these sizes (needs no clearing)."""
+    return torch.empty(max(16, sample_workspace_bytes(rows, vocab)), dtype=torch.uint8, device=device)
 
 
 def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprob=None, ws=None) -> torch.Tensor:

@@ -11,37 +11,40 @@
 // on their order; slices are added up as fp64 in one order.  fp32 would draw
 // another token wherever u falls within some 2^-20 of a border.
 //
-// Two launches, a workgroup per slice of a row in both:
-//   bins_kernel: the slice, held in registers, gives its largest logit and a
-//     histogram (tokens, weight) over bins of 1/8 in z, 32 down from it.  Bins
-//     are floor(8 x / T), the same numbers in every slice, so the histograms
-//     of a row add up.  The row's last workgroup does that, and names the bins
-//     in which the cuts of top-k, top-p and min-p lie.  Tokens further down
-//     than 32 weigh less than 2^-44 of the largest: nothing.
-//   pick_kernel: the tokens of those bins go to a list.  The row's last
-//     workgroup finds K and j in it (by 1024 digits of the keys' range at a
-//     time), adds up what stays per slice, and draws: the slice, then the token
-//     in it.
-// Where the list is too short for the bins (a flat row), the last workgroup
-// searches the whole row instead (search_row: a radix descent over the keys).
+// Four launches:
+//   bins_kernel, a workgroup per slice of a row: the slice, held in registers,
+//     gives its largest logit and a histogram (tokens, weight) over bins of 1/8
+//     in z, 32 down from it.  Bins are floor(8 x / T), the same numbers in
+//     every slice, so the histograms of a row add up.
+//   plan_kernel, one per row: adds them, and names the bins in which the cuts
+//     of top-k, top-p and min-p lie.  Tokens further down than 32 weigh less
+//     than 2^-44 of the largest: nothing.  Greedy rows end here.
+//   list_kernel, one per slice: the tokens of those bins.
+//   pick_kernel, one per row: finds K and j among them (by 1024 digits of the
+//     keys' range at a time), adds up what stays per slice, and draws: the
+//     slice, then the token in it.
+// Where a slice has too many of them (a flat row), pick_kernel searches the
+// whole row instead (search_row: a radix descent over the keys).
 //
-// Rows that need no search (greedy ones) end with the first launch.
+// (Two launches, whose last workgroups of a row did the second and the fourth
+// kernel's work, cost one row as much and 256 rows twice: counting arrivals
+// across the XCDs takes some 15 ns a workgroup whatever the counter's place.)
 #include <algorithm>
 
 #include "batch.h"
-#include "kernels.h"
 #include "seq.h"
 
 namespace tq {
 namespace {
 
 constexpr int kMaxWaves = 16;
-constexpr int kPer = 16;     // logits of a thread
+constexpr int kPer = 16;     // logits of a thread of the slices' kernels
+constexpr int kPickThreads = 1024;
 constexpr int kBins = 256;   // of 1 / kPerUnit
 constexpr int kPerUnit = 8;
-constexpr int kMost = 1 << 14;  // places of a row's list
+constexpr int kShare = 1024;  // places of a slice in its row's list
 constexpr int kMaxSlices = 65;
-constexpr int kNear = 1024;  // places of the list that are kept in LDS
+constexpr int kNear = 4096;  // places of the list that are kept in LDS
 constexpr int kDigits = 1024;
 constexpr uint64_t kOne = uint64_t(1) << 43;  // the weight of the largest logit
 
@@ -80,7 +83,8 @@ struct Scale {
   __device__ double z(float x) const { return x == most ? 0.0 : ((double)x - (double)most) * inv_t; }
   __device__ double e(float x) const {
     const double v = z(x);
-    return v > -50.0 ? exp_of(v, roots) : 0.0;  // (also where +inf makes z no number)
+    const double e = exp_of(fmax(v, -50.0), roots);
+    return v > -50.0 ? e : 0.0;  // (also where +inf makes z no number)
   }
   __device__ uint64_t weight(float x) const { return units(e(x)); }
   // A number up to 1 as a whole number of 2^-43: the low bits of its sum with 2^52
@@ -91,34 +95,32 @@ struct Scale {
 constexpr double kFar = 1e9;
 __device__ inline int bin_of(float x, double per) { return (int)__builtin_floor(fmax(-kFar, fmin((double)x * per, kFar))); }
 
-__device__ inline uint64_t shfl_up64(uint64_t v, int d) {
-  const uint32_t lo = __shfl_up((uint32_t)v, d, 64), hi = __shfl_up((uint32_t)(v >> 32), d, 64);
-  return (uint64_t)hi << 32 | lo;
+// Sums over the lanes up to one's own, by DPP (a shuffle through LDS takes ten times as long): within rows of 16 lanes, then
+// the rows' last lanes to the rows behind them.
+template <int CTRL, int ROWS, typename V>
+__device__ inline V lane_moved(V v) {  // 0 where no lane moves in
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
 }
-__device__ inline uint64_t wave_scan(uint64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = shfl_up64(v, d);
-    if (lane >= d) v += o;
-  }
+template <typename V>  // uint64_t or double
+__device__ inline V wave_scan(V v) {
+  v += lane_moved<0x111, 0xF>(v);  // row_shr:1
+  v += lane_moved<0x112, 0xF>(v);
+  v += lane_moved<0x114, 0xF>(v);
+  v += lane_moved<0x118, 0xF>(v);
+  v += lane_moved<0x142, 0xA>(v);  // row_bcast:15, to rows 1 and 3
+  v += lane_moved<0x143, 0xC>(v);  // row_bcast:31, to rows 2 and 3
   return v;
 }
-__device__ inline double wave_scan(double v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
-  return v;
+template <typename V>
+__device__ inline V lane_value(V v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
 }
-__device__ inline uint64_t wave_total(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint32_t lo = __shfl_xor((uint32_t)v, o, 64), hi = __shfl_xor((uint32_t)(v >> 32), o, 64);
-    v += (uint64_t)hi << 32 | lo;
-  }
-  return v;
-}
+__device__ inline uint64_t wave_total(uint64_t v) { return lane_value(wave_scan(v), 63); }
 
 // ---- the workspace ----
 
@@ -126,7 +128,7 @@ struct Slice {  // a slice's largest logit and its first place
   float most;
   int at;
 };
-// What bins_kernel's last workgroup of a row leaves for pick_kernel.  Bins count down from that of the row's largest logit.
+// What plan_kernel leaves for the kernels behind it.  Bins count down from that of the row's largest logit.
 struct Row {
   float most;
   int top_bin;
@@ -142,63 +144,37 @@ struct Row {
 struct Layout {
   int slices, threads;
   int64_t per;  // logits of a slice
-  int64_t rows, parts, mass, count, list, bytes;
+  int64_t rows, parts, mass, count, shares, list, bytes;
 };
-// The counters of a launch's rows lie in front, at the same places for every size, so that one workspace serves any call that it
-// is large enough for; a launch takes at most kRows rows.
-constexpr int64_t kRows = 4096;
-constexpr int64_t kCounterBytes = kRows * 16;
+constexpr int64_t kRows = 1024;  // of one launch
 Layout layout(int64_t rows, int64_t vocab) {
   Layout l;
   rows = std::min(rows, kRows);
-  // Slices of 4096 logits while they are few, of 16384 where there is work enough (or the slices are many).
+  // Slices of 4096 logits, since one workgroup draws in one: 16384 take its compute unit 9 us instead of 2.  More in vocabularies
+  // of more than 64 slices, whose sums one wave adds.
   l.threads = 256;
-  while (l.threads < 1024 && (rows * vocab / (l.threads * kPer) > 1024 || vocab + 7 > (int64_t)l.threads * kPer * kMaxSlices)) l.threads *= 2;
+  while (vocab + 7 > (int64_t)l.threads * kPer * kMaxSlices) l.threads *= 2;
   l.per = l.threads * kPer;
   l.slices = (int)((vocab + 7 + l.per - 1) / l.per);  // (the first logit may be place 7)
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  l.rows = kCounterBytes;
+  l.rows = 0;
   l.parts = l.rows + up(rows * (int64_t)sizeof(Row));
   l.mass = l.parts + up(rows * l.slices * (int64_t)sizeof(Slice));
   l.count = l.mass + up(rows * l.slices * kBins * 8);
-  l.list = l.count + up(rows * l.slices * kBins * 4);
-  l.bytes = l.list + up(rows * std::min<int64_t>(kMost, vocab) * 8);
+  l.shares = l.count + up(rows * l.slices * kBins * 4);
+  l.list = l.shares + up(rows * l.slices * 4);
+  l.bytes = l.list + up(rows * l.slices * kShare * 4);
   return l;
 }
 struct Space {
-  unsigned* counters;  // [rows][4]: arrivals of both launches, places of the list; zero between calls
   Row* rows;
-  unsigned long long* parts;  // [rows][slices] of Slice
+  Slice* parts;               // [rows][slices]
   unsigned long long* mass;   // [rows][slices][kBins], sums from the slice's first bin on
   unsigned* count;            // [rows][slices][kBins], likewise
-  unsigned long long* list;   // [rows][most]: key, place
-  int slices, most;
+  uint32_t* list;             // [rows][slices][kShare]: keys
+  unsigned* shares;           // [rows][slices]: how many a slice has
+  int slices;
 };
-
-// Data handed from one workgroup of a launch to another goes through agent-scope stores and loads; a workgroup's arrival is
-// counted once its stores are acknowledged (the order of the split products).
-template <typename T>
-__device__ inline void put(T* p, T v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <typename T>
-__device__ inline T get(const T* p) {
-  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// Whether this workgroup is the last of `n` (uniform); the counter is back at zero then.
-__device__ inline bool last_of(unsigned* counter, unsigned n, int* shared) {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *shared = before == n - 1;
-    if (before == n - 1) put(counter, 0u);
-  }
-  __syncthreads();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-  return *shared;
-}
 
 // Places of a row are counted from the 16-byte block that its first logit lies in, so that blocks of 16 bytes are read whole
 // whatever the row's alignment: logit i is place i + lead.
@@ -208,12 +184,12 @@ __device__ inline int lead_of(const T* row) {
 }
 // kPer logits of a thread: groups of 16 bytes from logit `at` on, `stride` logits apart.  What lies outside [0, n) or is NaN is
 // -inf.
-template <typename T>
+template <typename T, int PER = kPer>
 __device__ inline void load_logits(const T* row, int64_t at, int64_t stride, int64_t n, float* x) {
   constexpr int kV = 16 / sizeof(T);
   typedef Vec<T, kV> V;
 #pragma unroll
-  for (int g = 0; g < kPer / kV; ++g, at += stride) {
+  for (int g = 0; g < PER / kV; ++g, at += stride) {
     if (at >= 0 && at + kV <= n) {
       const V v = *reinterpret_cast<const V*>(row + at);
 #pragma unroll
@@ -224,15 +200,30 @@ __device__ inline void load_logits(const T* row, int64_t at, int64_t stride, int
     }
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = x[i] == x[i] ? x[i] : -INFINITY;
+  for (int i = 0; i < PER; ++i) x[i] = x[i] == x[i] ? x[i] : -INFINITY;
 }
 // A slice's logits spread over the workgroup, neighbours in neighbouring threads; and the logit that x[i] is.
-template <typename T>
+template <typename T, int PER = kPer>
 __device__ inline int64_t load_slice(const T* row, int slice, int64_t n, float* x) {
   constexpr int kV = 16 / sizeof(T);
-  const int64_t at = (int64_t)slice * blockDim.x * kPer + (int)threadIdx.x * kV - lead_of(row);
-  load_logits(row, at, (int64_t)blockDim.x * kV, n, x);
+  const int64_t at = (int64_t)slice * blockDim.x * PER + (int)threadIdx.x * kV - lead_of(row);
+  load_logits<T, PER>(row, at, (int64_t)blockDim.x * kV, n, x);
   return at;
+}
+// The same in any order, for parts of fewer than 16 bytes per thread.
+template <typename T, int PER>
+__device__ inline void load_part(const T* row, int slice, int64_t n, float* x) {
+  if constexpr (PER * sizeof(T) >= 16) {
+    load_slice<T, PER>(row, slice, n, x);
+  } else {
+    const int64_t at = (int64_t)slice * blockDim.x * PER - lead_of(row) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t j = at + (int64_t)i * blockDim.x;
+      x[i] = j >= 0 && j < n ? (float)row[j] : -INFINITY;
+      x[i] = x[i] == x[i] ? x[i] : -INFINITY;
+    }
+  }
 }
 template <typename T>
 __device__ inline int64_t logit_of(int64_t at, int i) {
@@ -277,11 +268,6 @@ struct BinsShared {
   unsigned long long sum[kBins / 64];
   unsigned tokens[kBins / 64];
   double roots[kRoots];
-  double cum_mass[kBins];
-  unsigned cum_count[kBins];
-  double scale[kMaxSlices];
-  int shift[kMaxSlices];
-  int flag;
 };
 
 // The largest of a workgroup's logits and its first place, in all threads.
@@ -322,13 +308,26 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
   if (q.sums && best > -INFINITY) {  // uniform
     const Scale sc{best, q.inv_t, sh.roots};
     const int top = bin_of(best, q.per);
+    constexpr int kSide = 4;  // exponentials side by side, without branches, so that they overlap
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (!(x[i] > -INFINITY)) continue;
-      const int b = top - bin_of(x[i], q.per);
-      if (b >= kBins) continue;
-      atomicAdd(&sh.mass[b], (unsigned long long)sc.weight(x[i]));
-      if (q.use_k) atomicAdd(&sh.count[b], 1u);
+    for (int i0 = 0; i0 < kPer; i0 += kSide) {
+      uint64_t w[kSide];
+      int b[kSide];
+#pragma unroll
+      for (int i = 0; i < kSide; ++i) w[i] = sc.weight(x[i0 + i]), b[i] = top - bin_of(x[i0 + i], q.per);
+#pragma unroll
+      for (int i = 0; i < kSide; ++i) {
+        const float v = x[i0 + i];
+        if (!(v > -INFINITY) || b[i] >= kBins) continue;
+        // equal logits of a wave (16-bit ones, flat rows) would queue at one address
+        const uint64_t same = __ballot(v == __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v))));
+        const bool first = (same & ((uint64_t(1) << lane) - 1)) == 0, other = !(same >> lane & 1);
+        const unsigned n = other ? 1u : (unsigned)__popcll(same);
+        if (other || first) {
+          atomicAdd(&sh.mass[b[i]], (unsigned long long)(w[i] * n));
+          if (q.use_k) atomicAdd(&sh.count[b[i]], n);
+        }
+      }
     }
   }
   __syncthreads();
@@ -336,25 +335,42 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
   if (q.sums) {  // sums from the first bin on: every sum that is asked for later is one number
     uint64_t m = 0, c = 0;
     if (tid < kBins) {
-      m = wave_scan((uint64_t)sh.mass[tid], lane);
-      if (q.use_k) c = wave_scan((uint64_t)sh.count[tid], lane);
+      m = wave_scan((uint64_t)sh.mass[tid]);
+      if (q.use_k) c = wave_scan((uint64_t)sh.count[tid]);
       if (lane == 63) sh.sum[tid >> 6] = m, sh.tokens[tid >> 6] = (unsigned)c;
     }
     __syncthreads();
     if (tid < kBins) {
       for (int w = 0; w < tid >> 6; ++w) m += sh.sum[w], c += sh.tokens[w];
-      put(&ws.mass[part * kBins + tid], (unsigned long long)m);
-      if (q.use_k) put(&ws.count[part * kBins + tid], (unsigned)c);
+      ws.mass[part * kBins + tid] = m;
+      if (q.use_k) ws.count[part * kBins + tid] = (unsigned)c;
     }
   }
-  if (tid == 0) put(&ws.parts[part], __builtin_bit_cast(unsigned long long, (Slice{best, at})));
-  if (!last_of(&ws.counters[4 * r], ws.slices, &sh.flag)) return;
+  if (tid == 0) ws.parts[part] = {best, at};
+}
 
-  // the row
-  best = -INFINITY, at = 0x7FFFFFFF;
+struct PlanShared {
+  float best[kMaxWaves];
+  int best_at[kMaxWaves];
+  double roots[kRoots];
+  double cum_mass[kBins];
+  unsigned cum_count[kBins];
+  double scale[kMaxSlices];
+  int shift[kMaxSlices];
+};
+
+// kBins threads
+__global__ __launch_bounds__(kBins) void plan_kernel(tq_sample_args a, Space ws) {
+  __shared__ PlanShared sh;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t r = blockIdx.x;
+  const Request q = request(a, r);
+  fill_roots(sh.roots);
+  float best = -INFINITY;
+  int at = 0x7FFFFFFF;
   Slice mine{-INFINITY, 0x7FFFFFFF};
   if (tid < ws.slices) {
-    mine = __builtin_bit_cast(Slice, get(&ws.parts[r * ws.slices + tid]));
+    mine = ws.parts[r * ws.slices + tid];
     best = mine.most, at = mine.at;
   }
   block_best(&best, &at, sh.best, sh.best_at);
@@ -373,20 +389,25 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
     sh.shift[tid] = some ? min(top - bin_of(mine.most, q.per), kBins) : kBins;
   }
   __syncthreads();
-  if (tid < kBins) {
+  {
     double m = 0;
     unsigned c = 0;
-    if (q.sums) {
-#pragma unroll 8
-      for (int s = 0; s < ws.slices; ++s) {
-        const int b = tid - sh.shift[s];
-        const int64_t i = (r * ws.slices + s) * kBins + max(b, 0);
-        const double v = (double)get(&ws.mass[i]);
-        m = b >= 0 ? __builtin_fma(v, sh.scale[s], m) : m;
-        if (q.use_k) {
-          const unsigned n = get(&ws.count[i]);
-          c += b >= 0 ? n : 0;
-        }
+    // kAhead slices' numbers are asked for before the first is used (counts also where nobody wrote any: they are not used then)
+    constexpr int kAhead = 16;
+    const int64_t i0 = r * ws.slices * kBins;
+    for (int s0 = 0; s0 < ws.slices && q.sums; s0 += kAhead) {
+      unsigned long long v[kAhead];
+      unsigned w[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = min(s0 + j, ws.slices - 1);
+        const int64_t i = i0 + s * kBins + max(tid - sh.shift[s], 0);
+        v[j] = ws.mass[i], w[j] = ws.count[i];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = min(s0 + j, ws.slices - 1);
+        if (s0 + j < ws.slices && tid >= sh.shift[s]) m = __builtin_fma((double)v[j], sh.scale[s], m), c += w[j];
       }
     }
     sh.cum_mass[tid] = m, sh.cum_count[tid] = c;
@@ -463,8 +484,33 @@ struct PickShared {
   double run;
   unsigned long long tied;
   double roots[kRoots];
-  unsigned long long near[kNear];  // the first of the list
+  uint32_t near[kNear];  // the first of the list
+  unsigned share[kMaxSlices + 1];  // a slice's first place in the row's list
 };
+
+// A token's digit counted.  Equal logits (16-bit ones are many) would queue at one address: the first few different keys of a
+// wave are counted by one lane each.
+__device__ inline void count_digit(uint32_t key, uint32_t b, const Scale& sc, PickShared& sh) {
+  const uint64_t w = sc.weight(value_of(key));
+  const int lane = threadIdx.x & 63;
+  uint64_t left = __ballot(true);
+#pragma unroll 1
+  for (int i = 0; i < 8 && left; ++i) {
+    const int who = __builtin_ctzll(left);
+    const uint64_t same = __ballot(key == (uint32_t)__builtin_amdgcn_readlane((int)key, who));
+    const int n = __popcll(same);
+    if (lane == who) {
+      atomicAdd(&sh.count[b], (uint32_t)n);
+      atomicAdd(&sh.mass[b], (unsigned long long)(w * n));
+    }
+    left &= ~same;
+    if (n < 4) break;
+  }
+  if (left >> lane & 1) {
+    atomicAdd(&sh.count[b], 1u);
+    atomicAdd(&sh.mass[b], (unsigned long long)w);
+  }
+}
 
 // The beginning of the order, among the keys in [lo, hi] that `each` goes through, that reaches `tokens` tokens (by_count) or
 // the weight `goal` (a fraction of 1), `above` of it already there: by 1024 digits of the keys' range at a time.
@@ -478,11 +524,9 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
     for (int b = tid; b < kDigits; b += blockDim.x) sh.count[b] = 0, sh.mass[b] = 0;
     if (tid == 0) sh.digit = -1;
     __syncthreads();
-    each([&](uint32_t key, int) {
+    each([&](uint32_t key) {
       if (key < lo || key > hi) return;
-      const uint32_t b = (key - lo) >> shift;
-      atomicAdd(&sh.count[b], 1u);
-      atomicAdd(&sh.mass[b], (unsigned long long)sc.weight(value_of(key)));
+      count_digit(key, (key - lo) >> shift, sc, sh);
     });
     __syncthreads();
     // thread i has the digits from kDigits - 1 - per * i downwards
@@ -492,7 +536,7 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
       const int b = kDigits - 1 - (per * tid + j);
       c += sh.count[b], m += sh.mass[b];
     }
-    const uint64_t c_in = wave_scan(c, lane), m_in = wave_scan(m, lane);
+    const uint64_t c_in = wave_scan(c), m_in = wave_scan(m);
     if (lane == 63) sh.part[wave] = c_in, sh.part2[wave] = m_in;
     __syncthreads();
     uint64_t cb = before_count + c_in - c, mb = before_mass + m_in - m;
@@ -546,29 +590,40 @@ struct Kept {
 };
 
 // The token of [first, last) at which the running weight passes `goal` (in units of 2^-43 of the row's largest), `ties` of the
-// equal ones still to come; the last one that weighs anything where it never does.  One workgroup, at most kPer logits a thread.
-template <typename T>
+// equal ones still to come; the last one that weighs anything where it never does.  PER logits a thread.
+template <typename T, int PER>
 __device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, uint64_t ties, double goal, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t at0 = first + (int64_t)tid * kPer;
-  float x[kPer];
-  load_logits(row, at0, 16 / sizeof(T), last, x);
-  uint64_t w[kPer], sum = 0, equal = 0;
-  unsigned tied = 0;
+  const int64_t at0 = first + (int64_t)tid * PER;
+  float x[PER];
+  if constexpr (PER * sizeof(T) >= 16) {
+    load_logits<T, PER>(row, at0, 16 / sizeof(T), last, x);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    double e = 0;
-    const int t = k.test(key_of(x[i]), x[i], &e);
-    w[i] = t ? Scale::units(e) : 0;
+    for (int i = 0; i < PER; ++i) {
+      x[i] = at0 + i >= 0 && at0 + i < last ? (float)row[at0 + i] : -INFINITY;
+      x[i] = x[i] == x[i] ? x[i] : -INFINITY;
+    }
+  }
+  uint64_t w[PER], sum = 0, equal = 0;
+  unsigned tied = 0;
+  double e[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) e[i] = k.sc.e(x[i]);  // (without branches, so that they overlap)
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t key = key_of(x[i]);
+    const int t = key == 0 || key < k.cut.key || !(e[i] >= k.min_p) ? 0 : key == k.cut.key ? 2 : 1;
+    w[i] = t ? Scale::units(e[i]) : 0;
     if (t == 2) tied |= 1u << i, ++equal;
   }
-  const uint64_t eq_in = wave_scan(equal, lane);
+  const uint64_t eq_in = wave_scan(equal);
   if (lane == 63) sh.part[wave] = eq_in;
   __syncthreads();
   uint64_t before = eq_in - equal;
   for (int v = 0; v < wave; ++v) before += sh.part[v];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     if (tied >> i & 1) {
       if (before >= ties) w[i] = 0;
       ++before;
@@ -576,7 +631,7 @@ __device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, ui
     sum += w[i];
   }
   __syncthreads();
-  const uint64_t in = wave_scan(sum, lane);
+  const uint64_t in = wave_scan(sum);
   if (lane == 63) sh.part[wave] = in;
   if (tid == 0) sh.token = -1, sh.pick = 0x7FFFFFFF;
   __syncthreads();
@@ -584,15 +639,19 @@ __device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, ui
   for (int v = 0; v < wave; ++v) run += sh.part[v];
   int found = 0x7FFFFFFF, final = -1;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     run += w[i];
     if (w[i]) {
       final = (int)(at0 - first) + i;
       if ((double)run > goal) found = min(found, final);
     }
   }
-  atomicMin(&sh.pick, found);
-  atomicMax(&sh.token, final);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) found = min(found, __shfl_xor(found, o, 64)), final = max(final, __shfl_xor(final, o, 64));
+  if (lane == 0) {
+    atomicMin(&sh.pick, found);
+    atomicMax(&sh.token, final);
+  }
   __syncthreads();
   const int p = sh.pick != 0x7FFFFFFF ? sh.pick : sh.token;
   __syncthreads();
@@ -603,17 +662,17 @@ __device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, ui
 __device__ inline double goal_of(float u, double sum) { return !(u > 0.0f) ? 0.0 : u >= 1.0f ? INFINITY : (double)u * sum; }
 
 // Per slice: the weight of what stays (units of 2^-43 of the row's largest) and the number equal to the cut's key.
-template <typename T>
+template <typename T, int PER>
 __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q, const Scale& sc, int slices, Kept* kept, PickShared& sh) {
   const T* row = static_cast<const T*>(a.logits) + r * a.logit_stride;
-  const int n = (int)a.vocab, per = (int)blockDim.x * kPer, lead = lead_of(row);
+  const int n = (int)a.vocab;
   const auto each = [&](auto f) {
     for (int s = 0; s < slices; ++s) {
-      float x[kPer];
-      const int64_t at = load_slice(row, s, n, x);
+      float x[PER];
+      load_part<T, PER>(row, s, n, x);
 #pragma unroll 1
-      for (int i = 0; i < kPer; ++i)
-        if (const uint32_t key = key_of(x[i])) f(key, (int)logit_of<T>(at, i));
+      for (int i = 0; i < PER; ++i)
+        if (const uint32_t key = key_of(x[i])) f(key);
     }
   };
   Cut cut{0, 0, 0};
@@ -626,7 +685,7 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
   if (q.use_p) {
     if (stays < 0) {
       uint64_t m = 0;
-      each([&](uint32_t key, int) { m += sc.weight(value_of(key)); });
+      each([&](uint32_t key) { m += sc.weight(value_of(key)); });
       m = wave_total(m);
       if ((threadIdx.x & 63) == 0) sh.part[threadIdx.x >> 6] = m;
       __syncthreads();
@@ -638,90 +697,132 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
     cut = find_cut(each, 1u, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, 0.0, sh);
   }
   *kept = Kept{sc, cut, q.min_p};
-  each([&](uint32_t key, int at) {
-    double e = 0;
-    const int t = kept->test(key, value_of(key), &e);
-    if (t == 1) atomicAdd(&sh.slice_mass[(at + lead) / per], (unsigned long long)Scale::units(e));
-    if (t == 2) atomicAdd(&sh.slice_ties[(at + lead) / per], 1ull);
-  });
+  for (int s = 0; s < slices; ++s) {
+    float x[PER];
+    load_part<T, PER>(row, s, n, x);
+    uint64_t m = 0, ties = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      double e = 0;
+      const int t = kept->test(key_of(x[i]), x[i], &e);
+      if (t == 1) m += Scale::units(e);
+      if (t == 2) ++ties;
+    }
+    m = wave_total(m), ties = wave_total(ties);
+    if ((threadIdx.x & 63) == 0) {
+      atomicAdd(&sh.slice_mass[s], (unsigned long long)m);
+      atomicAdd(&sh.slice_ties[s], (unsigned long long)ties);
+    }
+  }
   __syncthreads();
 }
 
-// ---- the second launch ----
+// ---- the tokens in question ----
+
+__device__ inline bool any_cut(const Row& row) { return row.k_bin < kBins || row.p0 <= row.p1 || row.m0 < kBins; }
 
 template <typename T>
-__global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) {
-  __shared__ PickShared sh;
+__global__ __launch_bounds__(1024) void list_kernel(tq_sample_args a, Space ws) {
+  __shared__ uint32_t keys[kShare];
+  __shared__ unsigned part[kMaxWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int slice = blockIdx.x % ws.slices;
   const int64_t r = blockIdx.x / ws.slices;
+  const Row& row = ws.rows[r];
+  if (!row.search || !any_cut(row)) return;  // uniform
+  const Request q = request(a, r);
+  const int top = row.top_bin, k_bin = row.k_bin < kBins ? row.k_bin : -1, p0 = row.p0, p1 = row.p1, m0 = row.m0, m1 = row.m1;
+  float x[kPer];
+  load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
+  unsigned in = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = top - bin_of(x[i], q.per);
+    if (x[i] > -INFINITY && (b == k_bin || (b >= p0 && b <= p1) || (b >= m0 && b <= m1))) in |= 1u << i;
+  }
+  const unsigned n = __popc(in), upto = (unsigned)wave_scan((uint64_t)n);
+  if (lane == 63) part[wave] = upto;
+  __syncthreads();
+  unsigned before = upto - n, all = 0;
+  for (int w = 0; w < waves; ++w) {
+    if (w < wave) before += part[w];
+    all += part[w];
+  }
+  if (tid == 0) ws.shares[r * ws.slices + slice] = all;
+  if (all == 0 || all > kShare) return;  // (too many: searched otherwise)
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (in >> i & 1) keys[before++] = key_of(x[i]);
+  __syncthreads();
+  for (unsigned i = tid; i < all; i += blockDim.x) ws.list[(r * ws.slices + slice) * kShare + i] = keys[i];
+}
+
+// ---- the draw ----
+
+// kPickThreads threads, PER of a slice's logits for each.
+template <typename T, int PER>
+__global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Space ws) {
+  __shared__ PickShared sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int waves = kPickThreads / 64, per = PER * kPickThreads;
+  const int64_t r = blockIdx.x;
   const Row row = ws.rows[r];
-  if (!row.search) return;  // uniform over the row
+  if (!row.search) return;  // uniform
   const Request q = request(a, r);
   fill_roots(sh.roots);
   const Scale sc{row.most, q.inv_t, sh.roots};
   const T* logits = static_cast<const T*>(a.logits) + r * a.logit_stride;
-  unsigned* places = &ws.counters[4 * r + 2];
-  const bool use_k = row.k_bin < kBins, use_p = row.p0 <= row.p1, use_m = row.m0 < kBins;
-  const auto listed = [&](int b) { return (use_k && b == row.k_bin) || (b >= row.p0 && b <= row.p1) || (b >= row.m0 && b <= row.m1); };
-
-  // this slice's tokens of the listed bins
-  if (use_k || use_p || use_m) {
-    float x[kPer];
-    const int64_t at0 = load_slice(logits, slice, a.vocab, x);
-    unsigned in = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (x[i] > -INFINITY && listed(row.top_bin - bin_of(x[i], q.per))) in |= 1u << i;
-    const unsigned n = __popc(in);
-    const unsigned upto = (unsigned)wave_scan((uint64_t)n, lane);
-    if (lane == 63) sh.part[wave] = upto;
-    __syncthreads();
-    unsigned before = upto - n, all = 0;
-    for (int w = 0; w < waves; ++w) {
-      if (w < wave) before += (unsigned)sh.part[w];
-      all += (unsigned)sh.part[w];
-    }
-    if (tid == 0) sh.pick = all ? (int)__hip_atomic_fetch_add(places, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    __syncthreads();
-    int64_t to = (int64_t)(unsigned)sh.pick + before;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (in >> i & 1) {
-        if (to < ws.most) put(&ws.list[r * ws.most + to], (unsigned long long)key_of(x[i]) << 32 | (unsigned)logit_of<T>(at0, i));
-        ++to;
-      }
+  const bool use_k = row.k_bin < kBins, use_p = row.p0 <= row.p1;
+  // the slices' shares one behind the other, in LDS as far as they fit
+  if (tid < ws.slices) {
+    sh.slice_mass[tid] = 0, sh.slice_ties[tid] = 0;
+    sh.share[tid + 1] = any_cut(row) ? ws.shares[r * ws.slices + tid] : 0;
   }
-  if (!last_of(&ws.counters[4 * r + 1], ws.slices, &sh.flag)) return;
-
-  const unsigned n = get(places);
-  for (unsigned i = tid; i < min(n, (unsigned)kNear); i += blockDim.x) sh.near[i] = get(&ws.list[r * ws.most + i]);
-  const int per = (int)blockDim.x * kPer, lead = lead_of(logits);
-  for (int s = tid; s < ws.slices; s += blockDim.x) sh.slice_mass[s] = 0, sh.slice_ties[s] = 0;
   __syncthreads();
-  if (tid == 0) put(places, 0u);
+  if (wave == 0) {  // slices 2 lane, 2 lane + 1
+    const unsigned c0 = 2 * lane < ws.slices ? sh.share[2 * lane + 1] : 0, c1 = 2 * lane + 1 < ws.slices ? sh.share[2 * lane + 2] : 0;
+    const uint64_t over = __ballot(c0 > kShare || c1 > kShare);
+    const unsigned upto = (unsigned)wave_scan((uint64_t)c0 + c1);
+    if (2 * lane < ws.slices) sh.share[2 * lane + 1] = upto - c1;
+    if (2 * lane + 1 < ws.slices) sh.share[2 * lane + 2] = upto;
+    if (lane == 0) sh.share[0] = 0, sh.flag = over != 0;
+  }
+  __syncthreads();
+  const bool too_many = sh.flag;
+  const unsigned n = sh.share[ws.slices];
+  const uint32_t* list = ws.list + r * ws.slices * kShare;
+  if (!too_many) {
+    for (int s = wave; s < ws.slices; s += waves)
+      for (unsigned i = sh.share[s] + lane; i < min(sh.share[s + 1], (unsigned)kNear); i += 64) sh.near[i] = list[s * kShare + i - sh.share[s]];
+  }
+  __syncthreads();
   Kept kept{sc, {0, 0, 0}, q.min_p};
   int sure = kBins;  // tokens of the bins above it stay, and are not in question
-  if (n > (unsigned)ws.most) {
-    search_row<T>(a, r, q, sc, ws.slices, &kept, sh);
+  if (too_many) {
+    search_row<T, PER>(a, r, q, sc, ws.slices, &kept, sh);
     sure = 0;
   } else {
-    const unsigned long long* list = ws.list + r * ws.most;
     // the listed tokens of the bins [b0, b1]
     const auto each_of = [&](int b0, int b1) {
       return [&, b0, b1](auto f) {
-        for (unsigned i = tid; i < n; i += blockDim.x) {
-          const unsigned long long v = i < kNear ? sh.near[i] : get(&list[i]);
-          const uint32_t key = (uint32_t)(v >> 32);
+        const auto one = [&](uint32_t key) {
           const int b = row.top_bin - bin_of(value_of(key), q.per);
-          if (b >= b0 && b <= b1) f(key, (int)(uint32_t)v);
-        }
+          if (b >= b0 && b <= b1) f(key);
+        };
+        for (unsigned i = tid; i < min(n, (unsigned)kNear); i += blockDim.x) one(sh.near[i]);
+        if (n > kNear)
+          for (int s = wave; s < ws.slices; s += waves)
+            for (unsigned i = max(sh.share[s], (unsigned)kNear) + lane; i < sh.share[s + 1]; i += 64) one(list[s * kShare + i - sh.share[s]]);
       };
     };
     const auto lowest = [&](int b0, int b1) {  // key
       if (tid == 0) sh.kmin = 0xFFFFFFFFu;
       __syncthreads();
-      each_of(b0, b1)([&](uint32_t key, int) { atomicMin(&sh.kmin, key); });
+      uint32_t least = 0xFFFFFFFFu;
+      each_of(b0, b1)([&](uint32_t key) { least = min(least, key); });
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) least = min(least, (uint32_t)__shfl_xor(least, o, 64));
+      if (lane == 0) atomicMin(&sh.kmin, least);
       __syncthreads();
       return sh.kmin;
     };
@@ -742,7 +843,7 @@ __global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) 
     }
     sure = min(cut_bin, row.m0);
     for (int s = tid; s < ws.slices && sure > 0; s += blockDim.x) {
-      const Slice part = __builtin_bit_cast(Slice, ws.parts[r * ws.slices + s]);
+      const Slice part = ws.parts[r * ws.slices + s];
       double m = 0;
       if (part.most > -INFINITY) {
         const int b = min(sure, kBins) - 1 - (row.top_bin - bin_of(part.most, q.per));
@@ -751,12 +852,23 @@ __global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) 
       sh.slice_sum[s] = m;
     }
     // what is in question: the cut's bin, and those of min_p above it
-    each_of(sure, min(cut_bin, row.m1))([&](uint32_t key, int at) {
-      double e = 0;
-      const int t = kept.test(key, value_of(key), &e);
-      if (t == 1) atomicAdd(&sh.slice_mass[(at + lead) / per], (unsigned long long)Scale::units(e));
-      if (t == 2) atomicAdd(&sh.slice_ties[(at + lead) / per], 1ull);
-    });
+    for (int s = wave; s < ws.slices && n > 0; s += waves) {
+      const unsigned first = sh.share[s], last = sh.share[s + 1];
+      if (first == last) continue;
+      uint64_t m = 0, ties = 0;
+      for (unsigned i = first + lane; i < last; i += 64) {
+        const uint32_t key = i < kNear ? sh.near[i] : list[s * kShare + i - first];
+        const float x = value_of(key);
+        const int b = row.top_bin - bin_of(x, q.per);
+        if (b < sure || b > min(cut_bin, row.m1)) continue;
+        double e = 0;
+        const int t = kept.test(key, x, &e);
+        if (t == 1) m += Scale::units(e);
+        if (t == 2) ++ties;
+      }
+      m = wave_total(m), ties = wave_total(ties);
+      if (lane == 0) sh.slice_mass[s] = m, sh.slice_ties[s] = ties;
+    }
     __syncthreads();
   }
 
@@ -772,14 +884,14 @@ __global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) 
       t[j] = sh.slice_ties[s];
       m[j] = (sure > 0 ? sh.slice_sum[s] : 0.0) + (double)sh.slice_mass[s];
     }
-    const uint64_t t_in = wave_scan(t[0] + t[1], lane);
+    const uint64_t t_in = wave_scan(t[0] + t[1]);
     uint64_t left[2];  // ties that are still to come where a slice begins
     left[0] = kept.cut.ties - min(kept.cut.ties, t_in - t[0] - t[1]);
     left[1] = left[0] - min(left[0], t[0]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) m[j] += (double)min(left[j], t[j]) * tie;
-    const double in = wave_scan(m[0] + m[1], lane);
-    const double goal = goal_of(a.u[r], __shfl(in, 63, 64));
+    const double in = wave_scan(m[0] + m[1]);
+    const double goal = goal_of(a.u[r], lane_value(in, 63));
     // the first slice that weighs something and whose sum passes the goal, or the last that weighs something
     const double begin[2] = {in - m[0] - m[1], in - m[1]};
     const bool some[2] = {m[0] > 0, m[1] > 0}, over[2] = {some[0] && begin[1] > goal, some[1] && in > goal};
@@ -797,8 +909,9 @@ __global__ __launch_bounds__(1024) void pick_kernel(tq_sample_args a, Space ws) 
   const uint64_t tied = sh.tied;
   __syncthreads();
   int token = -1;
+  const int lead = lead_of(logits);
   if (pick >= 0)
-    token = draw(logits, (int64_t)pick * per - lead, min((int64_t)a.vocab, (int64_t)(pick + 1) * per - lead), kept, tied, goal, sh);
+    token = draw<T, PER>(logits, (int64_t)pick * per - lead, min((int64_t)a.vocab, (int64_t)(pick + 1) * per - lead), kept, tied, goal, sh);
   if (tid == 0) finish(a, r, token, token < 0 ? 0.0 : sc.z((float)logits[token]), row.total);
 }
 
@@ -806,9 +919,9 @@ template <typename T>
 hipError_t launch_t(tq_sample_args a, hipStream_t s) {
   const Layout l = layout(a.rows, a.vocab);
   char* p = static_cast<char*>(a.workspace);
-  const Space ws{reinterpret_cast<unsigned*>(p), reinterpret_cast<Row*>(p + l.rows), reinterpret_cast<unsigned long long*>(p + l.parts),
+  const Space ws{reinterpret_cast<Row*>(p + l.rows), reinterpret_cast<Slice*>(p + l.parts),
                  reinterpret_cast<unsigned long long*>(p + l.mass), reinterpret_cast<unsigned*>(p + l.count),
-                 reinterpret_cast<unsigned long long*>(p + l.list), l.slices, (int)std::min<int64_t>(kMost, a.vocab)};
+                 reinterpret_cast<uint32_t*>(p + l.list), reinterpret_cast<unsigned*>(p + l.shares), l.slices};
   const int64_t all = a.rows;
   const auto from = [](auto*& q, int64_t n) {
     if (q) q += n;
@@ -819,9 +932,20 @@ hipError_t launch_t(tq_sample_args a, hipStream_t s) {
     hipLaunchKernelGGL((bins_kernel<T>), grid, block, 0, s, a, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((pick_kernel<T>), grid, block, 0, s, a, ws);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)a.rows), dim3(kBins), 0, s, a, ws);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.top_k || a.top_p || a.min_p) {
+      hipLaunchKernelGGL((list_kernel<T>), grid, block, 0, s, a, ws);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const dim3 rows((unsigned)a.rows), pick(kPickThreads);
+    if (l.per == 4 * kPickThreads)
+      hipLaunchKernelGGL((pick_kernel<T, 4>), rows, pick, 0, s, a, ws);
+    else if (l.per == 8 * kPickThreads)
+      hipLaunchKernelGGL((pick_kernel<T, 8>), rows, pick, 0, s, a, ws);
+    else
+      hipLaunchKernelGGL((pick_kernel<T, 16>), rows, pick, 0, s, a, ws);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     a.logits = static_cast<const T*>(a.logits) + kRows * a.logit_stride;
     from(a.u, kRows), from(a.temperature, kRows), from(a.top_k, kRows), from(a.top_p, kRows), from(a.min_p, kRows), from(a.tokens, kRows);
     from(a.logprob, kRows);

@@ -492,8 +492,7 @@ int tq_adapter_add(const tq_adapter_add_args *args, void *stream);
  * and logprob -inf.  Logits of +inf share equally.  e is fp64; sums are good
  * to some 2^-43 of the largest e and do not depend on timing; tokens below
  * 2^-44 of the largest weigh nothing.
- * workspace: tq_sample_workspace_bytes, zeroed before its first use and left
- * ready by every call; calls that overlap need workspaces of their own.  Not
+ * workspace: tq_sample_workspace_bytes of scratch, needs no clearing; not
  * nullable.  vocab 1 to 2^20. */
 typedef struct {
   const void *logits;       /* [rows][vocab], in_type, rows logit_stride elements apart */
