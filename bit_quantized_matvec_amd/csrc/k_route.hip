@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "batch.h"
+#include "lanes.h"
 #include "seq.h"
 
 namespace tq {
@@ -42,26 +43,6 @@ __device__ inline uint64_t ordered_key(double x) {
 __device__ inline uint32_t ordered_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
   return b >> 31 ? ~b : b | 0x80000000u;
-}
-
-template <int CTRL>
-__device__ inline uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
-// The largest of a wave's values, in all lanes: within rows of 16, then row 15 -> 31, then 31 -> 63.
-__device__ inline uint32_t wave_max_u32(uint32_t v) {
-  v = dpp_max<0x111>(v);  // row_shr:1
-  v = dpp_max<0x112>(v);
-  v = dpp_max<0x114>(v);
-  v = dpp_max<0x118>(v);
-  v = dpp_max<0x142>(v);  // row_bcast:15
-  v = dpp_max<0x143>(v);  // row_bcast:31
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ inline double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
 }
 
 // WIDE: keys of fp64 c; otherwise keys of the logits, in the high half.
@@ -87,14 +68,17 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(tq_route_args a) {
   }
   double s[NJ];
   if (a.score == TQ_SOFTMAX) {
-    most = wave_max(most);
+    {  // (exact: the largest key's value)
+      const uint32_t k = wave_max_u32(most > -INFINITY ? ordered_key(most) : 0u);
+      most = k ? __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k) : -INFINITY;
+    }
     double sum = 0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       s[j] = x[j] == -INFINITY ? 0.0 : x[j] == most ? 1.0 : exp((double)x[j] - (double)most);
       sum += s[j];
     }
-    sum = wave_sum(sum);
+    sum = wave_total(sum);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[j] = sum > 0 ? s[j] / sum : 0.0;
   } else {
@@ -170,7 +154,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(tq_route_args a) {
 
   double w = mine >= 0 ? sl[mine] : 0.0;
   if (a.renorm) {
-    const double sum = wave_sum(w);
+    const double sum = wave_total(w);
     w = sum > 0 ? w / sum : 0.0;
   }
   if (lane < a.k) {

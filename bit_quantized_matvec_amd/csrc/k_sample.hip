@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "batch.h"
+#include "lanes.h"
 #include "seq.h"
 
 namespace tq {
@@ -40,6 +41,7 @@ namespace {
 constexpr int kMaxWaves = 16;
 constexpr int kPer = 16;     // logits of a thread of the slices' kernels
 constexpr int kPickThreads = 1024;
+constexpr int kPlanShares = 4;
 constexpr int kBins = 256;   // of 1 / kPerUnit
 constexpr int kPerUnit = 8;
 constexpr int kShare = 1024;  // places of a slice in its row's list
@@ -64,15 +66,17 @@ __device__ inline void fill_roots(double* roots) {
 __device__ inline double exp_of(double z, const double* roots) {
   constexpr double kStep = 0.6931471805599453094 / kRoots, kHigh = (double)(float)kStep;
   constexpr double kLow = (kStep - kHigh) + 2.3190468138462996e-17 / kRoots;  // (the double nearest ln2 is that much short)
-  const double n = __builtin_rint(z * (1.0 / kStep));
+  constexpr double kRound = 0x1.8p52;  // a sum with it is rounded to a whole number, which its low bits hold
+  const double s = __builtin_fma(z, 1.0 / kStep, kRound), n = s - kRound;
+  const int i = (int)__builtin_bit_cast(uint64_t, s);
   const double r = __builtin_fma(n, -kLow, __builtin_fma(n, -kHigh, z));
   double p = __builtin_fma(r, 1.0 / 120, 1.0 / 24);
   p = __builtin_fma(r, p, 1.0 / 6);
   p = __builtin_fma(r, p, 0.5);
   p = __builtin_fma(r, p, 1.0);
   p = __builtin_fma(r, p, 1.0);
-  const int i = (int)n;
-  return __builtin_ldexp(roots[i & (kRoots - 1)] * p, i >> 6);
+  // times 2^(i >> 6), by the exponent's bits: z above -50 keeps them in range
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, roots[i & (kRoots - 1)] * p) + ((uint64_t)(uint32_t)(i >> 6) << 52));
 }
 
 struct Scale {
@@ -91,45 +95,26 @@ struct Scale {
   __device__ static uint64_t units(double e) { return __builtin_bit_cast(uint64_t, __builtin_fma(e, (double)kOne, 0x1p52)) & ((uint64_t(1) << 52) - 1); }
 };
 
-// The bin of a logit: the same for every slice, increasing with x.  (Beyond kFar logits that are 7 apart in z share one.)
-constexpr double kFar = 1e9;
-__device__ inline int bin_of(float x, double per) { return (int)__builtin_floor(fmax(-kFar, fmin((double)x * per, kFar))); }
-
-// Sums over the lanes up to one's own, by DPP (a shuffle through LDS takes ten times as long): within rows of 16 lanes, then
-// the rows' last lanes to the rows behind them.
-template <int CTRL, int ROWS, typename V>
-__device__ inline V lane_moved(V v) {  // 0 where no lane moves in
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
-  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
-}
-template <typename V>  // uint64_t or double
-__device__ inline V wave_scan(V v) {
-  v += lane_moved<0x111, 0xF>(v);  // row_shr:1
-  v += lane_moved<0x112, 0xF>(v);
-  v += lane_moved<0x114, 0xF>(v);
-  v += lane_moved<0x118, 0xF>(v);
-  v += lane_moved<0x142, 0xA>(v);  // row_bcast:15, to rows 1 and 3
-  v += lane_moved<0x143, 0xC>(v);  // row_bcast:31, to rows 2 and 3
-  return v;
-}
-template <typename V>
-__device__ inline V lane_value(V v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
-}
-__device__ inline uint64_t wave_total(uint64_t v) { return lane_value(wave_scan(v), 63); }
+// The bin of a logit, increasing with x and the same for every slice: floor(8 x / T), off by one at most for the rounding of
+// the product.  What lies further from 0 than kFar shares a bin (and is searched otherwise if the cuts lie there).
+constexpr float kFar = 0x1p23f;
+__device__ inline int bin_of(float x, float per) { return (int)__builtin_floorf(__builtin_amdgcn_fmed3f(x * per, -kFar, kFar)); }
 
 // ---- the workspace ----
 
+struct Request {
+  double inv_t, top_p, min_p;
+  float per;  // bins of a unit of x
+  int64_t top_k;
+  bool greedy, use_k, use_p, sums;
+};
 struct Slice {  // a slice's largest logit and its first place
   float most;
   int at;
 };
 // What plan_kernel leaves for the kernels behind it.  Bins count down from that of the row's largest logit.
 struct Row {
+  Request q;
   float most;
   int top_bin;
   int search;       // 0: the token is there already
@@ -231,21 +216,18 @@ __device__ inline int64_t logit_of(int64_t at, int i) {
   return at + (int64_t)(i / kV) * blockDim.x * kV + i % kV;
 }
 
-struct Request {
-  double inv_t, top_p, min_p;
-  double per;  // bins of a unit of x
-  int64_t top_k;
-  bool greedy, use_k, use_p, sums;
-};
 __device__ inline Request request(const tq_sample_args& a, int64_t r) {
+  // all asked for before the first is used (those that are not given read u)
+  const float t0 = (a.temperature ? a.temperature : a.u)[r], p0 = (a.top_p ? a.top_p : a.u)[r], m0 = (a.min_p ? a.min_p : a.u)[r];
+  const int32_t k0 = (a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[r];
   Request q;
-  const float t = a.temperature ? a.temperature[r] : 1.0f;
+  const float t = a.temperature ? t0 : 1.0f;
   q.greedy = !(t > 0.0f);
   q.inv_t = q.greedy ? 1.0 : 1.0 / (double)t;
-  q.per = kPerUnit * q.inv_t;
-  q.top_k = a.top_k ? a.top_k[r] : 0;
-  q.top_p = a.top_p ? (double)a.top_p[r] : 1.0;
-  const double m = a.min_p && !q.greedy ? (double)a.min_p[r] : 0.0;
+  q.per = (float)fmin(kPerUnit * q.inv_t, 0x1p100);
+  q.top_k = a.top_k ? k0 : 0;
+  q.top_p = a.top_p ? (double)p0 : 1.0;
+  const double m = a.min_p && !q.greedy ? (double)m0 : 0.0;
   q.min_p = m > 0.0 ? fmin(m, 1.0) : 0.0;
   q.use_k = !q.greedy && q.top_k > 0 && q.top_k < a.vocab;
   q.use_p = !q.greedy && q.top_p < 1.0;
@@ -263,7 +245,7 @@ __device__ inline void finish(const tq_sample_args& a, int64_t r, int token, dou
 struct BinsShared {
   unsigned long long mass[kBins];
   unsigned count[kBins];
-  float best[kMaxWaves];
+  uint32_t best[kMaxWaves];
   int best_at[kMaxWaves];
   unsigned long long sum[kBins / 64];
   unsigned tokens[kBins / 64];
@@ -271,19 +253,17 @@ struct BinsShared {
 };
 
 // The largest of a workgroup's logits and its first place, in all threads.
-__device__ inline void block_best(float* best, int* at, float* lds_best, int* lds_at) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float ox = __shfl_xor(*best, o, 64);
-    const int oa = __shfl_xor(*at, o, 64);
-    if (ox > *best || (ox == *best && oa < *at)) *best = ox, *at = oa;
-  }
+__device__ inline void block_best(float* best, int* at, uint32_t* lds_best, int* lds_at) {
+  const uint32_t mine = key_of(*best), most = wave_max_u32(mine);
+  const int first = (int)~wave_max_u32(mine == most ? ~(uint32_t)*at : 0u);
   const int waves = blockDim.x >> 6;
-  if ((threadIdx.x & 63) == 0) lds_best[threadIdx.x >> 6] = *best, lds_at[threadIdx.x >> 6] = *at;
+  if ((threadIdx.x & 63) == 0) lds_best[threadIdx.x >> 6] = most, lds_at[threadIdx.x >> 6] = first;
   __syncthreads();
-  *best = lds_best[0], *at = lds_at[0];
+  uint32_t key = lds_best[0];
+  *at = lds_at[0];
   for (int w = 1; w < waves; ++w)
-    if (lds_best[w] > *best || (lds_best[w] == *best && lds_at[w] < *at)) *best = lds_best[w], *at = lds_at[w];
+    if (lds_best[w] > key || (lds_best[w] == key && lds_at[w] < *at)) key = lds_best[w], *at = lds_at[w];
+  *best = key ? value_of(key) : -INFINITY;
   __syncthreads();
 }
 
@@ -317,15 +297,20 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
       for (int i = 0; i < kSide; ++i) w[i] = sc.weight(x[i0 + i]), b[i] = top - bin_of(x[i0 + i], q.per);
 #pragma unroll
       for (int i = 0; i < kSide; ++i) {
-        const float v = x[i0 + i];
-        if (!(v > -INFINITY) || b[i] >= kBins) continue;
-        // equal logits of a wave (16-bit ones, flat rows) would queue at one address
-        const uint64_t same = __ballot(v == __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v))));
-        const bool first = (same & ((uint64_t(1) << lane) - 1)) == 0, other = !(same >> lane & 1);
-        const unsigned n = other ? 1u : (unsigned)__popcll(same);
-        if (other || first) {
-          atomicAdd(&sh.mass[b[i]], (unsigned long long)(w[i] * n));
-          if (q.use_k) atomicAdd(&sh.count[b[i]], n);
+        const bool use = x[i0 + i] > -INFINITY && b[i] < kBins;
+        const uint64_t uses = __ballot(use);
+        if (uses == 0) continue;  // uniform
+        // a wave whose logits share a bin (a flat row) would queue at one address
+        const int first = (int)lane_value((uint32_t)b[i], __builtin_ctzll(uses));
+        if (__ballot(use && b[i] != first) == 0) {
+          const uint64_t sum = wave_total(use ? w[i] : uint64_t(0));
+          if (lane == 0) {
+            atomicAdd(&sh.mass[first], (unsigned long long)sum);
+            if (q.use_k) atomicAdd(&sh.count[first], (unsigned)__popcll(uses));
+          }
+        } else if (use) {
+          atomicAdd(&sh.mass[b[i]], (unsigned long long)w[i]);
+          if (q.use_k) atomicAdd(&sh.count[b[i]], 1u);
         }
       }
     }
@@ -350,17 +335,19 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
 }
 
 struct PlanShared {
-  float best[kMaxWaves];
+  uint32_t best[kMaxWaves];
   int best_at[kMaxWaves];
   double roots[kRoots];
+  double share_mass[kPlanShares][kBins];
+  unsigned share_count[kPlanShares][kBins];
   double cum_mass[kBins];
   unsigned cum_count[kBins];
   double scale[kMaxSlices];
   int shift[kMaxSlices];
 };
 
-// kBins threads
-__global__ __launch_bounds__(kBins) void plan_kernel(tq_sample_args a, Space ws) {
+// kBins threads for each share of the slices
+__global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_args a, Space ws) {
   __shared__ PlanShared sh;
   const int tid = threadIdx.x, lane = tid & 63;
   const int64_t r = blockIdx.x;
@@ -390,27 +377,36 @@ __global__ __launch_bounds__(kBins) void plan_kernel(tq_sample_args a, Space ws)
   }
   __syncthreads();
   {
+    // each slice of this thread's share is asked for before the first is used (counts also where nobody wrote any: they are not
+    // used then)
     double m = 0;
     unsigned c = 0;
-    // kAhead slices' numbers are asked for before the first is used (counts also where nobody wrote any: they are not used then)
-    constexpr int kAhead = 16;
+    constexpr int kEach = (kMaxSlices + kPlanShares - 1) / kPlanShares;
+    const int bin = tid & (kBins - 1), share = tid / kBins;
     const int64_t i0 = r * ws.slices * kBins;
-    for (int s0 = 0; s0 < ws.slices && q.sums; s0 += kAhead) {
-      unsigned long long v[kAhead];
-      unsigned w[kAhead];
+    unsigned long long v[kEach];
+    unsigned w[kEach];
+    if (q.sums) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int s = min(s0 + j, ws.slices - 1);
-        const int64_t i = i0 + s * kBins + max(tid - sh.shift[s], 0);
+      for (int j = 0; j < kEach; ++j) {
+        const int s = min(share + kPlanShares * j, ws.slices - 1);
+        const int64_t i = i0 + s * kBins + max(bin - sh.shift[s], 0);
         v[j] = ws.mass[i], w[j] = ws.count[i];
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int s = min(s0 + j, ws.slices - 1);
-        if (s0 + j < ws.slices && tid >= sh.shift[s]) m = __builtin_fma((double)v[j], sh.scale[s], m), c += w[j];
+      for (int j = 0; j < kEach; ++j) {
+        const int s = share + kPlanShares * j;
+        if (s < ws.slices && bin >= sh.shift[s]) m = __builtin_fma((double)v[j], sh.scale[s], m), c += w[j];
       }
     }
-    sh.cum_mass[tid] = m, sh.cum_count[tid] = c;
+    sh.share_mass[share][bin] = m, sh.share_count[share][bin] = c;
+    __syncthreads();
+    if (tid < kBins) {
+      m = 0, c = 0;
+#pragma unroll
+      for (int j = 0; j < kPlanShares; ++j) m += sh.share_mass[j][tid], c += sh.share_count[j][tid];
+      sh.cum_mass[tid] = m, sh.cum_count[tid] = c;
+    }
   }
   __syncthreads();
   if (tid >= 64) return;
@@ -432,7 +428,7 @@ __global__ __launch_bounds__(kBins) void plan_kernel(tq_sample_args a, Space ws)
     return;
   }
   Row row;
-  row.most = best, row.top_bin = top, row.search = 1, row.total = total;
+  row.q = q, row.most = best, row.top_bin = top, row.search = 1, row.total = total;
   row.k_bin = kBins, row.k_count = 0, row.k_mass = total;
   row.p0 = 1, row.p1 = 0, row.p_mass = 0, row.m0 = row.m1 = kBins;
   double hi = total;
@@ -453,10 +449,10 @@ __global__ __launch_bounds__(kBins) void plan_kernel(tq_sample_args a, Space ws)
     row.p_mass = row.p0 ? sh.cum_mass[row.p0 - 1] : 0.0;
   }
   if (q.min_p > 0.0) {
-    // z = log(min_p): bins of two logits differ from their difference's by one, and by one more for roundings
+    // z = log(min_p): the difference of two logits' bins is off by one, and by two more for roundings
     const int b = (int)fmin(-log(q.min_p) * kPerUnit, 1e6);
-    row.m0 = max(0, b - 2), row.m1 = b + 2;
-    if (fabs((double)best * q.per) >= kFar) row.m0 = 0, row.m1 = kBins;
+    row.m0 = max(0, b - 3), row.m1 = b + 3;
+    if (!(fabsf(best * q.per) < kFar)) row.m0 = 0, row.m1 = kBins;
   }
   if (lane == 0) ws.rows[r] = row;
 }
@@ -479,6 +475,8 @@ struct PickShared {
   unsigned long long before_count, before_mass, digit_count, digit_mass;
   unsigned long long slice_mass[kMaxSlices], slice_ties[kMaxSlices];
   double slice_sum[kMaxSlices];
+  int slice_shift[kMaxSlices];
+  float slice_most[kMaxSlices];
   int flag, pick;
   int token;
   double run;
@@ -487,6 +485,14 @@ struct PickShared {
   uint32_t near[kNear];  // the first of the list
   unsigned share[kMaxSlices + 1];  // a slice's first place in the row's list
 };
+
+// The cut at a key of which there are `equal`, each of weight w, with `sum` above it: `ties` of them, or as many as the goal
+// takes.
+__device__ inline Cut cut_of(uint32_t key, uint64_t ties, uint64_t equal, bool by_count, double goal, double sum, double w) {
+  if (!by_count) ties = w > 0 && goal > sum ? (uint64_t)fmin(fmax(1.0, __builtin_ceil((goal - sum) / w)), 1e9) : 1;
+  ties = min(ties, equal);
+  return {key, ties, sum + (double)ties * w};
+}
 
 // A token's digit counted.  Equal logits (16-bit ones are many) would queue at one address: the first few different keys of a
 // wave are counted by one lane each.
@@ -563,16 +569,28 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
     if (equal == 1) return {lo, 1, above + (double)(before_mass + digit_mass) / (double)kOne};
     if (shift == 0) break;
   }
-  const double sum = above + (double)before_mass / (double)kOne, w = (double)sc.weight(value_of(lo)) / (double)kOne;
-  uint64_t ties = 1;
-  if (by_count) {
-    ties = tokens - before_count;
-  } else {
-    const double need = goal - sum;
-    if (w > 0 && need > 0) ties = (uint64_t)fmin(fmax(1.0, __builtin_ceil(need / w)), 1e9);
+  return cut_of(lo, by_count ? tokens - before_count : 0, equal, by_count, goal, above + (double)before_mass / (double)kOne,
+                (double)sc.weight(value_of(lo)) / (double)kOne);
+}
+
+// The same among at most 64 keys, one per lane (0: none), by every wave for itself: each key's place by comparing it with all.
+__device__ inline Cut small_cut(uint32_t key, int n, const Scale& sc, bool by_count, uint64_t tokens, double goal, double above) {
+  const uint64_t w = key ? sc.weight(value_of(key)) : 0;
+  uint64_t mass = 0;
+  unsigned count = 0, equal = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint32_t k = lane_value(key, j);
+    const uint64_t v = lane_value(w, j);
+    count += k > key, equal += k == key;
+    mass += k > key ? v : 0;
   }
-  ties = min(ties, equal);
-  return {lo, ties, sum + (double)ties * w};
+  const auto reached = [&](uint64_t c, uint64_t m) { return by_count ? c >= tokens : c > 0 && above + (double)m / (double)kOne >= goal; };
+  const uint64_t hit = __ballot(key != 0 && reached(count + equal, mass + w * equal) && !reached(count, mass));
+  const int who = hit ? __builtin_ctzll(hit) : 0;
+  key = lane_value(key, who), count = lane_value(count, who), equal = lane_value(equal, who), mass = lane_value(mass, who);
+  if (!hit) return {0, 0, 0};
+  const double sum = above + (double)mass / (double)kOne, one = (double)lane_value(w, who) / (double)kOne;
+  return cut_of(key, by_count ? tokens - count : 0, equal, by_count, goal, sum, one);
 }
 
 // Whether a logit stays; ties are for the caller to count.
@@ -646,11 +664,11 @@ __device__ int draw(const T* row, int64_t first, int64_t last, const Kept& k, ui
       if ((double)run > goal) found = min(found, final);
     }
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) found = min(found, __shfl_xor(found, o, 64)), final = max(final, __shfl_xor(final, o, 64));
+  // threads are in the order of their logits
+  const uint64_t founds = __ballot(found != 0x7FFFFFFF), finals = __ballot(final >= 0);
   if (lane == 0) {
-    atomicMin(&sh.pick, found);
-    atomicMax(&sh.token, final);
+    if (founds) atomicMin(&sh.pick, (int)lane_value((uint32_t)found, __builtin_ctzll(founds)));
+    if (finals) atomicMax(&sh.token, (int)lane_value((uint32_t)final, 63 - __builtin_clzll(finals)));
   }
   __syncthreads();
   const int p = sh.pick != 0x7FFFFFFF ? sh.pick : sh.token;
@@ -728,17 +746,22 @@ __global__ __launch_bounds__(1024) void list_kernel(tq_sample_args a, Space ws) 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int slice = blockIdx.x % ws.slices;
   const int64_t r = blockIdx.x / ws.slices;
-  const Row& row = ws.rows[r];
+  const Row row = ws.rows[r];
   if (!row.search || !any_cut(row)) return;  // uniform
-  const Request q = request(a, r);
+  const Request& q = row.q;
   const int top = row.top_bin, k_bin = row.k_bin < kBins ? row.k_bin : -1, p0 = row.p0, p1 = row.p1, m0 = row.m0, m1 = row.m1;
+  // floor(v) from top - last to top - first is v from one whole number to below another
+  const int first = min(min(k_bin < 0 ? kBins : k_bin, p0 <= p1 ? p0 : kBins), m0), last = max(max(k_bin, p0 <= p1 ? p1 : -1), m0 < kBins ? m1 : -1);
+  const float low = (float)(top - last), high = (float)(top - first + 1);
   float x[kPer];
   load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
   unsigned in = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
+    const float v = __builtin_amdgcn_fmed3f(x[i] * q.per, -kFar, kFar);
+    if (!(v >= low && v < high && x[i] > -INFINITY)) continue;
     const int b = top - bin_of(x[i], q.per);
-    if (x[i] > -INFINITY && (b == k_bin || (b >= p0 && b <= p1) || (b >= m0 && b <= m1))) in |= 1u << i;
+    if (b == k_bin || (b >= p0 && b <= p1) || (b >= m0 && b <= m1)) in |= 1u << i;
   }
   const unsigned n = __popc(in), upto = (unsigned)wave_scan((uint64_t)n);
   if (lane == 63) part[wave] = upto;
@@ -768,13 +791,18 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
   const int64_t r = blockIdx.x;
   const Row row = ws.rows[r];
   if (!row.search) return;  // uniform
-  const Request q = request(a, r);
+  const Request& q = row.q;
+  const float u = a.u[r];
   fill_roots(sh.roots);
   const Scale sc{row.most, q.inv_t, sh.roots};
   const T* logits = static_cast<const T*>(a.logits) + r * a.logit_stride;
   const bool use_k = row.k_bin < kBins, use_p = row.p0 <= row.p1;
   // the slices' shares one behind the other, in LDS as far as they fit
   if (tid < ws.slices) {
+    const float most = ws.parts[r * ws.slices + tid].most;
+    const bool some = most > -INFINITY;
+    sh.slice_shift[tid] = some ? min(row.top_bin - bin_of(most, q.per), kBins) : kBins;
+    sh.slice_most[tid] = most;
     sh.slice_mass[tid] = 0, sh.slice_ties[tid] = 0;
     sh.share[tid + 1] = any_cut(row) ? ws.shares[r * ws.slices + tid] : 0;
   }
@@ -820,8 +848,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
       __syncthreads();
       uint32_t least = 0xFFFFFFFFu;
       each_of(b0, b1)([&](uint32_t key) { least = min(least, key); });
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) least = min(least, (uint32_t)__shfl_xor(least, o, 64));
+      least = ~wave_max_u32(~least);
       if (lane == 0) atomicMin(&sh.kmin, least);
       __syncthreads();
       return sh.kmin;
@@ -829,26 +856,36 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
     const uint32_t top = key_of(sc.most);
     int cut_bin = kBins;
     double stays = row.k_mass;
+    const bool few = n <= 64;
+    const uint32_t own = few && lane < (int)n ? sh.near[lane] : 0;
+    const int own_bin = own ? row.top_bin - bin_of(value_of(own), q.per) : kBins;
+    const auto cut_in = [&](int b0, int b1, bool by_count, uint64_t tokens, double goal, double above) {
+      if (few) {
+        const uint32_t key = own_bin >= b0 && own_bin <= b1 ? own : 0;
+        Cut c = small_cut(key, (int)n, sc, by_count, tokens, goal, above);
+        if (c.key == 0) c = {~wave_max_u32(key ? ~key : 0u), uint64_t(1) << 32, 0};
+        return c;
+      }
+      const uint32_t low = lowest(b0, b1);
+      Cut c = find_cut(each_of(b0, b1), low, top, sc, by_count, tokens, goal, above, sh);
+      if (c.key == 0) c = {low, uint64_t(1) << 32, 0};  // by roundings not reached: all of these
+      return c;
+    };
     if (use_k) {
-      kept.cut = find_cut(each_of(row.k_bin, row.k_bin), lowest(row.k_bin, row.k_bin), top, sc, true, (uint64_t)q.top_k - row.k_count, 0.0, row.k_mass, sh);
+      kept.cut = cut_in(row.k_bin, row.k_bin, true, (uint64_t)q.top_k - row.k_count, 0.0, row.k_mass);
       stays = kept.cut.sum;
       cut_bin = row.k_bin;
     }
     if (use_p) {
       // the bins from p0 on are in the list up to p1, where the cut is reached
-      const uint32_t low = lowest(row.p0, row.p1);
-      kept.cut = find_cut(each_of(row.p0, row.p1), low, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, row.p_mass, sh);
-      if (kept.cut.key == 0) kept.cut = {low, uint64_t(1) << 32, 0};  // by roundings not reached: all of these
+      kept.cut = cut_in(row.p0, row.p1, false, 0, fmax(q.top_p, 0.0) * stays, row.p_mass);
       cut_bin = row.top_bin - bin_of(value_of(kept.cut.key), q.per);
     }
     sure = min(cut_bin, row.m0);
     for (int s = tid; s < ws.slices && sure > 0; s += blockDim.x) {
-      const Slice part = ws.parts[r * ws.slices + s];
+      const int b = min(sure, kBins) - 1 - sh.slice_shift[s];
       double m = 0;
-      if (part.most > -INFINITY) {
-        const int b = min(sure, kBins) - 1 - (row.top_bin - bin_of(part.most, q.per));
-        if (b >= 0) m = (double)ws.mass[(r * ws.slices + s) * kBins + b] * sc.e(part.most);
-      }
+      if (b >= 0) m = (double)ws.mass[(r * ws.slices + s) * kBins + b] * sc.e(sh.slice_most[s]);
       sh.slice_sum[s] = m;
     }
     // what is in question: the cut's bin, and those of min_p above it
@@ -891,7 +928,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
 #pragma unroll
     for (int j = 0; j < 2; ++j) m[j] += (double)min(left[j], t[j]) * tie;
     const double in = wave_scan(m[0] + m[1]);
-    const double goal = goal_of(a.u[r], lane_value(in, 63));
+    const double goal = goal_of(u, lane_value(in, 63));
     // the first slice that weighs something and whose sum passes the goal, or the last that weighs something
     const double begin[2] = {in - m[0] - m[1], in - m[1]};
     const bool some[2] = {m[0] > 0, m[1] > 0}, over[2] = {some[0] && begin[1] > goal, some[1] && in > goal};
@@ -932,7 +969,7 @@ hipError_t launch_t(tq_sample_args a, hipStream_t s) {
     hipLaunchKernelGGL((bins_kernel<T>), grid, block, 0, s, a, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)a.rows), dim3(kBins), 0, s, a, ws);
+    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)a.rows), dim3(kBins * kPlanShares), 0, s, a, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.top_k || a.top_p || a.min_p) {
       hipLaunchKernelGGL((list_kernel<T>), grid, block, 0, s, a, ws);
