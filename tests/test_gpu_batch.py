@@ -224,6 +224,8 @@ ADAPT = [
     (130, 2, 40, 512, 515, HF, HF, F32),
     (33, 3, 128, 264, 96, F32, BF, HF),
     (20, 2, 256, 2048, 64, BF, BF, F32),
+    (1100, 3, 48, 136, 131, BF, BF, BF),
+    (1030, 40, 80, 64, 70, F32, HF, F32),
     (300, 4, 72, 640, 192, F32, HF, HF),
 ]
 
