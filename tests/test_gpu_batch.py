@@ -138,6 +138,11 @@ EXPERTS = [
     (300, 7, 4, 80, 512, False),
     (64, 64, 8, 48, 1024, False),
     (1, 64, 8, 2048, 5120, False),
+    (100, 2, 1, 520, 5120, False),     # many pairs of one expert: 32 pairs and 256 rows at a time, four runs of five superchunks
+    (70, 2, 1, 1030, 2304, True),      # runs of 3, 3 and 3, an odd last block
+    (60, 1, 1, 3000, 1280, False),     # of 2, 2 and 1
+    (20, 30, 3, 2600, 1536, False),    # few pairs each of many rows: several groups of row blocks per workgroup
+    (12, 60, 6, 1500, 512, True),
 ]
 
 
