@@ -197,9 +197,9 @@ __device__ inline int64_t load_slice(const T* row, int slice, int64_t n, float* 
 }
 // The same in any order, for parts of fewer than 16 bytes per thread.
 template <typename T, int PER>
-__device__ inline void load_part(const T* row, int slice, int64_t n, float* x) {
+__device__ inline int64_t load_part(const T* row, int slice, int64_t n, float* x) {
   if constexpr (PER * sizeof(T) >= 16) {
-    load_slice<T, PER>(row, slice, n, x);
+    return load_slice<T, PER>(row, slice, n, x);
   } else {
     const int64_t at = (int64_t)slice * blockDim.x * PER - lead_of(row) + threadIdx.x;
 #pragma unroll
@@ -208,10 +208,12 @@ __device__ inline void load_part(const T* row, int slice, int64_t n, float* x) {
       x[i] = j >= 0 && j < n ? (float)row[j] : -INFINITY;
       x[i] = x[i] == x[i] ? x[i] : -INFINITY;
     }
+    return at;
   }
 }
-template <typename T>
+template <typename T, int PER>
 __device__ inline int64_t logit_of(int64_t at, int i) {
+  if constexpr (PER * sizeof(T) < 16) return at + (int64_t)i * blockDim.x;
   constexpr int kV = 16 / sizeof(T);
   return at + (int64_t)(i / kV) * blockDim.x * kV + i % kV;
 }
@@ -267,7 +269,8 @@ __device__ inline void block_best(float* best, int* at, uint32_t* lds_best, int*
   __syncthreads();
 }
 
-template <typename T>
+// PER: logits of a thread.
+template <typename T, int PER>
 __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) {
   __shared__ BinsShared sh;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -277,38 +280,28 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
   for (int b = tid; b < kBins; b += blockDim.x) sh.mass[b] = 0, sh.count[b] = 0;
   fill_roots(sh.roots);
 
-  float x[kPer];
-  const int64_t at0 = load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
+  float x[PER];
+  const int64_t at0 = load_part<T, PER>(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
   float best = -INFINITY;
   int at = 0x7FFFFFFF;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (x[i] > best) best = x[i], at = (int)logit_of<T>(at0, i);
+  for (int i = 0; i < PER; ++i)
+    if (x[i] > best) best = x[i], at = (int)logit_of<T, PER>(at0, i);
   block_best(&best, &at, sh.best, sh.best_at);
   if (q.sums && best > -INFINITY) {  // uniform
     const Scale sc{best, q.inv_t, sh.roots};
     const int top = bin_of(best, q.per);
     constexpr int kSide = 4;  // exponentials side by side, without branches, so that they overlap
 #pragma unroll
-    for (int i0 = 0; i0 < kPer; i0 += kSide) {
+    for (int i0 = 0; i0 < PER; i0 += kSide) {
       uint64_t w[kSide];
       int b[kSide];
 #pragma unroll
       for (int i = 0; i < kSide; ++i) w[i] = sc.weight(x[i0 + i]), b[i] = top - bin_of(x[i0 + i], q.per);
 #pragma unroll
       for (int i = 0; i < kSide; ++i) {
-        const bool use = x[i0 + i] > -INFINITY && b[i] < kBins;
-        const uint64_t uses = __ballot(use);
-        if (uses == 0) continue;  // uniform
-        // a wave whose logits share a bin (a flat row) would queue at one address
-        const int first = (int)lane_value((uint32_t)b[i], __builtin_ctzll(uses));
-        if (__ballot(use && b[i] != first) == 0) {
-          const uint64_t sum = wave_total(use ? w[i] : uint64_t(0));
-          if (lane == 0) {
-            atomicAdd(&sh.mass[first], (unsigned long long)sum);
-            if (q.use_k) atomicAdd(&sh.count[first], (unsigned)__popcll(uses));
-          }
-        } else if (use) {
+        // (64 logits in one bin queue for 128 cycles, in 16 bins for 20, in 64 for 13)
+        if (x[i0 + i] > -INFINITY && b[i] < kBins) {
           atomicAdd(&sh.mass[b[i]], (unsigned long long)w[i]);
           if (q.use_k) atomicAdd(&sh.count[b[i]], 1u);
         }
@@ -966,7 +959,11 @@ hipError_t launch_t(tq_sample_args a, hipStream_t s) {
   for (int64_t done = 0; done < all; done += kRows) {
     a.rows = std::min(kRows, all - done);
     const dim3 grid((unsigned)(a.rows * l.slices)), block(l.threads);
-    hipLaunchKernelGGL((bins_kernel<T>), grid, block, 0, s, a, ws);
+    // few slices: more threads for each (one row of 131072: 6.2 us with 256, 3.5 with 1024)
+    if (l.threads == 256 && a.rows * l.slices <= 256)
+      hipLaunchKernelGGL((bins_kernel<T, kPer / 4>), grid, dim3(4 * l.threads), 0, s, a, ws);
+    else
+      hipLaunchKernelGGL((bins_kernel<T, kPer>), grid, block, 0, s, a, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(plan_kernel, dim3((unsigned)a.rows), dim3(kBins * kPlanShares), 0, s, a, ws);
