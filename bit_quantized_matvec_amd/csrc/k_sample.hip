@@ -328,8 +328,6 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
 }
 
 struct PlanShared {
-  uint32_t best[kMaxWaves];
-  int best_at[kMaxWaves];
   double roots[kRoots];
   double share_mass[kPlanShares][kBins];
   unsigned share_count[kPlanShares][kBins];
@@ -346,14 +344,20 @@ __global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_arg
   const int64_t r = blockIdx.x;
   const Request q = request(a, r);
   fill_roots(sh.roots);
-  float best = -INFINITY;
+  // by every wave for itself: slices lane and lane + 64
+  uint32_t key = 0;
   int at = 0x7FFFFFFF;
-  Slice mine{-INFINITY, 0x7FFFFFFF};
-  if (tid < ws.slices) {
-    mine = ws.parts[r * ws.slices + tid];
-    best = mine.most, at = mine.at;
+  Slice mine{-INFINITY, 0x7FFFFFFF};  // slice tid's
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const Slice part = lane + 64 * j < ws.slices ? ws.parts[r * ws.slices + lane + 64 * j] : Slice{-INFINITY, 0x7FFFFFFF};
+    if (key_of(part.most) > key) key = key_of(part.most), at = part.at;  // (equal ones: the first slice has the first place)
+    if (tid == lane + 64 * j) mine = part;
   }
-  block_best(&best, &at, sh.best, sh.best_at);
+  const uint32_t most = wave_max_u32(key);
+  at = (int)~wave_max_u32(key == most ? ~(uint32_t)at : 0u);
+  const float best = most ? value_of(most) : -INFINITY;
+  __syncthreads();  // (the roots)
   if (!(best > -INFINITY)) {  // nothing to draw from
     if (tid == 0) {
       finish(a, r, -1, 0.0, 1.0);
@@ -382,6 +386,7 @@ __global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_arg
     if (q.sums) {
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
+        if (kPlanShares * j >= ws.slices) continue;  // uniform
         const int s = min(share + kPlanShares * j, ws.slices - 1);
         const int64_t i = i0 + s * kBins + max(bin - sh.shift[s], 0);
         v[j] = ws.mass[i], w[j] = ws.count[i];
@@ -475,7 +480,8 @@ struct PickShared {
   double run;
   unsigned long long tied;
   double roots[kRoots];
-  uint32_t near[kNear];  // the first of the list
+  uint32_t near[kNear];  // the first of the list, and their e
+  double near_e[kNear];
   unsigned share[kMaxSlices + 1];  // a slice's first place in the row's list
 };
 
@@ -489,8 +495,7 @@ __device__ inline Cut cut_of(uint32_t key, uint64_t ties, uint64_t equal, bool b
 
 // A token's digit counted.  Equal logits (16-bit ones are many) would queue at one address: the first few different keys of a
 // wave are counted by one lane each.
-__device__ inline void count_digit(uint32_t key, uint32_t b, const Scale& sc, PickShared& sh) {
-  const uint64_t w = sc.weight(value_of(key));
+__device__ inline void count_digit(uint32_t key, uint32_t b, uint64_t w, PickShared& sh) {
   const int lane = threadIdx.x & 63;
   uint64_t left = __ballot(true);
 #pragma unroll 1
@@ -523,9 +528,9 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
     for (int b = tid; b < kDigits; b += blockDim.x) sh.count[b] = 0, sh.mass[b] = 0;
     if (tid == 0) sh.digit = -1;
     __syncthreads();
-    each([&](uint32_t key) {
+    each([&](uint32_t key, uint64_t weight) {
       if (key < lo || key > hi) return;
-      count_digit(key, (key - lo) >> shift, sc, sh);
+      count_digit(key, (key - lo) >> shift, weight, sh);
     });
     __syncthreads();
     // thread i has the digits from kDigits - 1 - per * i downwards
@@ -566,22 +571,37 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
                 (double)sc.weight(value_of(lo)) / (double)kOne);
 }
 
-// The same among at most 64 keys, one per lane (0: none), by every wave for itself: each key's place by comparing it with all.
-__device__ inline Cut small_cut(uint32_t key, int n, const Scale& sc, bool by_count, uint64_t tokens, double goal, double above) {
-  const uint64_t w = key ? sc.weight(value_of(key)) : 0;
+// The same among at most 64 keys (0: none), lane i of every wave with key i and its weight: each wave compares them with a
+// sixteenth of all, and the parts are added through LDS.
+__device__ inline Cut small_cut(uint32_t key, uint64_t w, bool by_count, uint64_t tokens, double goal, double above, PickShared& sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kWaves = kPickThreads / 64;
+  unsigned long long* masses = sh.mass;  // [kWaves][64]
+  uint32_t* counts = sh.count;
+  static_assert(kWaves * 64 <= kDigits, "the digits' places serve here");
   uint64_t mass = 0;
-  unsigned count = 0, equal = 0;
-  for (int j = 0; j < n; ++j) {
+  unsigned count = 0;  // above: low half, equal: high half
+#pragma unroll
+  for (int i = 0; i < 64 / kWaves; ++i) {
+    const int j = wave + kWaves * i;
     const uint32_t k = lane_value(key, j);
     const uint64_t v = lane_value(w, j);
-    count += k > key, equal += k == key;
+    count += (k > key ? 1u : 0u) + (k == key ? 0x10000u : 0u);
     mass += k > key ? v : 0;
   }
+  masses[wave * 64 + lane] = mass, counts[wave * 64 + lane] = count;
+  __syncthreads();
+  mass = 0, count = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) mass += masses[i * 64 + lane], count += counts[i * 64 + lane];
+  __syncthreads();
+  unsigned equal = count >> 16;
+  count &= 0xFFFF;
   const auto reached = [&](uint64_t c, uint64_t m) { return by_count ? c >= tokens : c > 0 && above + (double)m / (double)kOne >= goal; };
   const uint64_t hit = __ballot(key != 0 && reached(count + equal, mass + w * equal) && !reached(count, mass));
-  const int who = hit ? __builtin_ctzll(hit) : 0;
+  if (!hit) return {0, 0, 0};  // uniform over the workgroup
+  const int who = __builtin_ctzll(hit);
   key = lane_value(key, who), count = lane_value(count, who), equal = lane_value(equal, who), mass = lane_value(mass, who);
-  if (!hit) return {0, 0, 0};
   const double sum = above + (double)mass / (double)kOne, one = (double)lane_value(w, who) / (double)kOne;
   return cut_of(key, by_count ? tokens - count : 0, equal, by_count, goal, sum, one);
 }
@@ -683,7 +703,7 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
       load_part<T, PER>(row, s, n, x);
 #pragma unroll 1
       for (int i = 0; i < PER; ++i)
-        if (const uint32_t key = key_of(x[i])) f(key);
+        if (const uint32_t key = key_of(x[i])) f(key, sc.weight(x[i]));
     }
   };
   Cut cut{0, 0, 0};
@@ -696,7 +716,7 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
   if (q.use_p) {
     if (stays < 0) {
       uint64_t m = 0;
-      each([&](uint32_t key) { m += sc.weight(value_of(key)); });
+      each([&](uint32_t, uint64_t weight) { m += weight; });
       m = wave_total(m);
       if ((threadIdx.x & 63) == 0) sh.part[threadIdx.x >> 6] = m;
       __syncthreads();
@@ -814,7 +834,10 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
   const uint32_t* list = ws.list + r * ws.slices * kShare;
   if (!too_many) {
     for (int s = wave; s < ws.slices; s += waves)
-      for (unsigned i = sh.share[s] + lane; i < min(sh.share[s + 1], (unsigned)kNear); i += 64) sh.near[i] = list[s * kShare + i - sh.share[s]];
+      for (unsigned i = sh.share[s] + lane; i < min(sh.share[s + 1], (unsigned)kNear); i += 64) {
+        const uint32_t key = list[s * kShare + i - sh.share[s]];
+        sh.near[i] = key, sh.near_e[i] = sc.e(value_of(key));
+      }
   }
   __syncthreads();
   Kept kept{sc, {0, 0, 0}, q.min_p};
@@ -823,14 +846,28 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
     search_row<T, PER>(a, r, q, sc, ws.slices, &kept, sh);
     sure = 0;
   } else {
-    // the listed tokens of the bins [b0, b1]
+    // this thread's of the near ones
+    constexpr int kOwn = kNear / kPickThreads;
+    uint32_t key[kOwn];
+    uint64_t units[kOwn];
+    int bin[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const unsigned i = tid + kPickThreads * j;
+      key[j] = i < n ? sh.near[i] : 0;
+      units[j] = i < n ? Scale::units(sh.near_e[i]) : 0;
+      bin[j] = row.top_bin - bin_of(key[j] ? value_of(key[j]) : 0.0f, q.per);
+    }
+    // the listed tokens of the bins [b0, b1], and their weights
     const auto each_of = [&](int b0, int b1) {
       return [&, b0, b1](auto f) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+          if (key[j] && bin[j] >= b0 && bin[j] <= b1) f(key[j], units[j]);
         const auto one = [&](uint32_t key) {
           const int b = row.top_bin - bin_of(value_of(key), q.per);
-          if (b >= b0 && b <= b1) f(key);
+          if (b >= b0 && b <= b1) f(key, sc.weight(value_of(key)));
         };
-        for (unsigned i = tid; i < min(n, (unsigned)kNear); i += blockDim.x) one(sh.near[i]);
         if (n > kNear)
           for (int s = wave; s < ws.slices; s += waves)
             for (unsigned i = max(sh.share[s], (unsigned)kNear) + lane; i < sh.share[s + 1]; i += 64) one(list[s * kShare + i - sh.share[s]]);
@@ -840,7 +877,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
       if (tid == 0) sh.kmin = 0xFFFFFFFFu;
       __syncthreads();
       uint32_t least = 0xFFFFFFFFu;
-      each_of(b0, b1)([&](uint32_t key) { least = min(least, key); });
+      each_of(b0, b1)([&](uint32_t key, uint64_t) { least = min(least, key); });
       least = ~wave_max_u32(~least);
       if (lane == 0) atomicMin(&sh.kmin, least);
       __syncthreads();
@@ -855,7 +892,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
     const auto cut_in = [&](int b0, int b1, bool by_count, uint64_t tokens, double goal, double above) {
       if (few) {
         const uint32_t key = own_bin >= b0 && own_bin <= b1 ? own : 0;
-        Cut c = small_cut(key, (int)n, sc, by_count, tokens, goal, above);
+        Cut c = small_cut(key, key ? Scale::units(sh.near_e[lane]) : 0, by_count, tokens, goal, above, sh);
         if (c.key == 0) c = {~wave_max_u32(key ? ~key : 0u), uint64_t(1) << 32, 0};
         return c;
       }
@@ -882,22 +919,35 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
       sh.slice_sum[s] = m;
     }
     // what is in question: the cut's bin, and those of min_p above it
-    for (int s = wave; s < ws.slices && n > 0; s += waves) {
-      const unsigned first = sh.share[s], last = sh.share[s + 1];
-      if (first == last) continue;
-      uint64_t m = 0, ties = 0;
-      for (unsigned i = first + lane; i < last; i += 64) {
-        const uint32_t key = i < kNear ? sh.near[i] : list[s * kShare + i - first];
-        const float x = value_of(key);
-        const int b = row.top_bin - bin_of(x, q.per);
-        if (b < sure || b > min(cut_bin, row.m1)) continue;
-        double e = 0;
-        const int t = kept.test(key, x, &e);
-        if (t == 1) m += Scale::units(e);
-        if (t == 2) ++ties;
+    const int last_bin = min(cut_bin, row.m1);
+    const auto stays_at = [&](uint32_t key, double e) {  // 0, 1 or, for those equal to the cut's key, 2
+      const int b = row.top_bin - bin_of(value_of(key), q.per);
+      return b < sure || b > last_bin || key < kept.cut.key || !(e >= q.min_p) ? 0 : key > kept.cut.key ? 1 : 2;
+    };
+    if (n <= kPickThreads) {  // each thread its one
+      if (tid < (int)n) {
+        const int t = stays_at(sh.near[tid], sh.near_e[tid]);
+        int s = 0;  // the last slice whose share begins at or before this place
+        for (int step = 64; step > 0; step >>= 1)
+          if (s + step < ws.slices && sh.share[s + step] <= (unsigned)tid) s += step;
+        if (t == 1) atomicAdd(&sh.slice_mass[s], (unsigned long long)Scale::units(sh.near_e[tid]));
+        if (t == 2) atomicAdd(&sh.slice_ties[s], 1ull);
       }
-      m = wave_total(m), ties = wave_total(ties);
-      if (lane == 0) sh.slice_mass[s] = m, sh.slice_ties[s] = ties;
+    } else {
+      for (int s = wave; s < ws.slices; s += waves) {
+        const unsigned first = sh.share[s], last = sh.share[s + 1];
+        if (first == last) continue;
+        uint64_t m = 0, ties = 0;
+        for (unsigned i = first + lane; i < last; i += 64) {
+          const uint32_t key = i < kNear ? sh.near[i] : list[s * kShare + i - first];
+          const double e = i < kNear ? sh.near_e[i] : sc.e(value_of(key));
+          const int t = stays_at(key, e);
+          if (t == 1) m += Scale::units(e);
+          if (t == 2) ++ties;
+        }
+        m = wave_total(m), ties = wave_total(ties);
+        if (lane == 0) sh.slice_mass[s] = m, sh.slice_ties[s] = ties;
+      }
     }
     __syncthreads();
   }
