@@ -185,55 +185,68 @@ hipError_t launch_route_n(const tq_route_args& a, hipStream_t s) {
 }
 
 constexpr int kListWaves = 16;
-constexpr int kStep = 8;  // 64-id reads in flight
+constexpr int kStep = 4;  // reads of 256 ids in flight
+
+struct __attribute__((packed, aligned(4))) Ids {
+  unsigned v[4];
+};
 
 // Workgroup e: the pairs of expert e (e == experts: those without one) and offsets[e].
 __global__ __launch_bounds__(64 * kListWaves) void lists_kernel(const int32_t* __restrict__ ids, int pairs, int experts, int32_t* __restrict__ order,
                                                                 int32_t* __restrict__ offsets) {
-  __shared__ int below[kListWaves], ours[kListWaves];
+  __shared__ unsigned below[kListWaves], ours[kListWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const unsigned e = blockIdx.x;  // ids as unsigned: those outside [0, experts) are at least `experts`
-  const int share = ((pairs + waves - 1) / waves + 63) / 64 * 64;
+  const int share = ((pairs + waves - 1) / waves + 255) / 256 * 256;
   const int first = (int)min((int64_t)pairs, (int64_t)wave * share), last = (int)min((int64_t)pairs, (int64_t)first + share);
-  int lt = 0, eq = 0;
-  for (int i = first; i < last; i += 64 * kStep) {
-    unsigned id[kStep];
+  // Four neighbouring ids of each lane per read; behind the end one that is no expert's and not below any.
+  const auto read = [&](int i, Ids* id) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kStep; ++j) {
-      const int p = i + 64 * j + lane;
-      id[j] = p < last ? (unsigned)ids[p] : 0xFFFFFFFFu;
-    }
+      const int p = i + 256 * j + 4 * lane;
+      if (p + 4 <= last) {
+        id[j] = *reinterpret_cast<const Ids*>(ids + p);
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      const bool real = i + 64 * j + lane < last;
-      const unsigned b = min(id[j], (unsigned)experts);
-      lt += __popcll(__ballot(real && b < e));
-      eq += __popcll(__ballot(real && b == e));
+        for (int c = 0; c < 4; ++c) id[j].v[c] = min(id[j].v[c], (unsigned)experts);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) id[j].v[c] = p + c < last ? min((unsigned)ids[p + c], (unsigned)experts) : 0xFFFFFFFFu;
+      }
     }
+  };
+  unsigned lt = 0, eq = 0;  // this lane's
+  for (int i = first; i < last; i += 256 * kStep) {
+    Ids id[kStep];
+    read(i, id);
+#pragma unroll
+    for (int j = 0; j < kStep; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) lt += id[j].v[c] < e, eq += id[j].v[c] == e;
   }
+  lt = wave_total(lt), eq = wave_total(eq);
   if (lane == 0) below[wave] = lt, ours[wave] = eq;
   __syncthreads();
-  int at = 0, all = 0;
-  for (int w = 0; w < waves; ++w) {
-    at += below[w] + (w < wave ? ours[w] : 0);
-    all += below[w];
-  }
-  if (threadIdx.x == 0) offsets[e] = all;
+  // lane w: wave w's
+  const unsigned b = lane < waves ? below[lane] : 0, o = lane < waves ? ours[lane] : 0;
+  const unsigned all = wave_total(b);
+  int at = (int)(all + lane_value(wave_scan(o) - o, wave));
+  if (threadIdx.x == 0) offsets[e] = (int)all;
   if (eq == 0) return;
-  for (int i = first; i < last; i += 64 * kStep) {
-    unsigned id[kStep];
+  for (int i = first; i < last; i += 256 * kStep) {
+    Ids id[kStep];
+    read(i, id);
 #pragma unroll
     for (int j = 0; j < kStep; ++j) {
-      const int p = i + 64 * j + lane;
-      id[j] = p < last ? (unsigned)ids[p] : 0xFFFFFFFFu;
-    }
+      uint64_t hits[4];
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      const int p = i + 64 * j + lane;
-      const bool hit = p < last && min(id[j], (unsigned)experts) == e;
-      const uint64_t hits = __ballot(hit);
-      if (hit) order[at + __popcll(hits & ((uint64_t(1) << lane) - 1))] = p;
-      at += __popcll(hits);
+      for (int c = 0; c < 4; ++c) hits[c] = __ballot(id[j].v[c] == e);
+      if ((hits[0] | hits[1] | hits[2] | hits[3]) == 0) continue;  // uniform
+      const uint64_t lower = (uint64_t(1) << lane) - 1;
+      int to = at + __popcll(hits[0] & lower) + __popcll(hits[1] & lower) + __popcll(hits[2] & lower) + __popcll(hits[3] & lower);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (id[j].v[c] == e) order[to++] = i + 256 * j + 4 * lane + c;
+      at += __popcll(hits[0]) + __popcll(hits[1]) + __popcll(hits[2]) + __popcll(hits[3]);
     }
   }
 }
@@ -245,7 +258,7 @@ hipError_t launch_route(const tq_route_args& a, hipStream_t s) {
 }
 
 hipError_t launch_expert_lists(const int32_t* ids, int64_t pairs, int experts, int32_t* order, int32_t* offsets, hipStream_t s) {
-  const int waves = (int)std::min<int64_t>(kListWaves, std::max<int64_t>(1, (pairs + 511) / 512));
+  const int waves = (int)std::min<int64_t>(kListWaves, std::max<int64_t>(1, (pairs + 255) / 256));
   hipLaunchKernelGGL(lists_kernel, dim3((unsigned)experts + 1), dim3(64 * waves), 0, s, ids, (int)pairs, experts, order, offsets);
   return hipGetLastError();
 }
