@@ -30,6 +30,7 @@
 // kernel's work, cost one row as much and 256 rows twice: counting arrivals
 // across the XCDs takes some 15 ns a workgroup whatever the counter's place.)
 #include <algorithm>
+#include <type_traits>
 
 #include "batch.h"
 #include "lanes.h"
@@ -56,6 +57,14 @@ __device__ inline uint32_t key_of(float x) {  // 0: never drawn
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 __device__ inline float value_of(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
+// 16-bit logits as fp32 leave the lowest bits of keys alike.
+template <typename T>
+constexpr int kSame = sizeof(T) == 4 ? 0 : __is_same(T, bf16) ? 16 : 13;
+template <int SAME>
+__device__ inline uint32_t whole_key(uint32_t k) {  // of key >> SAME
+  const uint32_t key = k << SAME;
+  return key >> 31 ? key : key | ((1u << SAME) - 1);
+}
 
 // exp(z) for z in [-50, 0]: z = (64 k + j) ln2 / 64 + r, |r| <= ln2 / 128, exp(z) = 2^k 2^(j/64) exp(r), the last by its series
 // to r^6 / 720 < 2^-54.  k ln2 / 64 is taken off in two parts, the first of 24 bits, so that its product is exact.
@@ -90,7 +99,11 @@ struct Scale {
     const double e = exp_of(fmax(v, -50.0), roots);
     return v > -50.0 ? e : 0.0;  // (also where +inf makes z no number)
   }
-  __device__ uint64_t weight(float x) const { return units(e(x)); }
+  // units(e(x)), which of e^-50 are none.  FINITE: the largest logit is.
+  template <bool FINITE = false>
+  __device__ uint64_t weight(float x) const {
+    return units(exp_of(fmax(FINITE ? ((double)x - (double)most) * inv_t : z(x), -50.0), roots));
+  }
   // A number up to 1 as a whole number of 2^-43: the low bits of its sum with 2^52
   __device__ static uint64_t units(double e) { return __builtin_bit_cast(uint64_t, __builtin_fma(e, (double)kOne, 0x1p52)) & ((uint64_t(1) << 52) - 1); }
 };
@@ -292,21 +305,27 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
     const Scale sc{best, q.inv_t, sh.roots};
     const int top = bin_of(best, q.per);
     constexpr int kSide = 4;  // exponentials side by side, without branches, so that they overlap
+    const auto add = [&](auto finite) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i0 = 0; i0 < PER; i0 += kSide) {
-      uint64_t w[kSide];
-      int b[kSide];
+      for (int i0 = 0; i0 < PER; i0 += kSide) {
+        uint64_t w[kSide];
+        int b[kSide];
 #pragma unroll
-      for (int i = 0; i < kSide; ++i) w[i] = sc.weight(x[i0 + i]), b[i] = top - bin_of(x[i0 + i], q.per);
+        for (int i = 0; i < kSide; ++i) w[i] = sc.weight<decltype(finite)::value>(x[i0 + i]), b[i] = top - bin_of(x[i0 + i], q.per);
 #pragma unroll
-      for (int i = 0; i < kSide; ++i) {
-        // (64 logits in one bin queue for 128 cycles, in 16 bins for 20, in 64 for 13)
-        if (x[i0 + i] > -INFINITY && b[i] < kBins) {
-          atomicAdd(&sh.mass[b[i]], (unsigned long long)w[i]);
-          if (q.use_k) atomicAdd(&sh.count[b[i]], 1u);
+        for (int i = 0; i < kSide; ++i) {
+          // (64 logits in one bin queue for 128 cycles, in 16 bins for 20, in 64 for 13)
+          if (x[i0 + i] > -INFINITY && b[i] < kBins) {
+            atomicAdd(&sh.mass[b[i]], (unsigned long long)w[i]);
+            if (q.use_k) atomicAdd(&sh.count[b[i]], 1u);
+          }
         }
       }
-    }
+    };
+    if (best < INFINITY)
+      add(std::true_type());
+    else
+      add(std::false_type());
   }
   __syncthreads();
   const int64_t part = r * ws.slices + slice;
@@ -468,7 +487,7 @@ struct PickShared {
   unsigned long long mass[kDigits];
   uint32_t count[kDigits];
   unsigned long long part[kMaxWaves], part2[kMaxWaves];
-  uint32_t kmin;
+  uint32_t kmin, kmax;
   int digit;
   unsigned long long before_count, before_mass, digit_count, digit_mass;
   unsigned long long slice_mass[kMaxSlices], slice_ties[kMaxSlices];
@@ -518,10 +537,11 @@ __device__ inline void count_digit(uint32_t key, uint32_t b, uint64_t w, PickSha
 
 // The beginning of the order, among the keys in [lo, hi] that `each` goes through, that reaches `tokens` tokens (by_count) or
 // the weight `goal` (a fraction of 1), `above` of it already there: by 1024 digits of the keys' range at a time.
-template <typename EACH>
+template <int SAME, typename EACH>
 __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bool by_count, uint64_t tokens, double goal, double above, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint64_t before_count = 0, before_mass = 0, equal = 0;
+  lo >>= SAME, hi >>= SAME;
   while (true) {
     int shift = 0;
     while ((hi - lo) >> shift >= kDigits) ++shift;
@@ -529,8 +549,9 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
     if (tid == 0) sh.digit = -1;
     __syncthreads();
     each([&](uint32_t key, uint64_t weight) {
-      if (key < lo || key > hi) return;
-      count_digit(key, (key - lo) >> shift, weight, sh);
+      const uint32_t k = key >> SAME;
+      if (k < lo || k > hi) return;
+      count_digit(key, (k - lo) >> shift, weight, sh);
     });
     __syncthreads();
     // thread i has the digits from kDigits - 1 - per * i downwards
@@ -564,11 +585,12 @@ __device__ Cut find_cut(EACH each, uint32_t lo, uint32_t hi, const Scale& sc, bo
     hi = (uint32_t)min((uint64_t)hi, lo + ((uint64_t)(digit + 1) << shift) - 1);
     lo += (uint32_t)digit << shift;
     // one token in the digit: all from its lowest key on stay
-    if (equal == 1) return {lo, 1, above + (double)(before_mass + digit_mass) / (double)kOne};
+    if (equal == 1) return {whole_key<SAME>(lo), 1, above + (double)(before_mass + digit_mass) / (double)kOne};
     if (shift == 0) break;
   }
-  return cut_of(lo, by_count ? tokens - before_count : 0, equal, by_count, goal, above + (double)before_mass / (double)kOne,
-                (double)sc.weight(value_of(lo)) / (double)kOne);
+  const uint32_t key = whole_key<SAME>(lo);
+  return cut_of(key, by_count ? tokens - before_count : 0, equal, by_count, goal, above + (double)before_mass / (double)kOne,
+                (double)sc.weight(value_of(key)) / (double)kOne);
 }
 
 // The same among at most 64 keys (0: none), lane i of every wave with key i and its weight: each wave compares them with a
@@ -710,7 +732,7 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
   const uint32_t top = key_of(sc.most);
   double stays = -1;
   if (q.use_k) {
-    cut = find_cut(each, 1u, top, sc, true, (uint64_t)q.top_k, 0.0, 0.0, sh);
+    cut = find_cut<kSame<T>>(each, 1u, top, sc, true, (uint64_t)q.top_k, 0.0, 0.0, sh);
     if (cut.key) stays = cut.sum;
   }
   if (q.use_p) {
@@ -725,7 +747,7 @@ __device__ void search_row(const tq_sample_args& a, int64_t r, const Request& q,
       __syncthreads();
       stays = (double)m / (double)kOne;
     }
-    cut = find_cut(each, 1u, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, 0.0, sh);
+    cut = find_cut<kSame<T>>(each, 1u, top, sc, false, 0, fmax(q.top_p, 0.0) * stays, 0.0, sh);
   }
   *kept = Kept{sc, cut, q.min_p};
   for (int s = 0; s < slices; ++s) {
@@ -873,17 +895,16 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
             for (unsigned i = max(sh.share[s], (unsigned)kNear) + lane; i < sh.share[s + 1]; i += 64) one(list[s * kShare + i - sh.share[s]]);
       };
     };
-    const auto lowest = [&](int b0, int b1) {  // key
-      if (tid == 0) sh.kmin = 0xFFFFFFFFu;
+    const auto key_range = [&](int b0, int b1) {  // the lowest and the highest key
+      if (tid == 0) sh.kmin = 0xFFFFFFFFu, sh.kmax = 0;
       __syncthreads();
-      uint32_t least = 0xFFFFFFFFu;
-      each_of(b0, b1)([&](uint32_t key, uint64_t) { least = min(least, key); });
-      least = ~wave_max_u32(~least);
-      if (lane == 0) atomicMin(&sh.kmin, least);
+      uint32_t least = 0xFFFFFFFFu, most = 0;
+      each_of(b0, b1)([&](uint32_t key, uint64_t) { least = min(least, key), most = max(most, key); });
+      least = ~wave_max_u32(~least), most = wave_max_u32(most);
+      if (lane == 0) atomicMin(&sh.kmin, least), atomicMax(&sh.kmax, most);
       __syncthreads();
-      return sh.kmin;
+      return make_uint2(sh.kmin, sh.kmax);
     };
-    const uint32_t top = key_of(sc.most);
     int cut_bin = kBins;
     double stays = row.k_mass;
     const bool few = n <= 64;
@@ -896,9 +917,10 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
         if (c.key == 0) c = {~wave_max_u32(key ? ~key : 0u), uint64_t(1) << 32, 0};
         return c;
       }
-      const uint32_t low = lowest(b0, b1);
-      Cut c = find_cut(each_of(b0, b1), low, top, sc, by_count, tokens, goal, above, sh);
-      if (c.key == 0) c = {low, uint64_t(1) << 32, 0};  // by roundings not reached: all of these
+      const uint2 range = key_range(b0, b1);
+      if (range.y == 0) return Cut{0xFFFFFFFFu, 0, above};  // (none)
+      Cut c = find_cut<kSame<T>>(each_of(b0, b1), range.x, range.y, sc, by_count, tokens, goal, above, sh);
+      if (c.key == 0) c = {range.x, uint64_t(1) << 32, 0};  // by roundings not reached: all of these
       return c;
     };
     if (use_k) {
