@@ -210,9 +210,9 @@ __device__ inline int64_t load_slice(const T* row, int slice, int64_t n, float* 
 }
 // The same in any order, for parts of fewer than 16 bytes per thread.
 template <typename T, int PER>
-__device__ inline int64_t load_part(const T* row, int slice, int64_t n, float* x) {
+__device__ inline void load_part(const T* row, int slice, int64_t n, float* x) {
   if constexpr (PER * sizeof(T) >= 16) {
-    return load_slice<T, PER>(row, slice, n, x);
+    load_slice<T, PER>(row, slice, n, x);
   } else {
     const int64_t at = (int64_t)slice * blockDim.x * PER - lead_of(row) + threadIdx.x;
 #pragma unroll
@@ -221,12 +221,10 @@ __device__ inline int64_t load_part(const T* row, int slice, int64_t n, float* x
       x[i] = j >= 0 && j < n ? (float)row[j] : -INFINITY;
       x[i] = x[i] == x[i] ? x[i] : -INFINITY;
     }
-    return at;
   }
 }
-template <typename T, int PER>
+template <typename T>
 __device__ inline int64_t logit_of(int64_t at, int i) {
-  if constexpr (PER * sizeof(T) < 16) return at + (int64_t)i * blockDim.x;
   constexpr int kV = 16 / sizeof(T);
   return at + (int64_t)(i / kV) * blockDim.x * kV + i % kV;
 }
@@ -282,8 +280,7 @@ __device__ inline void block_best(float* best, int* at, uint32_t* lds_best, int*
   __syncthreads();
 }
 
-// PER: logits of a thread.
-template <typename T, int PER>
+template <typename T>
 __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) {
   __shared__ BinsShared sh;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -293,13 +290,13 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
   for (int b = tid; b < kBins; b += blockDim.x) sh.mass[b] = 0, sh.count[b] = 0;
   fill_roots(sh.roots);
 
-  float x[PER];
-  const int64_t at0 = load_part<T, PER>(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
+  float x[kPer];
+  const int64_t at0 = load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
   float best = -INFINITY;
   int at = 0x7FFFFFFF;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (x[i] > best) best = x[i], at = (int)logit_of<T, PER>(at0, i);
+  for (int i = 0; i < kPer; ++i)
+    if (x[i] > best) best = x[i], at = (int)logit_of<T>(at0, i);
   block_best(&best, &at, sh.best, sh.best_at);
   if (q.sums && best > -INFINITY) {  // uniform
     const Scale sc{best, q.inv_t, sh.roots};
@@ -307,7 +304,7 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
     constexpr int kSide = 4;  // exponentials side by side, without branches, so that they overlap
     const auto add = [&](auto finite) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i0 = 0; i0 < PER; i0 += kSide) {
+      for (int i0 = 0; i0 < kPer; i0 += kSide) {
         uint64_t w[kSide];
         int b[kSide];
 #pragma unroll
@@ -791,13 +788,24 @@ __global__ __launch_bounds__(1024) void list_kernel(tq_sample_args a, Space ws) 
   float x[kPer];
   load_slice(static_cast<const T*>(a.logits) + r * a.logit_stride, slice, a.vocab, x);
   unsigned in = 0;
+  const auto collect = [&](auto one_range) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float v = __builtin_amdgcn_fmed3f(x[i] * q.per, -kFar, kFar);
-    if (!(v >= low && v < high && x[i] > -INFINITY)) continue;
-    const int b = top - bin_of(x[i], q.per);
-    if (b == k_bin || (b >= p0 && b <= p1) || (b >= m0 && b <= m1)) in |= 1u << i;
-  }
+    for (int i = 0; i < kPer; ++i) {
+      const float v = __builtin_amdgcn_fmed3f(x[i] * q.per, -kFar, kFar);
+      bool ok = v >= low && v < high && x[i] > -INFINITY;
+      if constexpr (!decltype(one_range)::value) {
+        if (!ok) continue;
+        const int b = top - bin_of(x[i], q.per);
+        ok = b == k_bin || (b >= p0 && b <= p1) || (b >= m0 && b <= m1);
+      }
+      in |= ok ? 1u << i : 0u;
+    }
+  };
+  // One cut: its bins are all from `first` to `last`.  (With the test of each logit's bin 256 rows of 200003 take 37 us.)
+  if ((k_bin >= 0) + (p0 <= p1) + (m0 < kBins) == 1)
+    collect(std::true_type());
+  else
+    collect(std::false_type());
   const unsigned n = __popc(in), upto = (unsigned)wave_scan((uint64_t)n);
   if (lane == 63) part[wave] = upto;
   __syncthreads();
@@ -1031,11 +1039,7 @@ hipError_t launch_t(tq_sample_args a, hipStream_t s) {
   for (int64_t done = 0; done < all; done += kRows) {
     a.rows = std::min(kRows, all - done);
     const dim3 grid((unsigned)(a.rows * l.slices)), block(l.threads);
-    // few slices: more threads for each (one row of 131072: 6.2 us with 256, 3.5 with 1024)
-    if (l.threads == 256 && a.rows * l.slices <= 256)
-      hipLaunchKernelGGL((bins_kernel<T, kPer / 4>), grid, dim3(4 * l.threads), 0, s, a, ws);
-    else
-      hipLaunchKernelGGL((bins_kernel<T, kPer>), grid, block, 0, s, a, ws);
+    hipLaunchKernelGGL((bins_kernel<T>), grid, block, 0, s, a, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(plan_kernel, dim3((unsigned)a.rows), dim3(kBins * kPlanShares), 0, s, a, ws);
