@@ -3,10 +3,16 @@
 //
 // The arithmetic of each pair is the matrix-vector product's (k_gemv_pq2.hip)
 // bit for bit: wave w of a workgroup sums run w of its superchunks, in fp64,
-// and the runs are added in order.  A workgroup takes a tile of 16 NT pairs of
-// one expert and a range of that expert's 16-row blocks; operands and layouts
-// are those of the prompt product (k_gemm_pq2.hip), with each lane reading its
-// pair's activations at an address of its own.
+// and the runs are added in order.  A workgroup takes a tile of 16 pairs (32
+// where experts have many) of one expert and a range of that expert's 16-row
+// blocks; operands and layouts are those of the prompt product
+// (k_gemm_pq2.hip), with each lane reading its pair's activations at an address
+// of its own.
+//
+// Few pairs: bound by the codes.  One token's 8 experts of 2048 x 5120 take 8.8
+// us (22 MB, 4.3 at a large copy's rate, one launch 3.6), 48 tokens x 8 of 64
+// experts of 5120 x 1024 30 us (89 MB of codes, 19 at that rate).  Many pairs:
+// bound by the vector units, see below.
 //
 // Slots and tiles: lists.h.  Workgroups of slots without a tile end at once;
 // pairs without an expert get zeros.
@@ -22,39 +28,29 @@ namespace tq {
 namespace {
 
 constexpr int kMaxRuns = 4;  // waves per workgroup: the matrix-vector plan's runs
+constexpr int kTok = 16;     // pairs of a tile
 
 struct ExpertShape {
   int nrg;    // row ranges per tile of pairs
   int base;   // 16-row blocks per range: base, the first `extra` ranges one more
   int extra;
-  bool by_slot;
 };
 
 // A range's blocks are taken MRB at a time; the superchunks of all of them are one stream, RD of which are asked for ahead.
 //
-// Workgroups go to the XCDs in turn (id modulo 8).  by_slot: an XCD takes every eighth of the slots, one after the other, each with
-// all its row ranges: the ranges of a tile share its activations in that XCD's L2, and neighbouring tiles, mostly of one expert,
-// its codes.  Otherwise an XCD takes every eighth row range of all slots: what is read once is spread evenly, however the pairs
-// are spread over the experts.
-template <int NT, int RD, int MRB, bool LOOP>
-__global__ __launch_bounds__(64 * kMaxRuns, NT == 1 ? 2 : 1) void gemm_experts_kernel(tq_gemm_experts_args g, int64_t expert_bytes, int nsc, int spw,
-                                                                                     int slots, int slot0, bool places, ExpertShape gs) {
-  constexpr int kTok = 16 * NT;
-  constexpr int kAcc = MRB * NT * 4;
+// Workgroups go to the XCDs in turn (id modulo 8): each XCD takes every eighth row range of all slots, so that what is read once is
+// spread evenly, however the pairs are spread over the experts.
+template <int RD, int MRB, bool LOOP>
+__global__ __launch_bounds__(64 * kMaxRuns, 2) void gemm_experts_kernel(tq_gemm_experts_args g, int64_t expert_bytes, int nsc, int spw,
+                                                                        int slots, int slot0, bool places, ExpertShape gs) {
+  constexpr int kAcc = MRB * 4;
   extern __shared__ double sums[];
   __shared__ int pair_of[kTok];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), nruns = blockDim.x >> 6;
   const int l16 = lane & 15, qd = lane >> 4;
-  const int id = blockIdx.x;
-  int rg, local;
-  if (gs.by_slot) {
-    const int at = id / 8, share = (slots + 7) / 8;
-    rg = at % gs.nrg, local = id % 8 * share + at / gs.nrg;
-  } else {
-    const int rem = id % (8 * slots);
-    rg = id / (8 * slots) * 8 + rem % 8, local = rem / 8;
-  }
+  const int id = blockIdx.x, rem = id % (8 * slots);
+  const int rg = id / (8 * slots) * 8 + rem % 8, local = rem / 8;
   if (rg >= gs.nrg || local >= slots) return;
   const int slot = slot0 + local;
   const int pairs = (int)g.pairs, rows = (int)g.rows;
@@ -91,14 +87,12 @@ __global__ __launch_bounds__(64 * kMaxRuns, NT == 1 ? 2 : 1) void gemm_experts_k
   // Token t of a block of 16 sits in MFMA row 4 (t % 4) + t / 4.  Places without a pair read the first input and are not stored.
   const int trow = 4 * (l16 & 3) + (l16 >> 2);
   const int share = (int)(g.pairs / g.inputs);
-  const int8_t* qp[NT];
-#pragma unroll
-  for (int nb = 0; nb < NT; ++nb) qp[nb] = g.q + (int64_t)(max(0, pair_of[16 * nb + trow]) / share) * K + 16 * qd + 256 * sc0;
-  const float* dp = g.d + (int64_t)(max(0, pair_of[lane & (kTok - 1)]) / share) * nsc + sc0;
+  const int8_t* qp = g.q + (int64_t)(max(0, pair_of[trow]) / share) * K + 16 * qd + 256 * sc0;
+  const float* dp = g.d + (int64_t)(max(0, pair_of[l16]) / share) * nsc + sc0;
 
   v4u ra[RD][MRB];
   uint32_t rs[RD][MRB];
-  v4u rb[RD][NT][4];
+  v4u rb[RD][4];
   float rx[RD];
   const int groups = (blocks + MRB - 1) / MRB;
   int ahead_group = 0, ahead_k = 0;  // what is asked for next
@@ -109,9 +103,7 @@ __global__ __launch_bounds__(64 * kMaxRuns, NT == 1 ? 2 : 1) void gemm_experts_k
     const int sc = sc0 + ahead_k, first = ahead_group * MRB;
     if (acts) {
 #pragma unroll
-      for (int nb = 0; nb < NT; ++nb)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) rb[J][nb][c] = *reinterpret_cast<const v4u*>(qp[nb] + 256 * ahead_k + 64 * c);
+      for (int c = 0; c < 4; ++c) rb[J][c] = *reinterpret_cast<const v4u*>(qp + 256 * ahead_k + 64 * c);
       rx[J] = dp[ahead_k];
     }
 #pragma unroll
@@ -123,80 +115,61 @@ __global__ __launch_bounds__(64 * kMaxRuns, NT == 1 ? 2 : 1) void gemm_experts_k
     }
     if (++ahead_k == n) ahead_k = 0, ++ahead_group;
   };
-  double yacc[MRB][NT][4];
+  double yacc[MRB][4];
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MRB; ++i)
 #pragma unroll
-      for (int nb = 0; nb < NT; ++nb)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) yacc[i][nb][v] = 0.0;
+      for (int v = 0; v < 4; ++v) yacc[i][v] = 0.0;
   };
-  const int slots_used = NT == 1 ? (tile.count + 3) / 4 : 4;  // result slot v of a lane holds token 4 v + qd
-  int nrb = min(MRB, blocks);                                 // blocks of the present group
+  const int slots_used = (tile.count + 3) / 4;  // result slot v of a lane holds token 4 v + qd
+  int nrb = min(MRB, blocks);                   // blocks of the present group
 
   auto step = [&](int J) __attribute__((always_inline)) {
-    double xd[NT][4];
+    double xd[4];
     const int xi = __builtin_bit_cast(int, rx[J]);
 #pragma unroll
-    for (int nb = 0; nb < NT; ++nb)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) xd[nb][v] = (double)__builtin_bit_cast(float, __shfl(xi, 16 * nb + 4 * v + qd, 64)) * 0.015625;
+    for (int v = 0; v < 4; ++v) xd[v] = (double)__builtin_bit_cast(float, __shfl(xi, 4 * v + qd, 64)) * 0.015625;
 #pragma unroll
     for (int i = 0; i < MRB; ++i) {
       if (i >= nrb) continue;
-      v4i acc[NT][2];
-#pragma unroll
-      for (int nb = 0; nb < NT; ++nb) acc[nb][0] = acc[nb][1] = v4i{0, 0, 0, 0};
+      v4i acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const v4i w = expand64(ra[J][i][c]);
-#pragma unroll
-        for (int nb = 0; nb < NT; ++nb)
-          acc[nb][c >> 1] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, rb[J][nb][c]), w, acc[nb][c >> 1], 0, 0, 0);
+        acc[c >> 1] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, rb[J][c]), w, acc[c >> 1], 0, 0, 0);
       }
       const double d0 = lo_half(rs[J][i]), d1 = hi_half(rs[J][i]);
 #pragma unroll
-      for (int nb = 0; nb < NT; ++nb)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (NT == 1 && v >= slots_used) continue;  // uniform
-          const double inner = __builtin_fma(d1, (double)acc[nb][1][v], d0 * (double)acc[nb][0][v]);
-          yacc[i][nb][v] = __builtin_fma(xd[nb][v], inner, yacc[i][nb][v]);
-        }
+      for (int v = 0; v < 4; ++v) {
+        if (v >= slots_used) continue;  // uniform
+        const double inner = __builtin_fma(d1, (double)acc[1][v], d0 * (double)acc[0][v]);
+        yacc[i][v] = __builtin_fma(xd[v], inner, yacc[i][v]);
+      }
     }
   };
 
-  // The runs of a group added in run order; phases bound the LDS.
-  constexpr int kPh = kAcc > 20 ? 2 : 1, kPer = kAcc / kPh;
-  static_assert(kAcc % kPh == 0, "phases split the slots evenly");
+  // The runs of a group added in run order.
   auto finish = [&](int group) __attribute__((always_inline)) {
+    if (group > 0) __syncthreads();  // the sums before are read
 #pragma unroll
-    for (int p = 0; p < kPh; ++p) {
-      if (p > 0 || group > 0) __syncthreads();  // the sums before are read
+    for (int i = 0; i < MRB; ++i)
 #pragma unroll
-      for (int i = 0; i < MRB; ++i)
+      for (int v = 0; v < 4; ++v)
+        if (v < slots_used) sums[((size_t)wave * kAcc + 4 * i + v) * 64 + lane] = yacc[i][v];
+    __syncthreads();
+    for (int sl = wave; sl < kAcc; sl += nruns) {
+      const int i = sl / 4, v = sl % 4;
+      if (i >= nrb || v >= slots_used) continue;
+      double rv[kMaxRuns];
 #pragma unroll
-        for (int nb = 0; nb < NT; ++nb)
+      for (int w = 0; w < kMaxRuns; ++w) rv[w] = sums[((size_t)min(w, nruns - 1) * kAcc + sl) * 64 + lane];
+      double t = rv[0];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int sl = (i * NT + nb) * 4 + v;
-            if (sl / kPer == p && v < slots_used) sums[((size_t)wave * kPer + sl % kPer) * 64 + lane] = yacc[i][nb][v];
-          }
-      __syncthreads();
-      for (int sl = p * kPer + wave; sl < (p + 1) * kPer; sl += nruns) {
-        const int i = sl / (NT * 4), nb = (sl / 4) % NT, v = sl % 4;
-        if (i >= nrb || v >= slots_used) continue;
-        double rv[kMaxRuns];
-#pragma unroll
-        for (int w = 0; w < kMaxRuns; ++w) rv[w] = sums[((size_t)min(w, nruns - 1) * kPer + sl % kPer) * 64 + lane];
-        double t = rv[0];
-#pragma unroll
-        for (int w = 1; w < kMaxRuns; ++w)
-          if (w < nruns) t += rv[w];
-        const int row = (b0 + group * MRB + i) * 16 + l16, pr = pair_of[16 * nb + 4 * v + qd];
-        if (row < rows && pr >= 0) g.y[(int64_t)pr * rows + row] = (float)t;
-      }
+      for (int w = 1; w < kMaxRuns; ++w)
+        if (w < nruns) t += rv[w];
+      const int row = (b0 + group * MRB + i) * 16 + l16, pr = pair_of[4 * v + qd];
+      if (row < rows && pr >= 0) g.y[(int64_t)pr * rows + row] = (float)t;
     }
   };
 
@@ -232,30 +205,27 @@ __global__ __launch_bounds__(64 * kMaxRuns, NT == 1 ? 2 : 1) void gemm_experts_k
   }
 }
 
-template <int NT, int RD, int MRB, bool LOOP>
-hipError_t launch_t(const tq_gemm_experts_args& g, int64_t tiles, int64_t work, hipStream_t s) {
+template <int RD, int MRB, bool LOOP>
+hipError_t launch_t(const tq_gemm_experts_args& g, int64_t active, int64_t work, hipStream_t s) {
   const Dims dm = dims(g.rows, g.cols);
   const int64_t expert_bytes = pq2_code_bytes(dm) + pq2_scale_bytes(dm);
-  const int size = 16 * NT;
   ExpertShape gs;
-  const Slots slots = list_slots(g.pairs, g.experts, size);
+  const Slots slots = list_slots(g.pairs, g.experts, kTok);
   // Row ranges: about `work` workgroups with a tile, at most 64 blocks each (a range's codes stay within a buffer's 2^31 bytes)
   const int64_t nblk = 4 * dm.ntiles;
   const int64_t most_blocks = LOOP ? 64 : MRB;
-  const int64_t want = std::max((nblk + most_blocks - 1) / most_blocks, std::min(nblk, (work + tiles - 1) / tiles));
+  const int64_t want = std::max((nblk + most_blocks - 1) / most_blocks, std::min(nblk, (work + active - 1) / active));
   gs.nrg = (int)want;
   gs.base = (int)(nblk / want), gs.extra = (int)(nblk % want);
-  gs.by_slot = NT > 1;
   const GemvPlan p = plan_gemv_pq2(dm, false);  // the runs of the matrix-vector product
   const int nruns = (int)((dm.nsc + p.spw - 1) / p.spw);
-  constexpr int kAcc = MRB * NT * 4;
-  const size_t lds = (size_t)nruns * (kAcc > 20 ? kAcc / 2 : kAcc) * 64 * 8;
+  const size_t lds = (size_t)nruns * MRB * 4 * 64 * 8;
   // at most 2^22 workgroups per launch, as in the prompt product
   const int64_t most = std::max<int64_t>(8, (int64_t(1) << 22) / gs.nrg / 8 * 8);
   for (int64_t s0 = 0; s0 < slots.count; s0 += most) {
     const int64_t now = std::min(most, slots.count - s0);
-    const int64_t grid = gs.by_slot ? (now + 7) / 8 * 8 * gs.nrg : (gs.nrg + 7) / 8 * 8 * now;
-    hipLaunchKernelGGL((gemm_experts_kernel<NT, RD, MRB, LOOP>), dim3((unsigned)grid), dim3(64 * nruns), lds, s, g, expert_bytes, (int)dm.nsc, p.spw, (int)now,
+    const int64_t grid = (gs.nrg + 7) / 8 * 8 * now;
+    hipLaunchKernelGGL((gemm_experts_kernel<RD, MRB, LOOP>), dim3((unsigned)grid), dim3(64 * nruns), lds, s, g, expert_bytes, (int)dm.nsc, p.spw, (int)now,
                        (int)s0, slots.places, gs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -265,14 +235,17 @@ hipError_t launch_t(const tq_gemm_experts_args& g, int64_t tiles, int64_t work, 
 
 // ---- many pairs of one expert ----
 //
-// A workgroup's eight waves take up to 512 rows (kWideBlocks 16-row blocks each) and the same 32 pairs, so that these pairs'
-// activations come from memory once for 512 rows: with a wave per run of columns (the kernel above) they come once for 80, which
-// took half of its time.  Superchunk after superchunk the activations are staged in LDS in the order of the matrix
-// instructions' operands, one ahead of the products; a wave's codes are asked for one superchunk ahead in registers.  A wave goes
-// through all runs of the matrix-vector product in turn; the sum of those before waits in LDS.
+// A workgroup's four waves take up to 256 rows (kWideBlocks 16-row blocks each) and the same 32 pairs, so that these pairs'
+// activations come from memory once for 256 rows: with a wave per run of columns (the kernel above) they come once for 48.
+// Superchunk after superchunk the activations are staged in LDS in the order of the matrix instructions' operands, one ahead of the
+// products; a wave's codes are asked for one superchunk ahead in registers.  A wave goes through all runs of the matrix-vector
+// product in turn; the sum of those before waits in LDS.  An XCD takes an eighth of the slots, one after the other, each with all
+// its row ranges: the ranges of a tile share its activations in that XCD's L2, and neighbouring tiles, mostly of one expert, its codes.
 //
-// Bound by the vector units: per 16 rows, 32 pairs and superchunk 28 instructions expand the codes, 40 make the fp64 sums, and 8
-// matrix instructions of 16 cycles run beside them.
+// Bound by the vector units: per 16 rows, 32 pairs and superchunk 28 instructions expand the codes, 40 make the fp64 sums (5 to 6
+// cycles each with two waves per SIMD), and 8 matrix instructions of 16 cycles run beside them.  2048 tokens x 4 of 32 experts of
+// 2048 x 5120: 190 us, vector units 56 % and matrix units 20 % busy.  (Eight waves of 2 blocks, four per SIMD: 216, more reads of
+// the staged operands and 4 spilled registers; eight waves of 4 blocks, one workgroup per compute unit: 206.)
 constexpr int kWideWaves = 4;
 constexpr int kPieces = 8 / kWideWaves;  // 16-byte pieces of a superchunk that a thread stages
 constexpr int kWideBlocks = 4;
@@ -467,7 +440,6 @@ hipError_t launch_wide(const tq_gemm_experts_args& g, hipStream_t s) {
   const int64_t nblk = (dm.rows + 15) / 16;
   gs.nrg = (int)((nblk + kWideWaves * kWideBlocks - 1) / (kWideWaves * kWideBlocks));
   gs.base = (int)(nblk / gs.nrg), gs.extra = (int)(nblk % gs.nrg);
-  gs.by_slot = true;
   const GemvPlan p = plan_gemv_pq2(dm, false);
   const int each = (int)((gs.base + (gs.extra > 0) + kWideWaves - 1) / kWideWaves);
   const size_t lds = 2 * kWideStage + 2 * kWideTok * 8 + ((size_t)each * 8 - 1) * 64 * kWideWaves * 8;
@@ -487,11 +459,15 @@ hipError_t launch_wide(const tq_gemm_experts_args& g, hipStream_t s) {
 
 hipError_t launch_gemm_experts_pq2(const tq_gemm_experts_args& g, hipStream_t s) {
   const int64_t active = std::min<int64_t>(g.experts, g.pairs);
-  const int64_t nblk = (g.rows + 15) / 16;
-  if (g.pairs > 24 * active && nblk >= 16) return launch_wide(g, s);
-  if (g.pairs > 24 * active) return launch_t<2, 2, 5, false>(g, g.pairs / 32 + active, 512, s);
-  if (nblk * active > 1536) return launch_t<1, 1, 3, true>(g, active, 1024, s);
-  return launch_t<1, 2, 3, false>(g, active, 512, s);
+  const int64_t work = (g.rows + 15) / 16 * active;  // 16-row blocks of the experts that can have a pair
+  // Many pairs per expert.  wide / up to 48 rows per workgroup, us: 32 pairs per expert of 2048 x 5120 68 / 58, of 2048 x 2048 27 / 22;
+  // 48 pairs 71 / 83; 64 pairs 28 / 36 (2048 x 2048); 256 pairs 187 / 341, of 192 x 5120 41 / 108, of 128 x 1024 13 / 23.
+  if (g.pairs > 40 * active) return launch_wide(g, s);
+  // A workgroup for several groups of 48 rows, which the tile's activations and its start are shared by, where there are many
+  // blocks or each run is one superchunk.  Several / one, us: 20480 blocks 30 / 45 (1024 columns), 50 / 67 (2048); 8192 blocks
+  // 16 / 22 (1024), 46 / 48 (5120); 4096 blocks 55 / 44 (5120); 2048 blocks 8.6 / 9.6 (1024), 17 / 15 (2048).
+  if (work > (g.cols <= 256 * kMaxRuns ? 1536 : 6144)) return launch_t<1, 3, true>(g, active, 1024, s);
+  return launch_t<2, 3, false>(g, active, 512, s);
 }
 
 }  // namespace tq

@@ -170,6 +170,21 @@ def test_gemm_experts_of_many_experts(tq):
         assert torch.equal(y[t], whole[t, ids[t].long().cuda()])
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 256), (17, 1280), (64, 1024), (100, 2304), (257, 512), (300, 5120), (700, 1024)])
+@pytest.mark.parametrize("tokens,k,n", [(40, 1, 1), (41, 1, 1), (81, 1, 2), (60, 2, 3), (61, 2, 3), (200, 3, 3), (48, 8, 64)])
+def test_gemm_experts_where_kernels_change(tq, rows, cols, tokens, k, n):
+    """Every pair, bit for bit, at the sides of the rules that choose a kernel."""
+    g = np.random.default_rng(rows + cols + tokens)
+    w = torch.stack([tq.repack(torch.from_numpy(TI.pq2_matrix(g, rows, cols).reshape(-1)).cuda(), "pq2_0", rows, cols) for _ in range(n)])
+    q, d, bs = tq.quantize_q8k(torch.randn(tokens, cols, generator=gen(tokens)).cuda())
+    ids = torch.stack([torch.randperm(n, generator=gen(t))[:k] for t in range(tokens)]).int()
+    ids[torch.rand(tokens, k, generator=gen(1)) < 0.02] = -1
+    y = tq.gemm_experts("pq2_0", w, rows, cols, q, d, *tq.expert_lists(ids.cuda(), n)).view(tokens, k, rows)
+    whole = torch.stack([tq.gemm("pq2_0", w[e], rows, cols, q, d, bs) for e in range(n)] + [torch.zeros(tokens, rows, device="cuda")])
+    at = torch.where(ids < 0, n, ids).long().cuda()
+    assert torch.equal(y, whole[at, torch.arange(tokens, device="cuda")[:, None]])
+
+
 def rows_match(tq, x, u, **params):
     got = tq.sample(x.cuda(), u.cuda(), **{k: v.cuda() for k, v in params.items()}).cpu()
     off = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
