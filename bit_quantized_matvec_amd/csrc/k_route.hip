@@ -12,13 +12,17 @@
 //     lowest lane), which is then taken out.
 //   * groups: c of all experts in LDS; lane g sums the group's largest; ranks
 //     of groups by counting those worth more.
-// Bound by latency for few tokens, by instructions for many (two fp64
-// exponentials' worth per score, some 50 instructions per round).
+// Bound by latency for few tokens (one token of 64 experts 2.9 us), by
+// instructions for many (an fp64 exponential and a division per score, some 50
+// instructions per round): 4099 tokens of 256 experts with groups 13 us, vector
+// units 67 % busy, 2 MB read.
 //
 // expert_lists: one workgroup per expert reads every id and writes that
 // expert's pairs in their order: no atomics, so the lists do not depend on
 // timing.  Each wave has a contiguous share of the pairs, counts those below
-// and those of its expert, and, after one exchange, writes.
+// and those of its expert, and, after one exchange, writes.  32792 pairs of 256
+// experts 11 us, a chain of reads, an exchange and the reads again (with ids
+// read one per lane and counted by ballots 22).
 #include <algorithm>
 
 #include "batch.h"

@@ -23,6 +23,12 @@
 //   pick_kernel, one per row: finds K and j among them (by 1024 digits of the
 //     keys' range at a time), adds up what stays per slice, and draws: the
 //     slice, then the token in it.
+// One row of 131072: 6.2, 7.4, 4.4 and 13 us, latencies of one workgroup in the
+// second and the fourth.  256 rows of 200003 in bf16 with top-p 137 us: 72, 12,
+// 30 and 30; the first two kernels over the logits (102 MB, 20 us at a large
+// copy's rate) are bound by the vector units: some 30 instructions per
+// logit, half of them fp64, in the first, 10 in the list.
+//
 // Where a slice has too many of them (a flat row), pick_kernel searches the
 // whole row instead (search_row: a radix descent over the keys).
 //

@@ -115,14 +115,14 @@ def test_other_streams(tq):
 def test_used_workspaces(tq):
     """Workspaces need no clearing, and a larger one serves smaller calls and other shapes."""
     r = gen(4)
-    ws = torch.full((max(tq.sample_workspace_bytes(40, 200_000), tq.adapter_workspace_bytes(1500, 7, 64, 1024)),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(tq.sample_workspace_bytes(40, 200_000), tq.adapter_workspace_bytes(2100, 7, 64, 1024)),), 255, dtype=torch.uint8, device="cuda")
     for rows, vocab in ((40, 200_000), (3, 500), (40, 200_000), (1, 70_000), (17, 9_000)):
         x, u, k = torch.randn(rows, vocab, generator=r).cuda(), torch.rand(rows, generator=r).cuda(), torch.full((rows,), 30, dtype=I32, device="cuda")
         p = torch.full((rows,), 0.8, device="cuda")
         args = dict(top_k=k, top_p=p, out=torch.empty(rows, dtype=I32, device="cuda"))
         first = tq.sample(x, u, **args, ws=ws).clone()
         assert torch.equal(first, tq.sample(x, u, top_k=k, top_p=p)) and torch.equal(first, tq.sample(x, u, **args, ws=ws))
-    for tokens in (1500, 2, 64, 65, 1023, 1024):
+    for tokens in (2100, 2, 64, 65, 2047, 2048):
         y, x = torch.randn(tokens, 90, generator=r).cuda(), torch.randn(tokens, 1024, generator=r).cuda()
         a, b = torch.randn(7, 64, 1024, generator=r).to(HF).cuda(), torch.randn(7, 90, 64, generator=r).to(HF).cuda()
         index = torch.randint(-1, 7, (tokens,), generator=r, dtype=I32).cuda()
@@ -131,7 +131,7 @@ def test_used_workspaces(tq):
         ws.fill_(255)
 
 
-@pytest.mark.parametrize("tokens", [1, 15, 16, 17, 63, 64, 65, 129, 1023, 1024, 1025])
+@pytest.mark.parametrize("tokens", [1, 15, 16, 17, 63, 64, 65, 129, 1025, 2047, 2048, 2049])
 @pytest.mark.parametrize("n", [1, 70])
 def test_adapter_add_where_kernels_change(tq, tokens, n):
     r = gen(tokens + n)
