@@ -451,6 +451,7 @@ int tq_gemm_experts(const tq_gemm_experts_args *args, void *stream);
  * stride), and may not overlap it otherwise.
  * x_type fp32 or w_type; w_type bf16 or fp16; out has y's type.  Products are
  * exact to 24 bits of both factors, sums and A x fp32, one rounding at the end.
+ * An x that is not finite makes its own token's result not finite (of either kind).
  * cols and rank multiples of 8 (rank up to 256); x, a and b 16-byte aligned and
  * x_stride a multiple of 16 bytes; rows, y_stride and out_stride are free.
  * workspace: tq_adapter_workspace_bytes, needs no clearing; not nullable. */
