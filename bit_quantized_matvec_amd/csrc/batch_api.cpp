@@ -71,6 +71,7 @@ int adapter_status(const tq_adapter_add_args& a) {
   if (st != TQ_OK) return st;
   if (a.rows < 1 || a.rows > kMaxRows || !stride_ok(a.x_stride) || !stride_ok(a.y_stride) || !stride_ok(a.out_stride)) return TQ_ERR_SHAPE;
   if (a.out == a.y && a.out_stride != a.y_stride) return TQ_ERR_SHAPE;
+  if (a.tokens > 1 && a.out_stride < a.rows && a.out_stride > -a.rows) return TQ_ERR_SHAPE;  // rows that overlap
   if (a.tokens == 0) return TQ_OK;
   if (!a.x || !a.y || !a.a || !a.b || !a.out || !a.index || !a.workspace) return TQ_ERR_NULL;
   const int ye = bytes_of(a.y_type);

@@ -448,7 +448,7 @@ int tq_gemm_experts(const tq_gemm_experts_args *args, void *stream);
  * for index[t] >= adapters).  Adapter i uses the first ranks[i] rows of A_i and
  * columns of B_i (ranks NULL: all; clamped to [0, rank]); what lies behind them
  * is not used, whatever it holds.  scale NULL: 1.  out may be y itself (same
- * stride), and may not overlap it otherwise.
+ * stride), and may not overlap it otherwise; its own rows may not overlap.
  * x_type fp32 or w_type; w_type bf16 or fp16; out has y's type.  Products are
  * exact to 24 bits of both factors, sums and A x fp32, one rounding at the end.
  * An x that is not finite makes its own token's result not finite (of either kind).

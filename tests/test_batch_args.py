@@ -124,6 +124,13 @@ def test_adapter_add_refuses_shapes(tq, over, status):
     refuses(tq.TQError, tq.adapter_add, ADAPT, over, status)
 
 
+@pytest.mark.parametrize("stride", [1, 9])
+def test_adapter_add_refuses_rows_that_overlap(tq, stride):
+    y = fake(40).as_strided((3, 10), (stride, 1))
+    refuses(tq.TQError, tq.adapter_add, ADAPT, dict(out=y), -2)
+    refuses(tq.TQError, tq.adapter_add, ADAPT, dict(y=y, out=None), -2)
+
+
 def test_adapter_add_in_place_needs_one_stride(tq):
     y = fake(3, 20)
     refuses(tq.TQError, tq.adapter_add, ADAPT, dict(y=y[:, :10], out=y.view(6, 10)[:3]), -2)
