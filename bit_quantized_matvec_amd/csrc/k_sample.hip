@@ -40,6 +40,7 @@
 
 #include "batch.h"
 #include "lanes.h"
+#include "sample_bins.h"
 #include "seq.h"
 
 namespace tq {
@@ -49,8 +50,6 @@ constexpr int kMaxWaves = 16;
 constexpr int kPer = 16;     // logits of a thread of the slices' kernels
 constexpr int kPickThreads = 1024;
 constexpr int kPlanShares = 4;
-constexpr int kBins = 256;   // of 1 / kPerUnit
-constexpr int kPerUnit = 8;
 constexpr int kShare = 1024;  // places of a slice in its row's list
 constexpr int kMaxSlices = 65;
 constexpr int kNear = 4096;  // places of the list that are kept in LDS
@@ -113,11 +112,6 @@ struct Scale {
   // A number up to 1 as a whole number of 2^-43: the low bits of its sum with 2^52
   __device__ static uint64_t units(double e) { return __builtin_bit_cast(uint64_t, __builtin_fma(e, (double)kOne, 0x1p52)) & ((uint64_t(1) << 52) - 1); }
 };
-
-// The bin of a logit, increasing with x and the same for every slice: floor(8 x / T), off by one at most for the rounding of
-// the product.  What lies further from 0 than kFar shares a bin (and is searched otherwise if the cuts lie there).
-constexpr float kFar = 0x1p23f;
-__device__ inline int bin_of(float x, float per) { return (int)__builtin_floorf(__builtin_amdgcn_fmed3f(x * per, -kFar, kFar)); }
 
 // ---- the workspace ----
 
@@ -243,7 +237,7 @@ __device__ inline Request request(const tq_sample_args& a, int64_t r) {
   const float t = a.temperature ? t0 : 1.0f;
   q.greedy = !(t > 0.0f);
   q.inv_t = q.greedy ? 1.0 : 1.0 / (double)t;
-  q.per = (float)fmin(kPerUnit * q.inv_t, 0x1p100);
+  q.per = bins_per(q.inv_t);
   q.top_k = a.top_k ? k0 : 0;
   q.top_p = a.top_p ? (double)p0 : 1.0;
   const double m = a.min_p && !q.greedy ? (double)m0 : 0.0;
@@ -318,7 +312,7 @@ __global__ __launch_bounds__(1024) void bins_kernel(tq_sample_args a, Space ws) 
 #pragma unroll
         for (int i = 0; i < kSide; ++i) {
           // (64 logits in one bin queue for 128 cycles, in 16 bins for 20, in 64 for 13)
-          if (x[i0 + i] > -INFINITY && b[i] < kBins) {
+          if (x[i0 + i] > -INFINITY && (unsigned)b[i] < kBins) {
             atomicAdd(&sh.mass[b[i]], (unsigned long long)w[i]);
             if (q.use_k) atomicAdd(&sh.count[b[i]], 1u);
           }
@@ -392,7 +386,7 @@ __global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_arg
   if (tid < ws.slices) {
     const bool some = mine.most > -INFINITY;
     sh.scale[tid] = some ? sc.e(mine.most) / (double)kOne : 0.0;
-    sh.shift[tid] = some ? min(top - bin_of(mine.most, q.per), kBins) : kBins;
+    sh.shift[tid] = some ? bins_below(top, bin_of(mine.most, q.per)) : kBins;
   }
   __syncthreads();
   {
@@ -472,7 +466,7 @@ __global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_arg
     // z = log(min_p): the difference of two logits' bins is off by one, and by two more for roundings
     const int b = (int)fmin(-log(q.min_p) * kPerUnit, 1e6);
     row.m0 = max(0, b - 3), row.m1 = b + 3;
-    if (!(fabsf(best * q.per) < kFar)) row.m0 = 0, row.m1 = kBins;
+    if (!(fabsf(best * q.per) < kFar) || q.inv_t == 0.0) row.m0 = 0, row.m1 = kBins;
   }
   if (lane == 0) ws.rows[r] = row;
 }
@@ -797,7 +791,7 @@ __global__ __launch_bounds__(1024) void list_kernel(tq_sample_args a, Space ws) 
   const auto collect = [&](auto one_range) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const float v = __builtin_amdgcn_fmed3f(x[i] * q.per, -kFar, kFar);
+      const float v = bin_place(x[i], q.per);
       bool ok = v >= low && v < high && x[i] > -INFINITY;
       if constexpr (!decltype(one_range)::value) {
         if (!ok) continue;
@@ -850,7 +844,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
   if (tid < ws.slices) {
     const float most = ws.parts[r * ws.slices + tid].most;
     const bool some = most > -INFINITY;
-    sh.slice_shift[tid] = some ? min(row.top_bin - bin_of(most, q.per), kBins) : kBins;
+    sh.slice_shift[tid] = some ? bins_below(row.top_bin, bin_of(most, q.per)) : kBins;
     sh.slice_most[tid] = most;
     sh.slice_mass[tid] = 0, sh.slice_ties[tid] = 0;
     sh.share[tid + 1] = any_cut(row) ? ws.shares[r * ws.slices + tid] : 0;

@@ -1,0 +1,66 @@
+"""The operators of a mixed batch at the ends of their ranges: temperatures without measure, random numbers at the borders, scales and
+inputs next to infinity, lists that decrease, and workspaces of exactly a larger call's size."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import batch_oracle as bo
+import tq_inputs as TI
+
+pytestmark = pytest.mark.gpu
+
+F32, BF, HF, I32 = torch.float32, torch.bfloat16, torch.float16, torch.int32
+
+
+@pytest.fixture(scope="module")
+def tq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_quantized_matvec_amd as m
+
+    return m
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def rows_match(tq, x, u, **params):
+    got = tq.sample(x.cuda(), u.cuda(), **{k: v.cuda() for k, v in params.items()}).cpu()
+    off = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
+    want = [bo.sample(x[i].double(), float(u[i]), *(params[k][i].item() if k in params else v for k, v in off.items())) for i in range(x.shape[0])]
+    assert got.tolist() == [w[0] for w in want]
+
+
+# ---- temperatures without an end -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("vocab", [40, 3000, 5 * 4096, 70_000])
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+def test_sample_at_infinite_temperature(tq, vocab, dt):
+    """All finite logits weigh the same, and nothing beside one of +inf, which lies in one slice, in several or in none."""
+    r = gen(vocab)
+    rows = 8
+    x = torch.randn(rows, vocab, generator=r) * 4
+    x[1, vocab // 2] = math.inf
+    x[2, :: vocab // 4] = math.inf
+    x[3, 0] = x[3, -1] = math.inf
+    x[4] = math.inf
+    x[5, : vocab // 2] = -math.inf
+    x[6, ::3] = torch.finfo(dt).max
+    x[6, 1::3] = torch.finfo(dt).min
+    x[7, 5:] = math.nan
+    x = x.to(dt)
+    u = torch.rand(rows, generator=r)
+    t = torch.full((rows,), math.inf)
+    k = torch.full((rows,), 3, dtype=I32)
+    many = torch.full((rows,), vocab // 2, dtype=I32)
+    p, m = torch.full((rows,), 0.7), torch.tensor([1.0, 0.5] * (rows // 2))
+    for params in (dict(), dict(top_k=k), dict(top_k=many), dict(top_p=p), dict(min_p=m), dict(top_k=many, top_p=p, min_p=m)):
+        rows_match(tq, x, u, temperature=t, **params)
+    # in one launch with others
+    mixed = torch.tensor([math.inf, 1.0, 0.0, math.inf, 1e30, 1e-30, math.inf, 0.5])
+    rows_match(tq, x, u, temperature=mixed, top_k=k, top_p=p, min_p=m)
