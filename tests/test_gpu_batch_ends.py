@@ -64,3 +64,23 @@ def test_sample_at_infinite_temperature(tq, vocab, dt):
     # in one launch with others
     mixed = torch.tensor([math.inf, 1.0, 0.0, math.inf, 1e30, 1e-30, math.inf, 0.5])
     rows_match(tq, x, u, temperature=mixed, top_k=k, top_p=p, min_p=m)
+
+
+# ---- min_p where bins do not measure z -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("vocab", [300, 3000, 20_000])
+@pytest.mark.parametrize("t", [1e-30, 6e-30, 7e-30, 1e-32, 1e-36])
+def test_sample_min_p_at_small_temperatures(tq, t, vocab):
+    """Twenty tokens that pass min_p, and all others below it with a weight that would move the draw."""
+    r = gen(vocab)
+    rows = 48
+    z = -1.4 - 3.5 * torch.rand(rows, vocab, generator=r)
+    some = torch.rand(rows, vocab, generator=r).argsort(1)[:, :20]
+    z.scatter_(1, some, -1.1 * torch.rand(rows, 20, generator=r))
+    z.scatter_(1, some[:, :1], 0.0)
+    x = (z.double() * t).float()
+    u = (torch.arange(rows) + 0.5) / rows
+    params = dict(temperature=torch.full((rows,), t), min_p=torch.full((rows,), 0.3))
+    rows_match(tq, x, u, **params)
+    rows_match(tq, x, u, **params, top_p=torch.full((rows,), 0.99))
+    rows_match(tq, x, u, **params, top_k=torch.full((rows,), 30, dtype=I32))
