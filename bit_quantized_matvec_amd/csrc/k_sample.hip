@@ -466,7 +466,7 @@ __global__ __launch_bounds__(kBins * kPlanShares) void plan_kernel(tq_sample_arg
     // z = log(min_p): the difference of two logits' bins is off by one, and by two more for roundings
     const int b = (int)fmin(-log(q.min_p) * kPerUnit, 1e6);
     row.m0 = max(0, b - 3), row.m1 = b + 3;
-    if (!(fabsf(best * q.per) < kFar) || !bins_measure(q.inv_t)) row.m0 = 0, row.m1 = kBins;
+    if (!bins_measure(best, q.per, q.inv_t)) row.m0 = 0, row.m1 = kBins;
   }
   if (lane == 0) ws.rows[r] = row;
 }

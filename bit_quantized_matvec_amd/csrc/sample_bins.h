@@ -19,8 +19,6 @@ constexpr int kPerUnit = 8;
 // Bins of a unit of x.  Never 0, also where 1 / temperature is (then +inf * 0 would have no bin): 2^-126 takes finite logits
 // into the 8 bins around 0 and +inf behind them.
 TQ_BOTH inline float bins_per(double inv_t) { return (float)fmax(fmin(kPerUnit * inv_t, 0x1p100), 0x1p-126); }
-// Whether the difference of two bins is one of z: not where bins_per is held at an end.
-TQ_BOTH inline bool bins_measure(double inv_t) { return kPerUnit * inv_t <= 0x1p100 && kPerUnit * inv_t >= 0x1p-126; }
 
 // The bin of a logit that is a number: floor(8 x / T), off by one at most for the rounding of the product.  What lies further
 // from 0 than kFar shares a bin (and is searched otherwise if the cuts lie there).
@@ -34,6 +32,12 @@ TQ_BOTH inline float bin_place(float x, float per) {
 #endif
 }
 TQ_BOTH inline int bin_of(float x, float per) { return (int)floorf(bin_place(x, per)); }
+
+// Whether distances of up to kBins from the bin of `best` are distances in z: not where bins_per is held at an end, nor where
+// `best`, or what lies kBins below it, shares the bins at the ends.
+TQ_BOTH inline bool bins_measure(float best, float per, double inv_t) {
+  return kPerUnit * inv_t <= 0x1p100 && kPerUnit * inv_t >= 0x1p-126 && best * per < kFar && best * per > 2 * kBins - kFar;
+}
 
 // How far below `top` a bin lies: 0 to kBins, the last for all that are further down.  It is an index: held from both sides.
 TQ_BOTH inline int bins_below(int top, int bin) {

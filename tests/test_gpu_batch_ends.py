@@ -84,3 +84,19 @@ def test_sample_min_p_at_small_temperatures(tq, t, vocab):
     rows_match(tq, x, u, **params)
     rows_match(tq, x, u, **params, top_p=torch.full((rows,), 0.99))
     rows_match(tq, x, u, **params, top_k=torch.full((rows,), 30, dtype=I32))
+
+
+@pytest.mark.parametrize("bins", [3, 48, 200, 500])
+def test_sample_min_p_at_far_negative_logits(tq, bins):
+    """The largest logit lies `bins` eighths of z above where bins end, at -2^23 eighths."""
+    r = gen(bins)
+    rows, vocab, t = 48, 3000, 1e-4
+    best = -(2.0**23 - bins) / 8 * t
+    low = min(bins / 8 + 1, 8.0)
+    z = -low - 0.2 - 2 * torch.rand(rows, vocab, generator=r)
+    some = torch.rand(rows, vocab, generator=r).argsort(1)[:, :20]
+    z.scatter_(1, some, -(low - 0.2) * torch.rand(rows, 20, generator=r))
+    z.scatter_(1, some[:, :1], 0.0)
+    x = (best + z.double() * t).float()  # (z in steps of 0.08)
+    u = (torch.arange(rows) + 0.5) / rows
+    rows_match(tq, x, u, temperature=torch.full((rows,), t), min_p=torch.full((rows,), math.exp(-low)))
