@@ -944,8 +944,10 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(tq_sample_args a, Sp
     sure = min(cut_bin, row.m0);
     for (int s = tid; s < ws.slices && sure > 0; s += blockDim.x) {
       const int b = min(sure, kBins) - 1 - sh.slice_shift[s];
+      // (a slice whose largest weighs no unit of the row's has nothing that the draw in it could find)
+      const double e = sc.e(sh.slice_most[s]);
       double m = 0;
-      if (b >= 0) m = (double)ws.mass[(r * ws.slices + s) * kBins + b] * sc.e(sh.slice_most[s]);
+      if (b >= 0 && Scale::units(e) > 0) m = (double)ws.mass[(r * ws.slices + s) * kBins + b] * e;
       sh.slice_sum[s] = m;
     }
     // what is in question: the cut's bin, and those of min_p above it

@@ -100,3 +100,28 @@ def test_sample_min_p_at_far_negative_logits(tq, bins):
     x = (best + z.double() * t).float()  # (z in steps of 0.08)
     u = (torch.arange(rows) + 0.5) / rows
     rows_match(tq, x, u, temperature=torch.full((rows,), t), min_p=torch.full((rows,), math.exp(-low)))
+
+
+# ---- what weighs nothing is not drawn ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("low", [-30.0, -31.0, -31.75, -33.0])
+def test_sample_slices_that_weigh_nothing(tq, low, dt):
+    """The first and the last slices hold one token `low` below the largest and nothing else.  Tokens below 2^-44 of the largest
+    (z = -30.5) weigh nothing, wherever the row is cut."""
+    vocab = 5 * 4096
+    x = torch.full((vocab,), -200.0)
+    x[[10, 4096 + 20, 3 * 4096 + 30, vocab - 5]] = low
+    x[2 * 4096 + torch.arange(3) * 1000] = torch.tensor([-1.0, 0.0, -2.0])
+    u = torch.tensor([0.0, -1.0, math.nan, -math.inf, 1.0, 2.0, math.inf])
+    first, last = (10, vocab - 5) if low > -30.5 else (2 * 4096, 2 * 4096 + 2000)
+    want = torch.tensor([first] * 4 + [last] * 3, dtype=I32)
+    n = len(u)
+    full = lambda v, t=F32: torch.full((n,), v, dtype=t, device="cuda")  # noqa: E731
+    for params in (dict(), dict(temperature=full(1.0)), dict(top_k=full(7, I32)), dict(top_k=full(6000, I32)), dict(min_p=full(1e-30))):
+        logprob = torch.empty(n, device="cuda")
+        got = tq.sample(x.to(dt).repeat(n, 1).cuda(), u.cuda(), logprob=logprob, **params).cpu()
+        assert torch.equal(got, want), params
+        assert bool(logprob.isfinite().all())
+    cold = (x * 0.25).to(dt).repeat(n, 1).cuda()
+    assert torch.equal(tq.sample(cold, u.cuda(), temperature=full(0.25)).cpu(), want)
