@@ -47,9 +47,11 @@ constexpr int kExpandWaves = 4;
 constexpr int kFeat = 64;        // features per wave of expand
 constexpr int kMaxSplits = 8;
 
-// 8 values as TERMS bf16 vectors.  A term that is not finite leaves nothing behind it.
+// 8 values as TERMS (2 or 3) bf16 vectors.  The first term is held at bf16's largest, so that fp32 values above it, which would be
+// rounded to infinity, leave the rest to the second; so do infinities and NaN, and nothing is left behind a term that is not finite.
 template <int TERMS>
 __device__ inline void terms8(const float* p, b8* out) {
+  constexpr float kMost = 0x1.FEp127f;
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = p[i];
@@ -58,12 +60,13 @@ __device__ inline void terms8(const float* p, b8* out) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = pack2<bf16>(x[2 * i], x[2 * i + 1]);
+      w[i] = t == 0 ? pack2<bf16>(__builtin_amdgcn_fmed3f(x[2 * i], -kMost, kMost), __builtin_amdgcn_fmed3f(x[2 * i + 1], -kMost, kMost))
+                    : pack2<bf16>(x[2 * i], x[2 * i + 1]);
       if (t + 1 < TERMS) {
         float u, v;
         unpack2<bf16>(w[i], &u, &v);
-        x[2 * i] = fabsf(u) < INFINITY ? x[2 * i] - u : 0.0f;
-        x[2 * i + 1] = fabsf(v) < INFINITY ? x[2 * i + 1] - v : 0.0f;
+        x[2 * i] = t == 0 || fabsf(u) < INFINITY ? x[2 * i] - u : 0.0f;
+        x[2 * i + 1] = t == 0 || fabsf(v) < INFINITY ? x[2 * i + 1] - v : 0.0f;
       }
     }
     out[t] = __builtin_bit_cast(b8, w);

@@ -125,3 +125,25 @@ def test_sample_slices_that_weigh_nothing(tq, low, dt):
         assert bool(logprob.isfinite().all())
     cold = (x * 0.25).to(dt).repeat(n, 1).cuda()
     assert torch.equal(tq.sample(cold, u.cuda(), temperature=full(0.25)).cpu(), want)
+
+
+# ---- adapters next to infinity -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tokens", [3, 200, 2048])
+@pytest.mark.parametrize("wt", [BF, HF])
+def test_adapter_add_of_the_largest_floats(tq, tokens, wt):
+    """fp32 values above bf16's largest are finite, in x and in A x."""
+    big = torch.finfo(F32).max
+    assert big > torch.finfo(BF).max
+    r = gen(tokens)
+    x, a, b = torch.randn(tokens, 64, generator=r), torch.zeros(2, 8, 64), torch.randn(2, 40, 8, generator=r) * 2.0**-10
+    x[:, 3], x[:, 17] = big, -big * (1 - torch.rand(tokens, generator=r) * 2.0**-9)
+    a[0, 0, 3], a[0, 1, 17], a[0, 2, 5] = 1.0, -1.0, 1.0
+    a[1, 0, 3], a[1, 5, 17] = 2.0**-14, 1.5 * 2.0**-12
+    a, b = a.to(wt), b.to(wt)
+    index = torch.arange(tokens, dtype=I32) % 3 - 1
+    y = torch.randn(tokens, 40, generator=r)
+    got = tq.adapter_add(y.cuda(), x.cuda(), a.cuda(), b.cuda(), index.cuda()).double().cpu()
+    want, size = bo.adapter(y, x, a, b, index, None, None)
+    assert bool(want.isfinite().all()) and float(want.abs().max()) < big
+    assert bool(((got - want).abs() <= bo.adapter_bound(want, size, 64, 8, F32)).all())
