@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void gemm_experts_wide_kernel(t
     const int s = min(sc, nsc - 1);
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) q_ring[J][p] = *reinterpret_cast<const v4u*>(q_from[p] + 256 * s);
-    d_ring[J] = d_from[s];
+    d_ring[J] = sc < nsc ? d_from[s] : 0.0f;  // (behind the last zero: 0 times its scale would be NaN where that is not finite)
   };
   const auto put_acts = [&](int J, int to) __attribute__((always_inline)) {
 #pragma unroll

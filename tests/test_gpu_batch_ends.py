@@ -147,3 +147,25 @@ def test_adapter_add_of_the_largest_floats(tq, tokens, wt):
     want, size = bo.adapter(y, x, a, b, index, None, None)
     assert bool(want.isfinite().all()) and float(want.abs().max()) < big
     assert bool(((got - want).abs() <= bo.adapter_bound(want, size, 64, 8, F32)).all())
+
+
+# ---- experts: scales that are not finite ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cols", [256, 768, 1280, 1536, 2304])
+@pytest.mark.parametrize("tokens,k,n", [(90, 1, 2), (50, 1, 1), (9, 2, 4), (60, 2, 3)])
+def test_gemm_experts_scales_that_are_not_finite(tq, tokens, k, n, cols):
+    """A block's scale of infinity or NaN gives what the product gives."""
+    g = np.random.default_rng(cols + tokens)
+    rows = 70
+    w = torch.stack([tq.repack(torch.from_numpy(TI.pq2_matrix(g, rows, cols).reshape(-1)).cuda(), "pq2_0", rows, cols) for _ in range(n)])
+    q, d, _ = tq.quantize_q8k(torch.randn(tokens, cols, generator=gen(tokens)).cuda())
+    for t in range(0, tokens, 3):
+        d[t, (t // 3) % (cols // 256)] = (math.inf, -math.inf, math.nan)[t // 3 % 3]
+    d[0, -1] = math.inf
+    ids = torch.stack([torch.randperm(n, generator=gen(t))[:k] for t in range(tokens)]).int()
+    y = tq.gemm_experts("pq2_0", w, rows, cols, q, d, *tq.expert_lists(ids.cuda(), n)).view(tokens, k, rows)
+    for t in range(tokens):
+        for j in range(k):
+            want = tq.gemv("pq2_0", w[ids[t, j]], rows, cols, q[t], d[t])
+            assert torch.equal(y[t, j].nan_to_num(7.0, 1e30, -1e30), want.nan_to_num(7.0, 1e30, -1e30)), (t, j)
+    assert bool(y[0].isinf().any())
