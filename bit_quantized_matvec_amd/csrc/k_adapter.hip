@@ -189,7 +189,7 @@ __device__ inline Group find_group(const tq_adapter_add_args& a, const Find& f, 
     const int rest = 63 - (int)__popcll(__ballot(!in) & ((uint64_t(1) << lane) - 1));
     g.token = __builtin_amdgcn_ds_permute(4 * (in ? place - first : rest), lane);
   } else {
-    const Tile t = find_tile(f.offsets, a.adapters, tokens, SIZE, f.places, slot, lane, nullptr);
+    const Tile t = find_tile(f.offsets, a.adapters, tokens, SIZE, f.places, slot, lane);
     g.adapter = t.expert, g.count = t.count;
     g.token = lane < t.count ? f.order[t.first + lane] : 0;
   }

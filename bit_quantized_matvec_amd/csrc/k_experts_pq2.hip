@@ -51,10 +51,11 @@ __global__ __launch_bounds__(64 * kMaxRuns, 2) void gemm_experts_kernel(tq_gemm_
   const int l16 = lane & 15, qd = lane >> 4;
   const int id = blockIdx.x, rem = id % (8 * slots);
   const int rg = id / (8 * slots) * 8 + rem % 8, local = rem / 8;
+  const int pairs = (int)g.pairs, rows = (int)g.rows;
+  check_offsets(g.offsets, g.experts, pairs, g.bad_flag);
   if (rg >= gs.nrg || local >= slots) return;
   const int slot = slot0 + local;
-  const int pairs = (int)g.pairs, rows = (int)g.rows;
-  const Tile tile = find_tile(g.offsets, g.experts, pairs, kTok, places, slot, lane, g.bad_flag);
+  const Tile tile = find_tile(g.offsets, g.experts, pairs, kTok, places, slot, lane);
   if (tile.count == 0) return;  // uniform over the workgroup
   const int b0 = rg * gs.base + min(rg, gs.extra), blocks = gs.base + (rg < gs.extra ? 1 : 0);
   if (tid < kTok) {
@@ -264,9 +265,10 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void gemm_experts_wide_kernel(t
   const int l16 = lane & 15, qd = lane >> 4;
   const int at = blockIdx.x / 8, share = (slots + 7) / 8;
   const int rg = at % gs.nrg, local = blockIdx.x % 8 * share + at / gs.nrg;
-  if (local >= slots || at / gs.nrg >= share) return;
   const int pairs = (int)g.pairs, rows = (int)g.rows;
-  const Tile tile = find_tile(g.offsets, g.experts, pairs, kWideTok, places, slot0 + local, lane, g.bad_flag);
+  check_offsets(g.offsets, g.experts, pairs, g.bad_flag);
+  if (local >= slots || at / gs.nrg >= share) return;
+  const Tile tile = find_tile(g.offsets, g.experts, pairs, kWideTok, places, slot0 + local, lane);
   if (tile.count == 0) return;  // uniform over the workgroup
   const int r0 = rg * gs.base + min(rg, gs.extra), blocks = gs.base + (rg < gs.extra ? 1 : 0);
   if (tid < kWideTok) {

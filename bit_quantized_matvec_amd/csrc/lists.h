@@ -30,20 +30,25 @@ struct Tile {
   int expert, first, count;
 };
 
-__device__ inline int offset_at(const int32_t* offsets, int e, int pairs, int32_t* flag) {
-  const int o = offsets[e];
-  if (o < 0 || o > pairs) raise_flag(flag);
-  return min(max(o, 0), pairs);
+// Held in [0, pairs], whatever the list holds.
+__device__ inline int offset_at(const int32_t* offsets, int e, int pairs) { return min(max(offsets[e], 0), pairs); }
+
+// Offsets that decrease or leave [0, pairs] raise the flag.  All of them are looked at, by the launch's threads together: a
+// search for a slot passes most of them by.
+__device__ inline void check_offsets(const int32_t* offsets, int experts, int pairs, int32_t* flag) {
+  if (!flag) return;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i <= experts; i += (int64_t)gridDim.x * blockDim.x)
+    if (offsets[i] < (i > 0 ? offsets[i - 1] : 0) || offsets[i] > pairs) raise_flag(flag);
 }
 
 // The tile of `slot`, by one wave: the last expert whose first slot is at most it.
-__device__ inline Tile find_tile(const int32_t* offsets, int experts, int pairs, int size, bool places, int slot, int lane, int32_t* flag) {
+__device__ inline Tile find_tile(const int32_t* offsets, int experts, int pairs, int size, bool places, int slot, int lane) {
   int lo = 0, n = experts + 1;  // the last is none
   while (n > 1) {
     const int step = (n + 63) / 64, i = lo + lane * step;
     bool ok = false;
     if (lane * step < n) {
-      const int o = offset_at(offsets, i, pairs, flag);
+      const int o = offset_at(offsets, i, pairs);
       ok = (places ? o : o / size + i) <= slot;
     }
     const int last = max(1, (int)__popcll(__ballot(ok))) - 1;
@@ -51,7 +56,7 @@ __device__ inline Tile find_tile(const int32_t* offsets, int experts, int pairs,
     n = min(step, n - last * step);
   }
   const int e = __builtin_amdgcn_readfirstlane(lo);
-  const int begin = offset_at(offsets, e, pairs, flag), end = e < experts ? max(begin, offset_at(offsets, e + 1, pairs, flag)) : pairs;
+  const int begin = offset_at(offsets, e, pairs), end = e < experts ? max(begin, offset_at(offsets, e + 1, pairs)) : pairs;
   int first;
   if (places) {
     first = slot < begin || (slot - begin) % size ? end : slot;

@@ -169,3 +169,40 @@ def test_gemm_experts_scales_that_are_not_finite(tq, tokens, k, n, cols):
             want = tq.gemv("pq2_0", w[ids[t, j]], rows, cols, q[t], d[t])
             assert torch.equal(y[t, j].nan_to_num(7.0, 1e30, -1e30), want.nan_to_num(7.0, 1e30, -1e30)), (t, j)
     assert bool(y[0].isinf().any())
+
+
+# ---- experts: lists that decrease ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("pairs,n,offsets", [(4, 2, [0, 3, 1]), (4, 2, [3, 1, 4]), (4, 2, [0, 5, 4]), (4, 2, [-1, 2, 4]), (4, 2, [0, 2, 5]), (100, 2, [0, 90, 20]),
+                                             (100, 1, [60, 40]), (100, 1, [0, 101])])
+def test_gemm_experts_flags_lists(tq, pairs, n, offsets):
+    """Few pairs and many pairs per expert; the same call with a good list raises nothing."""
+    rows, cols = 64, 256
+    w = torch.stack([tq.repack(torch.from_numpy(TI.pq2_matrix(np.random.default_rng(i), rows, cols).reshape(-1)).cuda(), "pq2_0", rows, cols) for i in range(n)])
+    q, d, _ = tq.quantize_q8k(torch.randn(pairs, cols, generator=gen(pairs)).cuda())
+    ints = lambda v: torch.tensor(v, dtype=I32, device="cuda")  # noqa: E731
+    order = torch.arange(pairs, dtype=I32, device="cuda")
+    guard = torch.full((pairs + 2, rows), 7.0, device="cuda")
+    for lists, want in ((offsets, 1), (sorted(min(max(o, 0), pairs) for o in offsets), 0), ([0] * (n + 1), 0), ([pairs] * (n + 1), 0)):
+        flag = ints([0])
+        tq.gemm_experts("pq2_0", w, rows, cols, q, d, order, ints(lists), out=guard[1:-1], bad_flag=flag)
+        assert flag.item() == want, lists
+    assert bool((guard[0] == 7).all()) and bool((guard[-1] == 7).all())
+
+
+@pytest.mark.parametrize("pairs", [5, 4000])
+@pytest.mark.parametrize("at", [1, 77, 350, 699, 700])
+def test_gemm_experts_flags_a_hidden_decrease(tq, pairs, at):
+    """One offset of 701 is off, wherever the search for a slot looks."""
+    n, rows, cols = 700, 64, 256
+    w = torch.zeros(n, tq.repacked_bytes("pq2_0", rows, cols), dtype=torch.uint8, device="cuda")
+    q, d, _ = tq.quantize_q8k(torch.randn(pairs, cols, generator=gen(at)).cuda())
+    good = bo.lists(torch.randint(0, n, (pairs,), generator=gen(pairs + at), dtype=I32), n)
+    for value, want in ((None, 0), (-1, 1), (pairs + 1, 1), (0, 1)):
+        order, offsets = good[0].cuda(), good[1].clone()
+        if value is not None:
+            offsets[at] = value
+            offsets[at - 1] = max(1, int(offsets[at - 1]))  # (so that 0 is a decrease)
+        flag = torch.zeros(1, dtype=I32, device="cuda")
+        tq.gemm_experts("pq2_0", w, rows, cols, q, d, order, offsets.cuda(), bad_flag=flag)
+        assert flag.item() == want, value
