@@ -46,6 +46,7 @@ constexpr int kJoin = 2048;
 constexpr int kExpandWaves = 4;
 constexpr int kFeat = 64;        // features per wave of expand
 constexpr int kMaxSplits = 8;
+constexpr int kMaxGroups = 768;  // workgroups that splits of the columns may make (three per compute unit)
 
 // 8 values as TERMS (2 or 3) bf16 vectors.  The first term is held at bf16's largest, so that fp32 values above it, which would be
 // rounded to infinity, leave the rest to the second; so do infinities and NaN, and nothing is left behind a term that is not finite.
@@ -126,11 +127,21 @@ Plan plan(int64_t tokens, int adapters, int rank, int64_t cols) {
   const int64_t tiles = std::min<int64_t>(tokens, tokens / tok + std::min<int64_t>(adapters, tokens));
   const int64_t unit = 32 * shrink_waves(shrink_tiles(rank));
   const int64_t units = (cols + unit - 1) / unit;
-  const int64_t want = std::min<int64_t>(std::min<int64_t>(units, kMaxSplits), std::max<int64_t>(1, 768 / std::max<int64_t>(1, tiles)));
+  const int64_t want = std::min<int64_t>(std::min<int64_t>(units, kMaxSplits), std::max<int64_t>(1, kMaxGroups / std::max<int64_t>(1, tiles)));
   const int64_t per = (units + want - 1) / want;
   p.chunk = (int)(per * unit);
   p.splits = (int)((units + per - 1) / per);
   return p;
+}
+
+// Rows of partial sums that a call of these sizes, or of fewer tokens, has at most.  There are fewer splits the more tiles, so that
+// splits * tokens goes up and down; but it is tokens where there is one split, and otherwise below kMaxGroups / tiles * tokens with
+// tokens < tiles * shrink_tok.  So a workspace serves every call of fewer tokens, adapters or columns, or of a lower rank.
+int64_t partial_rows(int64_t tokens, int64_t cols) {
+  constexpr int64_t kMostTok = std::max(shrink_tok(8, true), shrink_tok(256, false));
+  constexpr int64_t kLeastUnit = 32 * std::min(shrink_waves(1), shrink_waves(16));
+  const int64_t splits = std::min<int64_t>(kMaxSplits, (cols + kLeastUnit - 1) / kLeastUnit);
+  return std::max(tokens, std::min(splits * tokens, kMaxGroups * kMostTok));
 }
 
 // Places in the workspace.
@@ -144,7 +155,7 @@ Space space(int64_t tokens, int adapters, int rank, int64_t cols) {
   w.order = 0;
   w.offsets = p.direct ? 0 : up(tokens * 4);
   w.h = p.direct ? 0 : w.offsets + up((adapters + 1) * int64_t(4));
-  w.terms = w.h + up((int64_t)p.splits * tokens * rank * 4);
+  w.terms = w.h + up(partial_rows(tokens, cols) * rank * 4);
   w.bytes = w.terms + (p.join ? up(tokens * rank * 6) : 0);
   return w;
 }

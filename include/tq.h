@@ -470,7 +470,8 @@ typedef struct {
   int32_t adapters, rank, x_type, w_type, y_type;
 } tq_adapter_add_args;
 
-/* Bytes for these sizes, 0 for sizes that tq_adapter_add refuses. */
+/* Bytes for these sizes, 0 for sizes that tq_adapter_add refuses.  They serve
+ * every call of which no size is larger. */
 int64_t tq_adapter_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank, int64_t cols);
 int tq_adapter_add(const tq_adapter_add_args *args, void *stream);
 

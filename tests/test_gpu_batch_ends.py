@@ -206,3 +206,25 @@ def test_gemm_experts_flags_a_hidden_decrease(tq, pairs, at):
         flag = torch.zeros(1, dtype=I32, device="cuda")
         tq.gemm_experts("pq2_0", w, rows, cols, q, d, order, offsets.cuda(), bad_flag=flag)
         assert flag.item() == want, value
+
+
+# ---- workspaces of a larger call's size ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("most,n,rank,cols", [(7000, 5, 64, 5120), (1500, 24, 32, 5120), (1696, 4, 64, 5120), (64, 9, 256, 2048)])
+def test_adapter_workspace_serves_smaller_batches(tq, most, n, rank, cols):
+    r = gen(most)
+    need = tq.adapter_workspace_bytes(most, n, rank, cols)
+    guard = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    ws = guard[:need]
+    a, b = torch.randn(n, rank, cols, generator=r).to(BF).cuda(), torch.randn(n, 24, rank, generator=r).to(BF).cuda()
+    x, y = torch.randn(most, cols, generator=r).to(BF).cuda(), torch.randn(most, 24, generator=r).cuda()
+    index = torch.randint(-1, n, (most,), generator=r, dtype=I32).cuda()
+    for tokens in sorted({1, 17, 64, 65, 1375, 1695, 2047, 2048, 6000, most}):
+        if tokens > most:
+            continue
+        for adapters in (n, 1):
+            i = index[:tokens].clamp(max=adapters - 1)
+            args = (y[:tokens], x[:tokens], a[:adapters], b[:adapters], i)
+            got = tq.adapter_add(*args, out=torch.empty_like(y[:tokens]), ws=ws)
+            assert torch.equal(got, tq.adapter_add(*args, out=torch.empty_like(y[:tokens]))), tokens
+    assert bool((guard[need:] == 171).all())
