@@ -138,7 +138,7 @@ def adapter_workspace_bytes(tokens: int, adapters: int, rank: int, cols: int) ->
 
 
 def adapter_workspace(tokens: int, adapters: int, rank: int, cols: int, device="cuda") -> torch.Tensor:
-    """Scratch for ``adapter_add`` calls of these sizes (needs no clearing)."""
+    """Scratch for ``adapter_add`` calls of these sizes and of smaller ones (needs no clearing)."""
     return torch.empty(max(16, adapter_workspace_bytes(tokens, adapters, rank, cols)), dtype=torch.uint8, device=device)
 
 
@@ -187,7 +187,7 @@ def sample_workspace_bytes(rows: int, vocab: int) -> int:
 
 
 def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
-    """Scratch for ``sample`` calls of these sizes (needs no clearing)."""
+    """Scratch for ``sample`` calls of these sizes and of smaller ones (needs no clearing)."""
     return torch.empty(max(16, sample_workspace_bytes(rows, vocab)), dtype=torch.uint8, device=device)
 
 

@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr int kPer = 16;     // logits of a thread of the slices' kernels
+constexpr int kLeastThreads = 256;  // of a slice
 constexpr int kPickThreads = 1024;
 constexpr int kPlanShares = 4;
 constexpr int kShare = 1024;  // places of a slice in its row's list
@@ -150,18 +151,20 @@ Layout layout(int64_t rows, int64_t vocab) {
   rows = std::min(rows, kRows);
   // Slices of 4096 logits, since one workgroup draws in one: 16384 take its compute unit 9 us instead of 2.  More in vocabularies
   // of more than 64 slices, whose sums one wave adds.
-  l.threads = 256;
+  l.threads = kLeastThreads;
   while (vocab + 7 > (int64_t)l.threads * kPer * kMaxSlices) l.threads *= 2;
   l.per = l.threads * kPer;
   l.slices = (int)((vocab + 7 + l.per - 1) / l.per);  // (the first logit may be place 7)
+  // Larger slices are fewer: places for as many as a smaller vocabulary has at most, so that a workspace serves it too.
+  const int64_t most = std::min<int64_t>(kMaxSlices, (vocab + 7 + kLeastThreads * kPer - 1) / (kLeastThreads * kPer));
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   l.rows = 0;
   l.parts = l.rows + up(rows * (int64_t)sizeof(Row));
-  l.mass = l.parts + up(rows * l.slices * (int64_t)sizeof(Slice));
-  l.count = l.mass + up(rows * l.slices * kBins * 8);
-  l.shares = l.count + up(rows * l.slices * kBins * 4);
-  l.list = l.shares + up(rows * l.slices * 4);
-  l.bytes = l.list + up(rows * l.slices * kShare * 4);
+  l.mass = l.parts + up(rows * most * (int64_t)sizeof(Slice));
+  l.count = l.mass + up(rows * most * kBins * 8);
+  l.shares = l.count + up(rows * most * kBins * 4);
+  l.list = l.shares + up(rows * most * 4);
+  l.bytes = l.list + up(rows * most * kShare * 4);
   return l;
 }
 struct Space {

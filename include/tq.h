@@ -509,7 +509,8 @@ typedef struct {
   int32_t in_type;
 } tq_sample_args;
 
-/* Bytes for these sizes, 0 for sizes that tq_sample refuses. */
+/* Bytes for these sizes, 0 for sizes that tq_sample refuses.  They serve every
+ * call of which neither size is larger. */
 int64_t tq_sample_workspace_bytes(int64_t rows, int64_t vocab);
 int tq_sample(const tq_sample_args *args, void *stream);
 

@@ -35,3 +35,12 @@ def test_an_adapter_workspace_serves_smaller_calls(tq):
         for small in n:
             if all(s <= b for s, b in zip(small, large)):
                 assert size(*small) <= size(*large), (small, large)
+
+
+def test_sample_workspaces_grow(tq):
+    size = tq.sample_workspace_bytes
+    borders = [b + i for b in (262_137, 262_144, 266_233, 266_240, 532_473, 532_480, 2**20 - 8) for i in range(-9, 9)]
+    for rows in (1, 3, 1024, 5000):
+        grows([size(rows, v) for v in sorted({*range(1, 2**20 + 1, 1013), *borders, 2**20})])
+    for vocab in (1, 4089, 4090, 131_072, 262_144, 270_000, 540_000, 2**20):
+        grows([size(rows, vocab) for rows in range(1, 3000)])

@@ -228,3 +228,16 @@ def test_adapter_workspace_serves_smaller_batches(tq, most, n, rank, cols):
             got = tq.adapter_add(*args, out=torch.empty_like(y[:tokens]), ws=ws)
             assert torch.equal(got, tq.adapter_add(*args, out=torch.empty_like(y[:tokens]))), tokens
     assert bool((guard[need:] == 171).all())
+
+
+@pytest.mark.parametrize("most", [270_000, 540_000])
+def test_sample_workspace_serves_smaller_vocabularies(tq, most):
+    r = gen(most)
+    need = tq.sample_workspace_bytes(3, most)
+    guard = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    x, u, p = torch.randn(3, most, generator=r).cuda(), torch.rand(3, generator=r).cuda(), torch.full((3,), 0.9, device="cuda")
+    for vocab in (1, 5000, 260_000, 266_233, 266_234, 530_000, most):
+        if vocab <= most:
+            got = tq.sample(x[:, :vocab], u, top_p=p, out=torch.empty(3, dtype=I32, device="cuda"), ws=guard[:need])
+            assert torch.equal(got, tq.sample(x[:, :vocab], u, top_p=p)), vocab
+    assert bool((guard[need:] == 171).all())
