@@ -14,12 +14,15 @@
 // sorted by adapter first (expert_lists).
 //
 // Memory bounds both: a token's x, y and out and an adapter's A and B are read
-// or written once (A once per 16 and B once per 64 of its tokens, from the L2).
+// or written once (A once per 16 of its tokens, or per 32 of many at ranks up to
+// 64, and B once per 16, or per 64 of many, from the L2).
 // 4099 tokens of 5 adapters of rank 64 (5120 columns in bf16, 7168 features in
 // fp32) take 101 us: the lists 5, shrink 27, join 5, expand 69 for 297 MB, 4.3
 // TB/s of a mix of reads and writes in 256-byte rows.  64 tokens of 24 adapters
 // 21 us: shrink 7.6, expand 13, mostly the latency of index, weights, sums and
-// y one after the other; one token 9.2.
+// y one after the other; one token 9.0.  Ranks above 64 take shrink's 16 tiles of
+// rank rows and read B as it is needed: 4099 tokens beside the same matrix, us at
+// ranks 64, 72, 128 and 256 used whole: 104, 166, 222, 376.
 //
 // Precision: fp32 factors are split into three bf16 terms (24 bits), fp16
 // weights beside them into two (11 bits, exactly); term products below 2^-24 of

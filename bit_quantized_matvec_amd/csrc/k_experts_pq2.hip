@@ -9,9 +9,9 @@
 // (k_gemm_pq2.hip), with each lane reading its pair's activations at an address
 // of its own.
 //
-// Few pairs: bound by the codes.  One token's 8 experts of 2048 x 5120 take 8.8
+// Few pairs: bound by the codes.  One token's 8 experts of 2048 x 5120 take 8.6
 // us (22 MB, 4.3 at a large copy's rate, one launch 3.6), 48 tokens x 8 of 64
-// experts of 5120 x 1024 30 us (89 MB of codes, 19 at that rate).  Many pairs:
+// experts of 5120 x 1024 29 us (89 MB of codes, 19 at that rate).  Many pairs:
 // bound by the vector units, see below.
 //
 // Slots and tiles: lists.h.  Workgroups of slots without a tile end at once;
@@ -245,7 +245,7 @@ hipError_t launch_t(const tq_gemm_experts_args& g, int64_t active, int64_t work,
 //
 // Bound by the vector units: per 16 rows, 32 pairs and superchunk 28 instructions expand the codes, 40 make the fp64 sums (5 to 6
 // cycles each with two waves per SIMD), and 8 matrix instructions of 16 cycles run beside them.  2048 tokens x 4 of 32 experts of
-// 2048 x 5120: 190 us, vector units 56 % and matrix units 20 % busy.  (Eight waves of 2 blocks, four per SIMD: 216, more reads of
+// 2048 x 5120: 191 to 207 us, vector units 56 % and matrix units 20 % busy.  (Eight waves of 2 blocks, four per SIMD: 216, more reads of
 // the staged operands and 4 spilled registers; eight waves of 4 blocks, one workgroup per compute unit: 206.)
 constexpr int kWideWaves = 4;
 constexpr int kPieces = 8 / kWideWaves;  // 16-byte pieces of a superchunk that a thread stages

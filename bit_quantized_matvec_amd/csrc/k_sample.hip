@@ -30,7 +30,8 @@
 // logit, half of them fp64, in the first, 10 in the list.
 //
 // Where a slice has too many of them (a flat row), pick_kernel searches the
-// whole row instead (search_row: a radix descent over the keys).
+// whole row instead (search_row: a radix descent over the keys).  One such row
+// of 131072 takes 171 us with top-k and 300 with top-p, 64 of them 241 and 327.
 //
 // (Two launches, whose last workgroups of a row did the second and the fourth
 // kernel's work, cost one row as much and 256 rows twice: counting arrivals

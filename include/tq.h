@@ -397,7 +397,8 @@ typedef enum { TQ_SOFTMAX = 0, TQ_SIGMOID = 1 } tq_score;
  * without sums of two the logits are compared, whose order is that of c.  An expert whose logit
  * or c is -inf or NaN is absent: it counts as s = 0, c = -inf and is never
  * chosen; where fewer than k are left the places behind them get id -1 and
- * weight 0.  Of a softmax with logits of +inf these share equally.
+ * weight 0.  Of a softmax with logits of +inf these share equally.  Chosen ones
+ * whose s are all 0 in fp64 (sigmoids of logits below -709) get weight 0 with renorm too.
  * Scores, sums and comparisons are fp64, weights are rounded once.
  * experts 1 to 1024; k 1 to 32, at most the experts that stay; groups divides
  * experts, up to 64. */
@@ -417,8 +418,10 @@ int tq_route(const tq_route_args *args, void *stream);
  * order int32 [pairs]: pair numbers by expert, those of one expert in their own
  * order; offsets int32 [experts + 1]: expert e has order[offsets[e]] ..
  * order[offsets[e + 1] - 1].  Pairs whose id is not in [0, experts) come last,
- * from offsets[experts] on.  experts 1 to 65536, pairs up to 2^25.  Adapters
- * and their tokens are sorted the same way. */
+ * from offsets[experts] on.  experts 1 to 65536, pairs up to 2^25; each expert's
+ * workgroup reads all ids, so that time grows with experts * pairs (some 4e12 a
+ * second: 65536 experts of 2^18 pairs take 4 ms).  Adapters and their tokens are
+ * sorted the same way. */
 int tq_expert_lists(const int32_t *ids, int64_t pairs, int32_t experts, int32_t *order, int32_t *offsets, void *stream);
 
 /* Ternary products whose matrix is chosen per pair: y[p] = W_e x[p / (pairs /
@@ -485,15 +488,17 @@ int tq_adapter_add(const tq_adapter_add_args *args, void *stream);
  *   token = the first index i that stays and whose running sum of e over the
  *     indices that stay exceeds u times their whole sum
  * temperature 0 (or less, or NaN): the index of the largest logit, the lowest
- * of equal ones.  logprob = log(e_token / sum of all e_i), before any filter
+ * of equal ones; +inf: all finite logits weigh the same.  logprob = log(e_token / sum of all e_i), before any filter
  * (temperature counts as 1 for greedy rows).  NaN parameters other than the
  * temperature switch their filter off (u: 0); u outside [0, 1) takes the first
  * or the last token that stays; top_p <= 0 keeps the first; min_p > 1 the
  * largest logits.  NULL parameters: temperature 1, filters off.
  * Logits of -inf and NaN are never drawn; a row without others gives token -1
- * and logprob -inf.  Logits of +inf share equally.  e is fp64; sums are good
- * to some 2^-43 of the largest e and do not depend on timing; tokens below
- * 2^-44 of the largest weigh nothing.
+ * and logprob -inf.  Logits of +inf share equally.  e is fp64; in sums each e
+ * counts to within 2^-44 of the largest, sums of n tokens to n times that, and
+ * tokens below 2^-44 of the largest weigh nothing.  Results do not depend on
+ * timing.  The roundings are those of slices that begin on 16 bytes: a row at
+ * another alignment may differ by as much.
  * workspace: tq_sample_workspace_bytes of scratch, needs no clearing; not
  * nullable.  vocab 1 to 2^20. */
 typedef struct {

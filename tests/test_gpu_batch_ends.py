@@ -241,3 +241,21 @@ def test_sample_workspace_serves_smaller_vocabularies(tq, most):
             got = tq.sample(x[:, :vocab], u, top_p=p, out=torch.empty(3, dtype=I32, device="cuda"), ws=guard[:need])
             assert torch.equal(got, tq.sample(x[:, :vocab], u, top_p=p)), vocab
     assert bool((guard[need:] == 171).all())
+
+
+# ---- routing: the type's lowest values -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+def test_route_of_the_lowest_logits(tq, dt):
+    """Logits of a mask that is the type's lowest value are logits: the lowest experts share a softmax equally.  Sigmoids of them are
+    0 in fp64 (fp32, bf16), and so are the weights."""
+    low = torch.finfo(dt).min
+    x = torch.full((2, 70), low, dtype=dt)
+    x[1, 40] = 3.0
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, torch.zeros(70)):
+            for renorm in (False, True):
+                want = bo.route(x, 4, score, bias, 1, 1, 1, renorm, 1.0)
+                w, i = tq.route(x.cuda(), 4, score=score, bias=None if bias is None else bias.cuda(), renorm=renorm)
+                assert torch.equal(i.cpu(), want[1]) and i.cpu().tolist() == [[0, 1, 2, 3], [40, 0, 1, 2]]
+                assert bool(((w.cpu().double() - want[0]).abs() <= want[0] * 2.0**-24 * 1.001).all()) and bool(w.isfinite().all())
